@@ -20,6 +20,12 @@ points have the names of the C ABI (include/gemm_preshuffle.h):
     workspace(dtype, M, N, K, opts)                  -> a zeroed device workspace of that size
     gemm_ex_noalloc(dtype, ...)                      -> gemm_ex_ws on the library's own static
                                                         device workspace (allocates nothing)
+    gemm_gated_preshuffle(w, dtype)                  -> gate / up weights [2F, H] laid out for gemm_gated
+    gemm_gated(dtype, x, w_shuf, act, save)          -> h = act(x Wg^T) * (x Wu^T) (and gate, up to keep)
+    gemm_gated_backward(dtype, dh, gate, up, x, w)   -> dx, dw
+    gemm_backward(dtype, dc, a, b)                   -> da, db of C = A B^T
+    gated_workspace, gated_backward_workspace, backward_workspace
+                                                     -> device workspaces of these
 
 Tensors: A is [M, K] (INT8 / FP8 as any 1-byte dtype, BF16 / FP16 as
 bfloat16 / float16 or a 2-byte integer view, MXFP4 as uint8 [M, K/2]; W4A8:
@@ -37,7 +43,9 @@ __all__ = [
     "GemmError", "GemmLibraryMissing", "GemmOpts", "lib_path", "load_library",
     "gemm_preshuffle_b", "gemm_a8w8", "gemm_bf16", "gemm_mxfp4", "gemm_f16", "gemm_w4a8", "gemm_ex",
     "gemm_plan", "ACTS", "gemm_ex_ws", "gemm_ex_noalloc", "gemm_workspace_size", "gemm_plan_ws", "workspace",
-    "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE", "KERNEL_SPLITK",
+    "gemm_gated_preshuffle", "gemm_gated", "gemm_gated_workspace_size", "gated_workspace", "gemm_gated_backward",
+    "gemm_gated_backward_workspace_size", "gated_backward_workspace", "gemm_backward", "gemm_backward_workspace_size",
+    "backward_workspace", "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE", "KERNEL_SPLITK",
     "KERNEL_WIDE",
 ]
 
@@ -53,6 +61,7 @@ _OUT = {GP_I8: GP_I32, GP_FP8_E4M3: GP_BF16, GP_BF16: GP_BF16, GP_FP4_E2M1: GP_B
         GP_I4: GP_BF16}
 # gp_status values of a HIP runtime or launch error, and of a missing / too small workspace
 GP_EHIP = 5
+GP_EDTYPE = 3
 GP_EWORKSPACE = 6
 # gp_act values of the C ABI
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
@@ -130,6 +139,14 @@ def load_library():
     lib.gemm_ex_ws.argtypes = [ci, ci, vp, vp, vp, vp, vp, ci, vp, i64, i64, i64, ctypes.POINTER(GemmOpts), vp,
                                ctypes.c_size_t, vp]
     lib.gemm_ex_noalloc.argtypes = [ci, ci, vp, vp, vp, vp, vp, ci, vp, i64, i64, i64, ctypes.POINTER(GemmOpts), vp]
+    sz, psz = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+    lib.gemm_gated_preshuffle.argtypes = [vp, vp, i64, i64, ci, vp]
+    lib.gemm_gated.argtypes = [ci, vp, vp, ci, vp, vp, vp, i64, i64, i64, vp, sz, vp]
+    lib.gemm_gated_workspace_size.argtypes = [ci, i64, i64, i64, psz]
+    lib.gemm_gated_backward.argtypes = [ci, vp, vp, vp, vp, vp, ci, vp, vp, i64, i64, i64, vp, sz, vp]
+    lib.gemm_gated_backward_workspace_size.argtypes = [ci, i64, i64, i64, ci, ci, psz]
+    lib.gemm_backward.argtypes = [ci, vp, vp, vp, vp, vp, i64, i64, i64, vp, sz, vp]
+    lib.gemm_backward_workspace_size.argtypes = [ci, i64, i64, i64, ci, ci, psz]
     lib.gemm_status_string.argtypes = [ci]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_last_hip_error.argtypes = []
@@ -137,7 +154,9 @@ def load_library():
     lib.gemm_last_hip_call.argtypes = []
     lib.gemm_last_hip_call.restype = ctypes.c_char_p
     for f in ("gemm_preshuffle_b", "gemm_a8w8", "gemm_bf16", "gemm_mxfp4", "gemm_f16", "gemm_w4a8", "gemm_ex",
-              "gemm_plan", "gemm_plan_ws", "gemm_workspace_size", "gemm_ex_ws", "gemm_ex_noalloc"):
+              "gemm_plan", "gemm_plan_ws", "gemm_workspace_size", "gemm_ex_ws", "gemm_ex_noalloc", "gemm_gated_preshuffle", "gemm_gated",
+              "gemm_gated_workspace_size", "gemm_gated_backward", "gemm_gated_backward_workspace_size",
+              "gemm_backward", "gemm_backward_workspace_size"):
         getattr(lib, f).restype = ci
     _lib = lib
     return lib
@@ -386,3 +405,200 @@ def gemm_ex_noalloc(dtype, a, b_shuf, c, scale_a=None, scale_b=None, bias=None, 
                                           _ptr(bias), a_, _ptr(c), M, N, K, _opts(opts), _stream(stream)),
            "gemm_ex_noalloc")
     return c
+
+
+# ---- gated feed-forward product, gradients ----
+
+_HALF = {GP_BF16: "bfloat16", GP_F16: "float16"}
+
+
+def _half(dtype):
+    """(gp_dtype, torch dtype) of a BF16 / FP16 operator."""
+    import torch
+
+    dt = _dt(dtype)
+    if dt not in _HALF:
+        raise GemmError(GP_EDTYPE, "BF16 or FP16 operator")
+    return dt, getattr(torch, _HALF[dt])
+
+
+def _want(where, t, shape, dtype, device=None):
+    """A given tensor is a contiguous device tensor of this shape and type."""
+    if (not t.is_cuda or tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()
+            or (device is not None and t.device != device)):
+        raise ValueError(f"{where}: expected a contiguous {dtype} tensor {tuple(shape)}"
+                         f"{'' if device is None else f' on {device}'}, got {t.dtype} {tuple(t.shape)} "
+                         f"on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _act(act) -> int:
+    return ACTS[act] if isinstance(act, str) else int(act)
+
+
+def _on(stream, device):
+    """Context in which torch allocates for the stream that a call runs on:
+    memory from torch's allocator belongs to the stream it was asked for on,
+    so a buffer that only the call holds must come from the call's stream."""
+    import contextlib
+
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)) if stream else \
+            torch.cuda.stream(torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
+def _size(fn, *args) -> int:
+    n = ctypes.c_size_t()
+    _check(getattr(load_library(), fn)(*args, ctypes.byref(n)), fn)
+    return int(n.value)
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def gemm_gated_preshuffle(w, dtype, out=None, stream=None):
+    """w [2F, H] (F gate rows, then F up rows) -> layout of gemm_gated (uint8, flat)."""
+    import torch
+
+    dt, t = _half(dtype)
+    F2, H = w.shape
+    if F2 % 2:
+        raise ValueError("gemm_gated_preshuffle: w holds F gate rows and F up rows")
+    _want("gemm_gated_preshuffle: w", w, (F2, H), t)
+    if out is None:
+        out = torch.empty(2 * F2 * H, dtype=torch.uint8, device=w.device)
+    _want("gemm_gated_preshuffle: out", out, (2 * F2 * H,), torch.uint8, w.device)
+    _check(load_library().gemm_gated_preshuffle(_ptr(w), _ptr(out), F2 // 2, H, dt, _stream(stream)),
+           "gemm_gated_preshuffle")
+    return out
+
+
+def gemm_gated_workspace_size(dtype, M: int, F: int, H: int) -> int:
+    """Host-only: workspace bytes of gemm_gated for these sizes (0: none)."""
+    return _size("gemm_gated_workspace_size", _dt(dtype), M, F, H)
+
+
+def gated_workspace(dtype, M: int, F: int, H: int, device="cuda"):
+    """A zero-filled device workspace for gemm_gated (None when none is needed). Zero once here;
+    every call leaves its counters zero again. Calls that may overlap need one each."""
+    import torch
+
+    n = gemm_gated_workspace_size(dtype, M, F, H)
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+
+def gemm_gated(dtype, x, w_shuf, act="silu", save=False, h=None, gate=None, up=None, workspace=None, stream=None):
+    """h = act(x Wg^T) * (x Wu^T), x [M, H], w_shuf from gemm_gated_preshuffle.
+    Returns h, or (h, gate, up) with save=True. Without a workspace one is made
+    for the call where the plan needs it."""
+    import torch
+
+    dt, t = _half(dtype)
+    M, H = x.shape
+    F = _nbytes(w_shuf) // (4 * H) if H else 0
+    _want("gemm_gated: x", x, (M, H), t)
+    _want("gemm_gated: w_shuf", w_shuf, (4 * F * H,), torch.uint8, x.device)
+    with _on(stream, x.device):
+        h = torch.empty(M, F, dtype=t, device=x.device) if h is None else h
+        if save:
+            gate = torch.empty_like(h) if gate is None else gate
+            up = torch.empty_like(h) if up is None else up
+        elif gate is not None or up is not None:
+            raise ValueError("gemm_gated: gate and up are written with save=True")
+        for name, v in (("h", h), ("gate", gate), ("up", up)):
+            if v is not None:
+                _want(f"gemm_gated: {name}", v, (M, F), t, x.device)
+        if workspace is None:
+            workspace = gated_workspace(dt, M, F, H, x.device)
+        _check(load_library().gemm_gated(dt, _ptr(x), _ptr(w_shuf), _act(act), _ptr(h), _ptr(gate), _ptr(up), M, F, H,
+                                         _ptr(workspace), _nbytes(workspace), _stream(stream)), "gemm_gated")
+    return (h, gate, up) if save else h
+
+
+def gemm_gated_backward_workspace_size(dtype, M: int, F: int, H: int, want_dx=True, want_dw=True) -> int:
+    """Host-only: workspace bytes of gemm_gated_backward."""
+    return _size("gemm_gated_backward_workspace_size", _dt(dtype), M, F, H, int(want_dx), int(want_dw))
+
+
+def gated_backward_workspace(dtype, M: int, F: int, H: int, want_dx=True, want_dw=True, device="cuda"):
+    """A device workspace for gemm_gated_backward (its contents need not be set)."""
+    import torch
+
+    return torch.empty(gemm_gated_backward_workspace_size(dtype, M, F, H, want_dx, want_dw), dtype=torch.uint8,
+                       device=device)
+
+
+def gemm_gated_backward(dtype, dh, gate, up, x, w, act="silu", want_dx=True, want_dw=True, dx=None, dw=None,
+                        workspace=None, stream=None):
+    """(dx [M, H], dw [2F, H]) of gemm_gated from dh and the kept gate and up
+    ([M, F]); w [2F, H] row-major. An output that is not wanted is None, and the
+    operand that it alone needs (w for dx, x for dw) may be None."""
+    import torch
+
+    dt, t = _half(dtype)
+    M, F = dh.shape
+    dev = dh.device
+    if not (want_dx or want_dw):
+        raise ValueError("gemm_gated_backward: no output wanted")
+    if (want_dx and w is None) or (want_dw and x is None):
+        raise ValueError("gemm_gated_backward: dx needs w, dw needs x")
+    H = w.shape[1] if w is not None else x.shape[1]
+    for name, v, shape in (("dh", dh, (M, F)), ("gate", gate, (M, F)), ("up", up, (M, F)), ("x", x, (M, H)),
+                           ("w", w, (2 * F, H)), ("dx", dx, (M, H)), ("dw", dw, (2 * F, H))):
+        if v is not None:
+            _want(f"gemm_gated_backward: {name}", v, shape, t, dev)
+    with _on(stream, dev):
+        dx = (torch.empty(M, H, dtype=t, device=dev) if dx is None else dx) if want_dx else None
+        dw = (torch.empty(2 * F, H, dtype=t, device=dev) if dw is None else dw) if want_dw else None
+        if workspace is None:
+            workspace = gated_backward_workspace(dt, M, F, H, want_dx, want_dw, dev)
+        _check(load_library().gemm_gated_backward(dt, _ptr(dh), _ptr(gate), _ptr(up), _ptr(x), _ptr(w), _act(act),
+                                                  _ptr(dx), _ptr(dw), M, F, H, _ptr(workspace), _nbytes(workspace),
+                                                  _stream(stream)), "gemm_gated_backward")
+    return dx, dw
+
+
+def gemm_backward_workspace_size(dtype, M: int, N: int, K: int, want_da=True, want_db=True) -> int:
+    """Host-only: workspace bytes of gemm_backward."""
+    return _size("gemm_backward_workspace_size", _dt(dtype), M, N, K, int(want_da), int(want_db))
+
+
+def backward_workspace(dtype, M: int, N: int, K: int, want_da=True, want_db=True, device="cuda"):
+    """A device workspace for gemm_backward (its contents need not be set)."""
+    import torch
+
+    return torch.empty(gemm_backward_workspace_size(dtype, M, N, K, want_da, want_db), dtype=torch.uint8,
+                       device=device)
+
+
+def gemm_backward(dtype, dc, a, b, want_da=True, want_db=True, da=None, db=None, workspace=None, stream=None):
+    """(da [M, K], db [N, K]) of C = A B^T from dc [M, N]; a [M, K] and b [N, K]
+    row-major. An output that is not wanted is None, and the operand that it
+    alone needs (b for da, a for db) may be None."""
+    import torch
+
+    dt, t = _half(dtype)
+    M, N = dc.shape
+    dev = dc.device
+    if not (want_da or want_db):
+        raise ValueError("gemm_backward: no output wanted")
+    if (want_da and b is None) or (want_db and a is None):
+        raise ValueError("gemm_backward: da needs b, db needs a")
+    K = b.shape[1] if b is not None else a.shape[1]
+    for name, v, shape in (("dc", dc, (M, N)), ("a", a, (M, K)), ("b", b, (N, K)), ("da", da, (M, K)),
+                           ("db", db, (N, K))):
+        if v is not None:
+            _want(f"gemm_backward: {name}", v, shape, t, dev)
+    with _on(stream, dev):
+        da = (torch.empty(M, K, dtype=t, device=dev) if da is None else da) if want_da else None
+        db = (torch.empty(N, K, dtype=t, device=dev) if db is None else db) if want_db else None
+        if workspace is None:
+            workspace = backward_workspace(dt, M, N, K, want_da, want_db, dev)
+        _check(load_library().gemm_backward(dt, _ptr(dc), _ptr(a), _ptr(b), _ptr(da), _ptr(db), M, N, K,
+                                            _ptr(workspace), _nbytes(workspace), _stream(stream)), "gemm_backward")
+    return da, db

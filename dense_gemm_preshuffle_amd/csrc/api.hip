@@ -10,17 +10,12 @@
 #include <mutex>
 
 #include "../../include/gemm_preshuffle.h"
+#include "host.hpp"
 #include "launch.hpp"
 #include "variants.hpp"
 
 namespace gp {
 namespace {
-
-constexpr int64_t kMaxBytes = (int64_t)1 << 31;  // 32-bit buffer offsets
-
-// rows * row_bytes < kMaxBytes, decided without forming the product (rows and
-// row_bytes are positive; a product of two sizes near 2^62 would overflow)
-bool fits(int64_t rows, int64_t row_bytes) { return row_bytes < kMaxBytes && rows <= (kMaxBytes - 1) / row_bytes; }
 
 // Bits per element of B (and of A, except W4A8 whose A is int8).
 int elem_bits(int dt) {
@@ -102,28 +97,6 @@ bool split_compiled(int dt, int nb, int waves, int kch, int mb) {
   return false;
 }
 
-struct Plan {
-  int kernel = 0;
-  int ms = 16;                  // MFMA block (16 or 32)
-  int pipe = 0;                 // 0 VGPR-staged A, 2 .. 6 LDS DMA stages
-  int tm = 0, tn = 0, tkb = 0;  // tile and wide kernels (tkb in bytes)
-  int kg = 1;                   // tile kernel: K groups of 4 waves
-  int epi = EPI_DIRECT;
-  int xcd = 1;
-  int nb = 0, waves = 4, kch = 0, mb = 1;  // split-K kernel (mb: 16-row blocks per workgroup)
-  int ks = 1;                   // tile kernel: K split across workgroups
-  int sched = 1;                // tile kernel: 1 pinned hot-loop schedule, 2 the compiler's
-  int64_t Kb = 0;
-};
-
-// Workspace of a K split across workgroups: a fixed area of arrival counters
-// (4 bytes per tile, for up to kMaxSplitTiles tiles), then ks partial tiles of
-// TM x TN 4-byte sums per tile. The counter area is the same for every
-// shape, so a workspace whose counters are zero (as every call leaves them)
-// can serve calls of any shape: a later call's counters never fall where an
-// earlier call left partial sums.
-constexpr int64_t kMaxSplitTiles = 16384;
-constexpr int64_t kCounterBytes = kMaxSplitTiles * 4;
 int64_t tiles_of(const Plan& p, int64_t M, int64_t N) { return ((M + p.tm - 1) / p.tm) * ((N + p.tn - 1) / p.tn); }
 int64_t workspace_bytes(const Plan& p, int64_t M, int64_t N) {
   if (p.ks <= 1) return 0;
@@ -969,6 +942,7 @@ int launch(int in_dtype, const Plan& p, const void* a, const void* b, const void
     t.tiles_n = (uint32_t)((N + p.tn - 1) / p.tn);
     t.xcd = p.xcd == 1 ? 1u : 0u;
     t.act = act;
+    t.gate = t.up = nullptr;
     t.ksplit = (uint32_t)p.ks;
     t.cnt = p.ks > 1 ? (uint32_t*)ws : nullptr;
     t.part = p.ks > 1 ? (char*)ws + kCounterBytes : nullptr;
@@ -1148,6 +1122,19 @@ int run_gemm(int in_dtype, int out_dtype, const void* a, const void* b_shuf, con
 }
 
 }  // namespace
+
+int plan_gemm(int in_dtype, int64_t M, int64_t N, int64_t K, Plan* p) {
+  return make_plan(in_dtype, M, N, K, nullptr, p, true);
+}
+int64_t plan_workspace(const Plan& p, int64_t M, int64_t N) { return workspace_bytes(p, M, N); }
+int launch_gemm(int in_dtype, const Plan& p, const void* a, const void* b_shuf, void* c, int64_t M, int64_t N,
+                void* ws, hipStream_t s) {
+  return launch(in_dtype, p, a, b_shuf, nullptr, nullptr, nullptr, GP_ACT_NONE, c, M, N, ws, s);
+}
+int report_hip(hipError_t e, const char* call) { return hip_status(e, call); }
+void forget_hip_error() { clear_last_error(); }
+int require_gfx950() { return check_device(); }
+
 }  // namespace gp
 
 using namespace gp;

@@ -1,0 +1,315 @@
+// Host side of the gated feed-forward product, its backward pass and the
+// backward pass of a linear layer: validation, plans, workspaces, launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/gemm_preshuffle.h"
+#include "host.hpp"
+#include "launch_gated.hpp"
+#include "transpose.hpp"
+
+namespace gp {
+namespace {
+
+bool half_type(int dtype) { return dtype == GP_BF16 || dtype == GP_F16; }
+
+// 16-byte pieces of the preshuffled gated layout: block 2p is gate block p of
+// the weights, block 2p + 1 up block p.
+__global__ __launch_bounds__(256) void preshuffle_gated_kernel(const char* __restrict__ w, char* __restrict__ dst,
+                                                               uint32_t kb64, uint32_t Kb, uint32_t F, uint32_t chunks) {
+  const uint32_t x = blockIdx.x * 256u + threadIdx.x;
+  if (x >= chunks) return;
+  const uint32_t j = x & 15u, g = (x >> 4) & 3u, t = x >> 6;
+  const uint32_t k0 = t % kb64, nb = t / kb64;
+  const uint32_t row = (nb & 1u) * F + (nb >> 1) * 16u + j;
+  *(v4i*)(dst + (size_t)x * 16u) = *(const v4i*)(w + (size_t)row * Kb + 64u * k0 + 16u * g);
+}
+
+// ---- gated product ----
+struct GatedPlan {
+  bool small = false;   // gated_small_kernel, else the tile kernel
+  int mb = 1, waves = 4;
+  Plan tile;
+};
+
+int check_gated(int dtype, int64_t M, int64_t F, int64_t H) {
+  if (M <= 0 || F <= 0 || H <= 0) return GP_EINVAL;
+  if (!half_type(dtype)) return GP_EDTYPE;
+  if (M >= kMaxBytes || F >= kMaxBytes / 2 || H >= kMaxBytes) return GP_ESHAPE;
+  if (F % 16 || H % 32) return GP_ESHAPE;
+  if (!fits(M, 2 * H) || !fits(2 * F, 2 * H) || !fits(M, 4 * F)) return GP_ESHAPE;
+  return GP_OK;
+}
+
+// Up to 64 rows, and above wherever the GEMM planner takes its small-M
+// kernel for [M][2F] outputs, the small gated kernel; otherwise the planner's
+// tile (every one it picks for these types has the gated epilogue, except the
+// 16-column waves of 16 x 64, a small-M shape).
+int plan_gated(int dtype, int64_t M, int64_t F, int64_t H, GatedPlan* p) {
+  const int r = check_gated(dtype, M, F, H);
+  if (r) return r;
+  p->small = M <= 64;
+  if (!p->small) {
+    const int rc = plan_gemm(dtype, M, 2 * F, H, &p->tile);
+    p->small = rc != GP_OK || p->tile.kernel != GP_KERNEL_TILE || p->tile.tn < 128;
+  }
+  if (p->small) {
+    p->mb = M > 32 ? 4 : M > 16 ? 2 : 1;
+    p->waves = 8;
+  }
+  return GP_OK;
+}
+
+// ---- backward pass of a linear layer C[M][N] = A[M][K] B[N][K]^T ----
+// da = dc b: K axis N; b transposed into the preshuffled layout.
+// db = dc^T a: K axis M, padded with zeros to whole 64-byte blocks; dc
+// transposed row-major, a transposed into the preshuffled layout.
+struct BackwardPlan {
+  Plan da, db;
+  int64_t Mp = 0;
+  // workspace: counters and partial sums of the two products (one after the
+  // other), then the transposed copies
+  int64_t parts = 0, off_bt = 0, off_at = 0, off_ct = 0, off_d = 0, bytes = 0;
+};
+
+int64_t align256(int64_t v) { return (v + 255) & ~(int64_t)255; }
+
+// gated: dc itself is made by the call ([M][N] in the workspace).
+int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, bool gated, BackwardPlan* p) {
+  if (M <= 0 || N <= 0 || K <= 0) return GP_EINVAL;
+  if (!half_type(dtype)) return GP_EDTYPE;
+  if (M >= kMaxBytes / 4 || N >= kMaxBytes || K >= kMaxBytes) return GP_ESHAPE;
+  if (N % 32 || K % 32) return GP_ESHAPE;
+  p->Mp = (M + 31) / 32 * 32;
+  if (!fits(p->Mp, 2 * K) || !fits(N, 2 * K) || !fits(p->Mp, 2 * N)) return GP_ESHAPE;
+  int r;
+  int64_t parts = 0;
+  if (want_da) {
+    if ((r = plan_gemm(dtype, M, K, N, &p->da))) return r;
+    parts = std::max(parts, plan_workspace(p->da, M, K));
+  }
+  if (want_db) {
+    if ((r = plan_gemm(dtype, N, K, p->Mp, &p->db))) return r;
+    parts = std::max(parts, plan_workspace(p->db, N, K));
+  }
+  int64_t at = p->parts = align256(parts);
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  p->off_bt = take(want_da ? N * K * 2 : 0);
+  p->off_at = take(want_db ? p->Mp * K * 2 : 0);
+  p->off_ct = take(want_db ? p->Mp * N * 2 : 0);
+  p->off_d = take(gated && want_da ? M * N * 2 : 0);
+  p->bytes = at;
+  return GP_OK;
+}
+
+__global__ __launch_bounds__(256) void clear_words_kernel(uint32_t* p, uint32_t n) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i < n) p[i] = 0u;
+}
+
+uint32_t tiles64(int64_t R, int64_t C) { return (uint32_t)(((R + 63) / 64) * ((C + 63) / 64)); }
+
+// Launches, in order, what has to run once the pointers are valid. dc: the
+// output gradient, or (gated) null with its transpose already in the
+// workspace. Stops at the first launch that fails.
+int run_backward(int dtype, const BackwardPlan& p, const void* dc, const void* a, const void* b, void* da, void* db,
+                 int64_t M, int64_t N, int64_t K, bool ct_ready, char* ws, hipStream_t s) {
+  int r;
+  if (p.parts > 0) {
+    // arrival counters of the K splits: cleared here, so that the workspace
+    // needs no state from earlier calls
+    forget_hip_error();
+    hipLaunchKernelGGL(clear_words_kernel, dim3((uint32_t)(kCounterBytes / 4 / 256)), dim3(256), 0, s, (uint32_t*)ws,
+                       (uint32_t)(kCounterBytes / 4));
+    if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
+  }
+  if (da) {
+    forget_hip_error();
+    hipLaunchKernelGGL(preshuffle_t_kernel, dim3(tiles64(N, K)), dim3(256), 0, s, (const char*)b, ws + p.off_bt,
+                       (uint32_t)N, (uint32_t)K, (uint32_t)N, (uint32_t)((K + 63) / 64));
+    if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
+    if ((r = launch_gemm(dtype, p.da, dc, ws + p.off_bt, da, M, K, ws, s))) return r;
+  }
+  if (db) {
+    forget_hip_error();
+    hipLaunchKernelGGL(preshuffle_t_kernel, dim3(tiles64(p.Mp, K)), dim3(256), 0, s, (const char*)a, ws + p.off_at,
+                       (uint32_t)M, (uint32_t)K, (uint32_t)p.Mp, (uint32_t)((K + 63) / 64));
+    if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
+    if (!ct_ready) {
+      forget_hip_error();
+      hipLaunchKernelGGL(transpose_kernel, dim3(tiles64(p.Mp, N)), dim3(256), 0, s, (const char*)dc, ws + p.off_ct,
+                         (uint32_t)M, (uint32_t)N, (uint32_t)p.Mp, (uint32_t)((N + 63) / 64));
+      if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
+    }
+    if ((r = launch_gemm(dtype, p.db, ws + p.off_ct, ws + p.off_at, db, N, K, ws, s))) return r;
+  }
+  return GP_OK;
+}
+
+int plan_gated_backward(int dtype, int64_t M, int64_t F, int64_t H, bool dx, bool dw, BackwardPlan* p) {
+  const int r = check_gated(dtype, M, F, H);
+  if (r) return r;
+  return plan_backward(dtype, M, 2 * F, H, dx, dw, true, p);
+}
+
+}  // namespace
+}  // namespace gp
+
+using namespace gp;
+
+extern "C" {
+
+int gemm_gated_preshuffle(const void* w, void* w_shuf, int64_t F, int64_t H, int dtype, void* stream) {
+  if (!w || !w_shuf || !is_aligned16(w) || !is_aligned16(w_shuf)) return GP_EINVAL;
+  int r = check_gated(dtype, 1, F, H);
+  if (r) return r;
+  const int64_t bytes = 4 * F * H;
+  const char *wb = (const char*)w, *sb = (const char*)w_shuf;
+  if (sb < wb + bytes && wb < sb + bytes) return GP_EINVAL;   // overlap
+  if ((r = require_gfx950())) return r;
+  const uint32_t chunks = (uint32_t)(bytes / 16);
+  forget_hip_error();
+  hipLaunchKernelGGL(preshuffle_gated_kernel, dim3((chunks + 255) / 256), dim3(256), 0, (hipStream_t)stream, wb,
+                     (char*)w_shuf, (uint32_t)(H / 32), (uint32_t)(2 * H), (uint32_t)F, chunks);
+  return report_hip(hipGetLastError(), "kernel launch");
+}
+
+int gemm_gated_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, size_t* bytes) {
+  if (!bytes) return GP_EINVAL;
+  GatedPlan p;
+  const int r = plan_gated(dtype, M, F, H, &p);
+  if (r) return r;
+  *bytes = p.small ? 0 : (size_t)plan_workspace(p.tile, M, 2 * F);
+  return GP_OK;
+}
+
+int gemm_gated(int dtype, const void* x, const void* w_shuf, int act, void* h, void* gate, void* up, int64_t M,
+               int64_t F, int64_t H, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!x || !w_shuf || !h || !is_aligned16(x) || !is_aligned16(w_shuf) || !is_aligned16(h)) return GP_EINVAL;
+  if (!gate != !up || !is_aligned16(gate) || !is_aligned16(up)) return GP_EINVAL;
+  if (act < GP_ACT_NONE || act > GP_ACT_GELU) return GP_EINVAL;
+  GatedPlan p;
+  int r = plan_gated(dtype, M, F, H, &p);
+  if (r) return r;
+  const int64_t need = p.small ? 0 : plan_workspace(p.tile, M, 2 * F);
+  if (need > 0) {
+    if (!workspace || (int64_t)workspace_bytes < need) return GP_EWORKSPACE;
+    if (!is_aligned16(workspace)) return GP_EINVAL;
+  }
+  if ((r = require_gfx950())) return r;
+  const hipStream_t s = (hipStream_t)stream;
+  forget_hip_error();
+  hipError_t e;
+  if (p.small) {
+    GatedArgs t;
+    t.a = (const char*)x;
+    t.b = (const char*)w_shuf;
+    t.c = (char*)h;
+    t.gate = (char*)gate;
+    t.up = (char*)up;
+    t.M = (uint32_t)M;
+    t.F = (uint32_t)F;
+    t.Kb = (uint32_t)(2 * H);
+    t.act = act;
+    e = dtype == GP_BF16 ? launch_gated_small_bf16(p.mb, p.waves, t, s) : launch_gated_small_f16(p.mb, p.waves, t, s);
+  } else {
+    TileArgs t;
+    t.a = (const char*)x;
+    t.b = (const char*)w_shuf;
+    t.sa = t.sb = nullptr;
+    t.bias = nullptr;
+    t.c = (char*)h;
+    t.M = (uint32_t)M;
+    t.N = (uint32_t)(2 * F);
+    t.Kb = (uint32_t)(2 * H);
+    t.tiles_m = (uint32_t)((M + p.tile.tm - 1) / p.tile.tm);
+    t.tiles_n = (uint32_t)((2 * F + p.tile.tn - 1) / p.tile.tn);
+    t.xcd = 1;
+    t.act = act;
+    t.gate = (char*)gate;
+    t.up = (char*)up;
+    t.ksplit = (uint32_t)p.tile.ks;
+    t.cnt = p.tile.ks > 1 ? (uint32_t*)workspace : nullptr;
+    t.part = p.tile.ks > 1 ? (char*)workspace + kCounterBytes : nullptr;
+    e = dtype == GP_BF16 ? launch_gated_tile_bf16(p.tile.tm, p.tile.tn, p.tile.tkb, p.tile.pipe, t, s)
+                         : launch_gated_tile_f16(p.tile.tm, p.tile.tn, p.tile.tkb, p.tile.pipe, t, s);
+  }
+  return report_hip(e, "kernel launch");
+}
+
+int gemm_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int want_da, int want_db, size_t* bytes) {
+  if (!bytes || (!want_da && !want_db)) return GP_EINVAL;
+  BackwardPlan p;
+  const int r = plan_backward(dtype, M, N, K, want_da != 0, want_db != 0, false, &p);
+  if (r) return r;
+  *bytes = (size_t)p.bytes;
+  return GP_OK;
+}
+
+int gemm_backward(int dtype, const void* dc, const void* a, const void* b, void* da, void* db, int64_t M, int64_t N,
+                  int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dc || !is_aligned16(dc) || (!da && !db)) return GP_EINVAL;
+  if ((da && !b) || (db && !a)) return GP_EINVAL;
+  if (!is_aligned16(a) || !is_aligned16(b) || !is_aligned16(da) || !is_aligned16(db)) return GP_EINVAL;
+  BackwardPlan p;
+  int r = plan_backward(dtype, M, N, K, da != nullptr, db != nullptr, false, &p);
+  if (r) return r;
+  if (!workspace || (int64_t)workspace_bytes < p.bytes) return GP_EWORKSPACE;
+  if (!is_aligned16(workspace)) return GP_EINVAL;
+  if ((r = require_gfx950())) return r;
+  return run_backward(dtype, p, dc, a, b, da, db, M, N, K, false, (char*)workspace, (hipStream_t)stream);
+}
+
+int gemm_gated_backward_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, int want_dx, int want_dw,
+                                       size_t* bytes) {
+  if (!bytes || (!want_dx && !want_dw)) return GP_EINVAL;
+  BackwardPlan p;
+  const int r = plan_gated_backward(dtype, M, F, H, want_dx != 0, want_dw != 0, &p);
+  if (r) return r;
+  *bytes = (size_t)p.bytes;
+  return GP_OK;
+}
+
+int gemm_gated_backward(int dtype, const void* dh, const void* gate, const void* up, const void* x, const void* w,
+                        int act, void* dx, void* dw, int64_t M, int64_t F, int64_t H, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  if (!dh || !gate || !up || (!dx && !dw)) return GP_EINVAL;
+  if ((dx && !w) || (dw && !x)) return GP_EINVAL;
+  if (!is_aligned16(dh) || !is_aligned16(gate) || !is_aligned16(up) || !is_aligned16(x) || !is_aligned16(w) ||
+      !is_aligned16(dx) || !is_aligned16(dw))
+    return GP_EINVAL;
+  if (act < GP_ACT_NONE || act > GP_ACT_GELU) return GP_EINVAL;
+  BackwardPlan p;
+  int r = plan_gated_backward(dtype, M, F, H, dx != nullptr, dw != nullptr, &p);
+  if (r) return r;
+  if (!workspace || (int64_t)workspace_bytes < p.bytes) return GP_EWORKSPACE;
+  if (!is_aligned16(workspace)) return GP_EINVAL;
+  if ((r = require_gfx950())) return r;
+  char* ws = (char*)workspace;
+  const hipStream_t s = (hipStream_t)stream;
+  GateGradArgs t;
+  t.dh = (const char*)dh;
+  t.gate = (const char*)gate;
+  t.up = (const char*)up;
+  t.d = dx ? ws + p.off_d : nullptr;
+  t.dt = dw ? ws + p.off_ct : nullptr;
+  t.M = (uint32_t)M;
+  t.F = (uint32_t)F;
+  t.Mp = (uint32_t)p.Mp;
+  t.tiles_c = (uint32_t)((F + 63) / 64);
+  t.act = act;
+  forget_hip_error();
+  const dim3 grid(tiles64(p.Mp, F));
+  if (dtype == GP_BF16) hipLaunchKernelGGL((gate_grad_kernel<DT_BF16>), grid, dim3(256), 0, s, t);
+  else hipLaunchKernelGGL((gate_grad_kernel<DT_F16>), grid, dim3(256), 0, s, t);
+  if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
+  return run_backward(dtype, p, ws + p.off_d, x, w, dx, dw, M, 2 * F, H, true, ws, s);
+}
+
+}  // extern "C"

@@ -50,6 +50,8 @@ struct TileArgs {
   uint32_t tiles_m, tiles_n;  // ceil(M / TM), ceil(N / TN)
   uint32_t xcd;       // 1: XCD-aware, grouped tile order
   int act;            // Act
+  char* gate;         // EPI_GATED: [M][N/2] gate and up products to keep, or null
+  char* up;
   // K split across workgroups (tile kernel): ksplit workgroups share each
   // tile, each taking a contiguous range of its K tiles; their partial sums
   // meet in `part` and the last one to finish adds them and stores the tile.
@@ -121,8 +123,9 @@ struct TileCfg {
   static constexpr int ABUF = TM * TKA + (APART ? 16 : 0);   // + a spare slot for idle lanes
   static constexpr int OB = (DT == DT_I8) ? 4 : 2;        // output element bytes
   static constexpr bool FSC = DT == DT_FP8 || DT == DT_I4;  // fp32 row / column scales
-  static constexpr int CSTRIDE = TN * OB + 16;            // padded C row in LDS
-  static constexpr int CBYTES = (EPI == EPI_CSHUFFLE) ? TM * CSTRIDE : 0;
+  static constexpr int CCOLS = (EPI == EPI_GATED) ? TN / 2 : TN;   // stored columns
+  static constexpr int CSTRIDE = CCOLS * OB + 16;         // padded C row in LDS
+  static constexpr int CBYTES = (EPI == EPI_DIRECT) ? 0 : TM * CSTRIDE;
   static constexpr int SWP = (TKA >= 256) ? 1 : 256 / TKA;  // rows per 256-byte period
   static constexpr int SWM = ((CPR < 16) ? CPR : 16) - 1;   // chunk xor mask
   static constexpr int NSC = (DT == DT_FP4) ? 1 : 0;
@@ -212,6 +215,8 @@ struct TileCfg {
   static_assert(KG == 1 || (KG == 2 && !NSC), "K groups: not with FP4's staged scales");
   static_assert(DT != DT_I4 || MS == 16, "W4A8: 16 x 16 blocks");
   static_assert(WAVES == 4 || KG == 1, "8-wave tiles: one K group");
+  static_assert(EPI != EPI_GATED || (MS == 16 && NACC % 2 == 0 && KG == 1 && (DT == DT_BF16 || DT == DT_F16)),
+                "gated epilogue: whole gate / up pairs of 16-column blocks per wave");
 };
 
 // Tile (tm, tn) and K split z of this workgroup. With a K split the ksplit
@@ -890,6 +895,51 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
       emit(pack_out4<DT>(v));
     }
   };
+
+  if constexpr (EPI == EPI_GATED) {
+    // B's 16-column blocks alternate between gate and up rows of the weights,
+    // so blocks 2j and 2j+1 of a lane hold the two products of the same
+    // output columns: h = act(gate) * up, in fp32, rounded once. Each of h,
+    // gate and up goes through LDS (the A buffers are dead) for whole-row
+    // stores, one after the other through the same tile.
+    constexpr int HPW = C::NPW / 2, CH_ROW = C::CCOLS * C::OB / 16, TOTAL = TM * CH_ROW;
+    const uint32_t F = p.N / 2, f0 = n0 / 2, fskip = nskip / 2;
+    const size_t base = ((size_t)m0 * F + f0) * C::OB;
+    const uint32_t bytes = ((TM - 1) * F + C::CCOLS) * C::OB;
+    auto store_half = [&](char* dst, auto&& value) GP_INLINE {
+      __syncthreads();   // the tile in LDS is free (K loop, or the previous output's reads)
+#pragma unroll
+      for (int mi = 0; mi < C::MREP; ++mi)
+#pragma unroll
+        for (int nj = 0; nj < C::NACC / 2; ++nj)
+          *(v2i*)(lds + (mi * MS + elrow) * C::CSTRIDE + (wave * HPW + nj * 16 + 4 * elgrp) * C::OB) =
+              pack_out4<DT>(value(acc[mi][2 * nj], acc[mi][2 * nj + 1]));
+      __syncthreads();
+      const __amdgpu_buffer_rsrc_t rh = make_rsrc(dst + base, bytes);
+#pragma unroll
+      for (int i = 0; i < (TOTAL + C::THREADS - 1) / C::THREADS; ++i) {
+        const int q = i * C::THREADS + etid;
+        if (TOTAL % C::THREADS != 0 && q >= TOTAL) break;
+        const uint32_t row = q / CH_ROW, col = (q % CH_ROW) * 8;
+        const v4i v = *(const v4i*)(lds + row * C::CSTRIDE + col * C::OB);
+        buf_store16(v, rh, (row >= mskip && col >= fskip) ? (row * F + col) * C::OB : 0x80000000u);
+      }
+    };
+    with_act(p.act, [&](auto act_c) GP_INLINE {
+      constexpr int A = decltype(act_c)::value;
+      store_half(p.c, [](Acc g, Acc u) GP_INLINE {
+        v4f h;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = activate<A>(g[r]) * u[r];
+        return h;
+      });
+    });
+    if (p.gate) {
+      store_half(p.gate, [](Acc g, Acc) GP_INLINE -> v4f { return g; });
+      store_half(p.up, [](Acc, Acc u) GP_INLINE -> v4f { return u; });
+    }
+    return;
+  }
 
   const bool storer = grp == 0;
   auto store_tile = [&](auto act_c) GP_INLINE {

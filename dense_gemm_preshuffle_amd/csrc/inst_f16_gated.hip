@@ -1,0 +1,9 @@
+// Kernel instantiations with the gated epilogue for one input type.
+#include "launch_gated.hpp"
+#include "variants.hpp"
+
+namespace gp {
+
+GP_DEFINE_GATED(f16, DT_F16, GP_TILE_GATED_F16, GP_TILE_GATED_KSPLIT_F16)
+
+}  // namespace gp

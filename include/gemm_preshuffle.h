@@ -348,6 +348,76 @@ int gemm_workspace_size(int in_dtype, int64_t M, int64_t N, int64_t K, const gem
  */
 int gemm_plan_ws(int in_dtype, int64_t M, int64_t N, int64_t K, const gemm_opts* opts, gemm_plan_info* out);
 
+/*
+ * ---- Gated feed-forward product and its backward pass (BF16, FP16) ----
+ *
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) * u
+ *
+ * x [M][H], h / g / u [M][F], both weights in one matrix w [2F][H]: the F gate
+ * rows, then the F up rows. act is a GP_ACT_* (the activations above). M is
+ * free, F % 16 == 0, H % 32 == 0 (else GP_ESHAPE), every matrix below 2^31
+ * bytes; the buffers of one type (GP_BF16 or GP_F16, else GP_EDTYPE).
+ *
+ * gemm_gated_preshuffle -- w [2F][H] -> w_shuf (4 F H bytes, no overlap): the
+ * layout of gemm_preshuffle_b with 16-row blocks of gate and up alternating,
+ * so that one lane of a product ends up with both factors of its outputs.
+ */
+int gemm_gated_preshuffle(const void* w, void* w_shuf, int64_t F, int64_t H, int dtype, void* stream);
+
+/*
+ * gemm_gated -- h = act(x Wg^T) * (x Wu^T) in one kernel: both products are
+ * accumulated in fp32, the activation and the product taken in fp32, and h
+ * rounded once to the type.
+ *   w_shuf      from gemm_gated_preshuffle.
+ *   gate, up    device [M][F], or both NULL: the two products rounded to the
+ *               type, which the backward pass reads (one of them: GP_EINVAL).
+ *   workspace   as for gemm_ex_ws (its first 64 KiB zero before the first
+ *               call and left zero by each), at least
+ *               gemm_gated_workspace_size bytes; may be NULL where that is 0.
+ */
+int gemm_gated(int dtype, const void* x, const void* w_shuf, int act, void* h, void* gate, void* up, int64_t M,
+               int64_t F, int64_t H, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Host-only: the workspace bytes of gemm_gated for these sizes (0: none). */
+int gemm_gated_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, size_t* bytes);
+
+/*
+ * gemm_gated_backward -- gradients of gemm_gated from dh = dL/dh and the kept
+ * gate and up:
+ *   dg = dh * up * act'(gate),  du = dh * act(gate)
+ *   dx [M][H] = [dg du] w,      dw [2F][H] = [dg du]^T x
+ *   w           row-major [2F][H], as given to gemm_gated_preshuffle (needed
+ *               for dx); x [M][H] (needed for dw).
+ *   dx, dw      outputs; either may be NULL (not computed), not both.
+ *   workspace   16-byte aligned, at least gemm_gated_backward_workspace_size
+ *               bytes for the same outputs; its contents need not be set.
+ * dg and du are rounded to the type before the two products, which accumulate
+ * in fp32 and round once. relu'(0) is 0. The same call gives the same bits.
+ */
+int gemm_gated_backward(int dtype, const void* dh, const void* gate, const void* up, const void* x, const void* w,
+                        int act, void* dx, void* dw, int64_t M, int64_t F, int64_t H, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Host-only: the workspace bytes of gemm_gated_backward. */
+int gemm_gated_backward_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, int want_dx, int want_dw,
+                                       size_t* bytes);
+
+/*
+ * gemm_backward -- gradients of a linear layer C[M][N] = A[M][K] B[N][K]^T
+ * (gemm_bf16, gemm_f16) from dc = dL/dC [M][N]:
+ *   da [M][K] = dc B,  db [N][K] = dc^T A
+ *   a, b        row-major (b is not preshuffled); a is needed for db, b for da.
+ *   da, db      outputs; either may be NULL, not both.
+ *   workspace   16-byte aligned, at least gemm_backward_workspace_size bytes
+ *               for the same outputs; its contents need not be set.
+ * N % 32 == 0 and K % 32 == 0 (else GP_ESHAPE); M is free.
+ */
+int gemm_backward(int dtype, const void* dc, const void* a, const void* b, void* da, void* db, int64_t M, int64_t N,
+                  int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Host-only: the workspace bytes of gemm_backward. */
+int gemm_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int want_da, int want_db, size_t* bytes);
+
 /* Static, human-readable description of a gp_status value. */
 const char* gemm_status_string(int status);
 
