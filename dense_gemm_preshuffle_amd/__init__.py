@@ -26,6 +26,9 @@ points have the names of the C ABI (include/gemm_preshuffle.h):
     gemm_backward(dtype, dc, a, b)                   -> da, db of C = A B^T
     gated_workspace, gated_backward_workspace, backward_workspace
                                                      -> device workspaces of these
+    gemm_w4a16_preshuffle(q, scales, zeros, group)   -> W4Weights, 4-bit weights laid out with their scales
+    gemm_w4a16(x, weights, bias, act)                -> act(x W^T + bias) (BF16 / FP16 activations)
+    gemm_w4a16_gated(x, weights, act)                -> act(x Wg^T) * (x Wu^T) on 4-bit weights
 
 Tensors: A is [M, K] (INT8 / FP8 as any 1-byte dtype, BF16 / FP16 as
 bfloat16 / float16 or a 2-byte integer view, MXFP4 as uint8 [M, K/2]; W4A8:
@@ -45,8 +48,9 @@ __all__ = [
     "gemm_plan", "ACTS", "gemm_ex_ws", "gemm_ex_noalloc", "gemm_workspace_size", "gemm_plan_ws", "workspace",
     "gemm_gated_preshuffle", "gemm_gated", "gemm_gated_workspace_size", "gated_workspace", "gemm_gated_backward",
     "gemm_gated_backward_workspace_size", "gated_backward_workspace", "gemm_backward", "gemm_backward_workspace_size",
-    "backward_workspace", "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE", "KERNEL_SPLITK",
-    "KERNEL_WIDE",
+    "backward_workspace", "W4Weights", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle", "gemm_w4a16",
+    "gemm_w4a16_gated", "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE",
+    "KERNEL_SPLITK", "KERNEL_WIDE",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -147,6 +151,10 @@ def load_library():
     lib.gemm_gated_backward_workspace_size.argtypes = [ci, i64, i64, i64, ci, ci, psz]
     lib.gemm_backward.argtypes = [ci, vp, vp, vp, vp, vp, i64, i64, i64, vp, sz, vp]
     lib.gemm_backward_workspace_size.argtypes = [ci, i64, i64, i64, ci, ci, psz]
+    lib.gemm_w4a16_weights_size.argtypes = [i64, i64, ci, ci, ci, psz]
+    lib.gemm_w4a16_preshuffle.argtypes = [ci, vp, vp, vp, vp, i64, i64, ci, ci, vp]
+    lib.gemm_w4a16.argtypes = [ci, vp, vp, ci, vp, ci, vp, i64, i64, i64, ci, vp]
+    lib.gemm_w4a16_gated.argtypes = [ci, vp, vp, ci, ci, vp, i64, i64, i64, ci, vp]
     lib.gemm_status_string.argtypes = [ci]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_last_hip_error.argtypes = []
@@ -156,7 +164,8 @@ def load_library():
     for f in ("gemm_preshuffle_b", "gemm_a8w8", "gemm_bf16", "gemm_mxfp4", "gemm_f16", "gemm_w4a8", "gemm_ex",
               "gemm_plan", "gemm_plan_ws", "gemm_workspace_size", "gemm_ex_ws", "gemm_ex_noalloc", "gemm_gated_preshuffle", "gemm_gated",
               "gemm_gated_workspace_size", "gemm_gated_backward", "gemm_gated_backward_workspace_size",
-              "gemm_backward", "gemm_backward_workspace_size"):
+              "gemm_backward", "gemm_backward_workspace_size", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle",
+              "gemm_w4a16", "gemm_w4a16_gated"):
         getattr(lib, f).restype = ci
     _lib = lib
     return lib
@@ -602,3 +611,87 @@ def gemm_backward(dtype, dc, a, b, want_da=True, want_db=True, da=None, db=None,
         _check(load_library().gemm_backward(dt, _ptr(dc), _ptr(a), _ptr(b), _ptr(da), _ptr(db), M, N, K,
                                             _ptr(workspace), _nbytes(workspace), _stream(stream)), "gemm_backward")
     return da, db
+
+
+# ---- 4-bit weights with group scales ----
+
+class W4Weights:
+    """Laid-out 4-bit weights (gemm_w4a16_preshuffle): the device buffer and what it holds.
+    N is the number of output columns (gated: F, from 2 F rows)."""
+
+    __slots__ = ("data", "dtype", "N", "K", "group", "has_zeros", "gated")
+
+    def __init__(self, data, dtype, N, K, group, has_zeros, gated):
+        self.data, self.dtype, self.N, self.K = data, dtype, N, K
+        self.group, self.has_zeros, self.gated = group, has_zeros, gated
+
+
+def gemm_w4a16_weights_size(N: int, K: int, group: int, has_zeros=False, gated=False) -> int:
+    """Host-only: bytes of laid-out 4-bit weights (gated: N = 2 F rows)."""
+    return _size("gemm_w4a16_weights_size", N, K, group, int(has_zeros), int(gated))
+
+
+def gemm_w4a16_preshuffle(q, scales, zeros=None, group=128, gated=False, out=None, stream=None) -> W4Weights:
+    """q uint8 [N, K/2] (two's complement 4-bit integers, the even k in the low nibble), scales bf16 or
+    fp16 [N, ceil(K/group)], zeros int8 of that shape or None -> W4Weights for gemm_w4a16, or with
+    gated (F gate rows, then F up rows) for gemm_w4a16_gated. x has the scales' type."""
+    import torch
+
+    where = "gemm_w4a16_preshuffle"
+    N, K = q.shape[0], 2 * q.shape[1]
+    if scales.dtype not in (torch.bfloat16, torch.float16):
+        raise GemmError(GP_EDTYPE, f"{where}: scales are bf16 or fp16")
+    dt = GP_BF16 if scales.dtype == torch.bfloat16 else GP_F16
+    n = gemm_w4a16_weights_size(N, K, group, zeros is not None, gated)
+    groups = -(-K // group)
+    _want(f"{where}: q", q, (N, K // 2), torch.uint8)
+    _want(f"{where}: scales", scales, (N, groups), scales.dtype, q.device)
+    if zeros is not None:
+        _want(f"{where}: zeros", zeros, (N, groups), torch.int8, q.device)
+    with _on(stream, q.device):
+        out = torch.empty(n, dtype=torch.uint8, device=q.device) if out is None else out
+        _want(f"{where}: out", out, (n,), torch.uint8, q.device)
+        _check(load_library().gemm_w4a16_preshuffle(dt, _ptr(q), _ptr(scales), _ptr(zeros), _ptr(out), N, K, group,
+                                                    int(gated), _stream(stream)), where)
+    return W4Weights(out, scales.dtype, N // 2 if gated else N, K, group, zeros is not None, bool(gated))
+
+
+def _w4_args(where, x, weights, y, gated):
+    """Checks x and the weights of a 4-bit product."""
+    if weights.gated != gated:
+        raise ValueError(f"{where}: the weights were laid out {'' if weights.gated else 'not '}gated")
+    M = x.shape[0]
+    _want(f"{where}: x", x, (M, weights.K), weights.dtype, weights.data.device)
+    if y is not None:
+        _want(f"{where}: output", y, (M, weights.N), weights.dtype, x.device)
+    import torch
+
+    return M, (GP_BF16 if weights.dtype == torch.bfloat16 else GP_F16)
+
+
+def gemm_w4a16(x, weights: W4Weights, bias=None, act="none", y=None, stream=None):
+    """y = act(x W^T + bias) on 4-bit weights: x [M, K] of the scales' type, bias fp32 [N] or None."""
+    import torch
+
+    M, dt = _w4_args("gemm_w4a16", x, weights, y, False)
+    if bias is not None:
+        _want("gemm_w4a16: bias", bias, (weights.N,), torch.float32, x.device)
+    with _on(stream, x.device):
+        y = torch.empty(M, weights.N, dtype=x.dtype, device=x.device) if y is None else y
+        _check(load_library().gemm_w4a16(dt, _ptr(x), _ptr(weights.data), int(weights.has_zeros), _ptr(bias),
+                                         _act(act), _ptr(y), M, weights.N, weights.K, weights.group,
+                                         _stream(stream)), "gemm_w4a16")
+    return y
+
+
+def gemm_w4a16_gated(x, weights: W4Weights, act="silu", h=None, stream=None):
+    """h = act(x Wg^T) * (x Wu^T) on 4-bit weights laid out gated: x [M, K] of the scales' type."""
+    import torch
+
+    M, dt = _w4_args("gemm_w4a16_gated", x, weights, h, True)
+    with _on(stream, x.device):
+        h = torch.empty(M, weights.N, dtype=x.dtype, device=x.device) if h is None else h
+        _check(load_library().gemm_w4a16_gated(dt, _ptr(x), _ptr(weights.data), int(weights.has_zeros), _act(act),
+                                               _ptr(h), M, weights.N, weights.K, weights.group, _stream(stream)),
+               "gemm_w4a16_gated")
+    return h

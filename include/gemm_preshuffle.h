@@ -418,6 +418,45 @@ int gemm_backward(int dtype, const void* dc, const void* a, const void* b, void*
 /* Host-only: the workspace bytes of gemm_backward. */
 int gemm_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int want_da, int want_db, size_t* bytes);
 
+/*
+ * ---- Products with 4-bit weights and group scales (BF16 / FP16 activations) ----
+ *
+ *   y = act(x W^T + bias),  W[n][k] = scale[n][k / G] (q[n][k] - zero[n][k / G])
+ *
+ * for few rows (a generated token, a small batch): bound by reading the 4-bit
+ * weights. q [N][K/2] holds two's complement 4-bit integers, the even k in the
+ * low nibble; scales [N][ceil(K / G)] are of x's type, zeros int8 of the same
+ * shape, or absent (0). M and N are free, K % 32 == 0 and K < 2^23, the group
+ * size G a power of two from 32 on (one that covers K: a scale per output); the
+ * last group may be short. Else GP_ESHAPE. No weight is rounded: the integers
+ * are multiplied exactly and summed per group in fp32, then scaled.
+ *
+ * gemm_w4a16_weights_size -- host-only: bytes of the laid-out weights. gated:
+ * N is 2 F (the F gate rows, then the F up rows).
+ */
+int gemm_w4a16_weights_size(int64_t N, int64_t K, int group, int has_zeros, int gated, size_t* bytes);
+
+/* gemm_w4a16_preshuffle -- q, scales and zeros (or NULL) -> w_shuf
+ * (gemm_w4a16_weights_size bytes, no overlap), once per weight matrix. */
+int gemm_w4a16_preshuffle(int dtype, const void* q, const void* scales, const int8_t* zeros, void* w_shuf, int64_t N,
+                          int64_t K, int group, int gated, void* stream);
+
+/*
+ * gemm_w4a16 -- y [M][N] in x's type (GP_BF16 or GP_F16, else GP_EDTYPE).
+ *   w_shuf, has_zeros, group  as laid out (gated 0).
+ *   bias                      device fp32 [N], or NULL.
+ * All device pointers 16-byte aligned (GP_EINVAL). The same call gives the
+ * same bits. Any M is served, more than 32 rows in blocks that read the
+ * weights again.
+ */
+int gemm_w4a16(int dtype, const void* x, const void* w_shuf, int has_zeros, const float* bias, int act, void* y,
+               int64_t M, int64_t N, int64_t K, int group, void* stream);
+
+/* gemm_w4a16_gated -- h [M][F] = act(x Wg^T) * (x Wu^T), w_shuf laid out with
+ * gated = 1 from N = 2 F rows; both products stay in fp32, h is rounded once. */
+int gemm_w4a16_gated(int dtype, const void* x, const void* w_shuf, int has_zeros, int act, void* h, int64_t M,
+                     int64_t F, int64_t K, int group, void* stream);
+
 /* Static, human-readable description of a gp_status value. */
 const char* gemm_status_string(int status);
 
