@@ -127,13 +127,13 @@ __device__ __forceinline__ void activate_grad(float g, float& value, float& slop
 //   dg = dh * up * act'(gate), du = dh * act(gate)
 // in fp32, rounded once to the 16-bit type the matrix products read (the
 // products' own results are rounded to it as well, so this adds at most as
-// much error again). Written as d [M][2F] (dg then du in each row; null if
-// dx is not wanted) and dt = d^T [2F][Mp], zeros from M to Mp (null if dw is
+// much error again). Written as d [M][Np] (dg, du, then zeros from 2F to Np in
+// each row; null if dx is not wanted) and dt = d^T [2F][Mp], zeros from M to Mp (null if dw is
 // not wanted). F % 16 == 0.
 struct GateGradArgs {
   const char *dh, *gate, *up;
   char *d, *dt;
-  uint32_t M, F, Mp, tiles_c;
+  uint32_t M, F, Mp, Np, tiles_c;
   int act;
 };
 template <int DT>
@@ -180,10 +180,16 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateGradArgs p) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       if (r + h < p.M) {
-        char* o = p.d + ((size_t)(r + h) * 2 * p.F + c) * 2;
+        char* o = p.d + ((size_t)(r + h) * p.Np + c) * 2;
         *(v4i*)o = dg[h];
         *(v4i*)(o + (size_t)p.F * 2) = du[h];
       }
+  if (p.d && c0 + 64 >= p.F) {
+    // the last column tile fills the padding of its rows, 8 columns at a time
+    const uint32_t pad = (p.Np - 2 * p.F) / 8, rows = r0 < p.M ? min(64u, p.M - r0) : 0u;
+    for (uint32_t x = threadIdx.x; x < rows * pad; x += 256)
+      *(v4i*)(p.d + ((size_t)(r0 + x / pad) * p.Np + 2 * p.F + x % pad * 8) * 2) = v4i{0, 0, 0, 0};
+  }
   if (!p.dt) return;
   tg.put(q, rp, dg[0], dg[1]);
   tu.put(q, rp, du[0], du[1]);
