@@ -5,40 +5,51 @@
 
 namespace gp {
 
-// A variant: row blocks, column blocks, waves, 128-element K blocks per chunk.
+// A variant of w4a16_kernel: x loads (0: one row, else rows / 4), column
+// blocks, waves, 128-element K blocks per chunk.
 struct W4Plan {
-  int mb = 1, nb = 1, waves = 8;
-  bool one = false;   // a single row
+  int xl = 0, nb = 1, waves = 16, s = 1;
 };
-// sg: scales per 128-element block and column (1, 2, 4). hipErrorInvalidValue
-// if the variant is not compiled.
+// sg: scales per 128-element block and column (1, 2, 4); _z: with zero points.
+// hipErrorInvalidValue if the variant is not compiled.
 hipError_t launch_w4_bf16(const W4Plan& p, int sg, const W4Args& a, hipStream_t s);
+hipError_t launch_w4_bf16_z(const W4Plan& p, int sg, const W4Args& a, hipStream_t s);
 hipError_t launch_w4_f16(const W4Plan& p, int sg, const W4Args& a, hipStream_t s);
+hipError_t launch_w4_f16_z(const W4Plan& p, int sg, const W4Args& a, hipStream_t s);
 
 }  // namespace gp
 
-#define GP_W4_KERNEL(DT, MB, NB, W, S, SGV, ZV, ONE)                                                              \
-  {                                                                                                            \
-    const dim3 grid(((a.nblk + NB - 1) / NB) * ((a.M + 16 * MB - 1) / (16 * MB)));                              \
-    hipLaunchKernelGGL((w4a16_kernel<DT, MB, NB, W, S, SGV, ZV, ONE>), grid, dim3(W * 64), 0, s, a);            \
+#define GP_W4_KERNEL(DT, XL, NB, W, S, SGV, ZV)                                                                \
+  if (sg == SGV) {                                                                                             \
+    constexpr uint32_t rows = XL == 0 ? 1 : 4 * XL;                                                            \
+    const dim3 grid(((a.nblk + NB - 1) / NB) * ((a.M + rows - 1) / rows));                                     \
+    hipLaunchKernelGGL((w4a16_kernel<DT, XL, NB, W, S, SGV, ZV>), grid, dim3(W * 64), 0, s, a);                \
     return hipGetLastError();                                                                                  \
   }
-#define GP_W4_CASE(DT, MB, NB, W, S, ONE)                                                                      \
-  if (p.mb == MB && p.nb == NB && p.waves == W && p.one == ONE) {                                              \
-    if (sg == 1 && !a.z) GP_W4_KERNEL(DT, MB, NB, W, S, 1, false, ONE)                                         \
-    if (sg == 2 && !a.z) GP_W4_KERNEL(DT, MB, NB, W, S, 2, false, ONE)                                         \
-    if (sg == 4 && !a.z) GP_W4_KERNEL(DT, MB, NB, W, S, 4, false, ONE)                                         \
-    if (sg == 1) GP_W4_KERNEL(DT, MB, NB, W, S, 1, true, ONE)                                                  \
-    if (sg == 2) GP_W4_KERNEL(DT, MB, NB, W, S, 2, true, ONE)                                                  \
-    if (sg == 4) GP_W4_KERNEL(DT, MB, NB, W, S, 4, true, ONE)                                                  \
+#define GP_W4_CASE(DT, ZV, XL, NB, W, S)                                                                       \
+  if (p.xl == XL && p.nb == NB && p.waves == W && p.s == S) {                                                  \
+    GP_W4_KERNEL(DT, XL, NB, W, S, 1, ZV)                                                                      \
+    GP_W4_KERNEL(DT, XL, NB, W, S, 2, ZV)                                                                      \
+    GP_W4_KERNEL(DT, XL, NB, W, S, 4, ZV)                                                                      \
   }
-// (rows / 16, columns / 16, waves, K blocks per chunk, single row)
-#define GP_DEFINE_W4(NAME, DT)                                                                                 \
+#define GP_DEFINE_W4(NAME, DT, ZV)                                                                             \
   hipError_t launch_w4_##NAME(const W4Plan& p, int sg, const W4Args& a, hipStream_t s) {                       \
-    GP_W4_CASE(DT, 1, 1, 8, 2, true)                                                                           \
-    GP_W4_CASE(DT, 1, 2, 8, 2, true)                                                                           \
-    GP_W4_CASE(DT, 1, 1, 8, 2, false)                                                                          \
-    GP_W4_CASE(DT, 1, 2, 8, 2, false)                                                                          \
-    GP_W4_CASE(DT, 2, 2, 8, 1, false)                                                                          \
+    GP_W4_CASE(DT, ZV, 0, 1, 16, 1)                                                                            \
+    GP_W4_CASE(DT, ZV, 0, 2, 16, 1)                                                                            \
+    GP_W4_CASE(DT, ZV, 0, 2, 8, 1)                                                                             \
+    GP_W4_CASE(DT, ZV, 0, 2, 4, 2)                                                                             \
+    GP_W4_CASE(DT, ZV, 1, 1, 16, 1)                                                                            \
+    GP_W4_CASE(DT, ZV, 1, 2, 16, 1)                                                                            \
+    GP_W4_CASE(DT, ZV, 1, 2, 8, 1)                                                                             \
+    GP_W4_CASE(DT, ZV, 1, 4, 4, 1)                                                                             \
+    GP_W4_CASE(DT, ZV, 4, 1, 8, 1)                                                                             \
+    GP_W4_CASE(DT, ZV, 4, 2, 8, 1)                                                                             \
+    GP_W4_CASE(DT, ZV, 4, 4, 8, 1)                                                                             \
+    GP_W4_CASE(DT, ZV, 8, 1, 8, 1)                                                                             \
+    GP_W4_CASE(DT, ZV, 8, 2, 8, 1)                                                                             \
+    GP_W4_CASE(DT, ZV, 8, 4, 8, 1)                                                                             \
+    GP_W4_CASE(DT, ZV, 16, 1, 8, 1)                                                                            \
+    GP_W4_CASE(DT, ZV, 16, 2, 4, 1)                                                                            \
+    GP_W4_CASE(DT, ZV, 16, 4, 4, 1)                                                                            \
     return hipErrorInvalidValue;                                                                               \
   }

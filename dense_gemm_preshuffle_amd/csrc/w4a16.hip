@@ -90,14 +90,38 @@ __global__ __launch_bounds__(256) void layout_w4_kernel(W4LayoutArgs p) {
   }
 }
 
-// Rows per workgroup by M; two column blocks where one each would give more
-// than two workgroups per CU (and for gate and up pairs).
+// The variant by the number of rows and column blocks; microseconds on one
+// MI355X, groups of 128 unless named (nb x waves, chunks of one K block):
+//   one row, up to 4 rows: 16 waves on single blocks while those give at most
+//     two workgroups per CU: 4096 x 4096 3.95 (8 waves 4.53, pairs 4.24), 8192 x
+//     28672 22.7 (pairs on 8 waves 23.0); above, pairs on 8 waves: 28672 x 8192
+//     21.4 (21.7), and on 4 waves with chunks of two where 8 would have less
+//     than four K blocks each: 32768 x 2048 8.4 (9.4 on 8 waves, 11.8 on 16);
+//     3 rows, gated, 14336 x 4096 14.1 on fours and 4 waves (pairs on 8 14.5).
+//   more rows: as many blocks per workgroup as still give one workgroup per CU,
+//     since every workgroup reads all of x: 16 rows 16384 x 8192 15.3 on fours
+//     (pairs 18.8, single 25.5), 4091 x 7168 in groups of 64 8.0 on single ones
+//     (pairs 9.5); 32 rows 14336 x 8192 19.0 on fours (25.9, 40.9), 4096 x 4096
+//     7.6 on single ones (8.7); 64 rows 14336 x 8192 33.9 on fours (46.5).
 int plan_w4(int64_t M, const W4Layout& l, bool gated, W4Plan* p) {
-  p->one = M == 1;
-  p->mb = M > 16 ? 2 : 1;
-  p->nb = gated || p->mb > 1 || l.nblk > 512 ? 2 : 1;
-  p->waves = 8;
-  const int64_t wgs = ((l.nblk + p->nb - 1) / p->nb) * ((M + 16 * p->mb - 1) / (16 * p->mb));
+  p->xl = M == 1 ? 0 : M <= 4 ? 1 : M <= 16 ? 4 : M <= 32 ? 8 : 16;
+  if (p->xl <= 1) {
+    const bool many = l.nblk > 512;
+    p->nb = gated || many ? 2 : 1;
+    p->waves = many ? 8 : 16;
+    if (many && p->xl == 1) {
+      p->nb = 4;
+      p->waves = 4;
+    } else if (many && l.kblk < 32) {
+      p->waves = 4;
+      p->s = 2;
+    }
+  } else {
+    p->nb = l.nblk >= 1024 || (p->xl > 4 && l.nblk >= 768) ? 4 : gated || l.nblk >= 512 ? 2 : 1;
+    p->waves = p->xl == 16 && p->nb > 1 ? 4 : 8;
+  }
+  const int64_t rows = p->xl == 0 ? 1 : 4 * p->xl;
+  const int64_t wgs = ((l.nblk + p->nb - 1) / p->nb) * ((M + rows - 1) / rows);
   if (wgs * p->waves * 64 >= (int64_t)1 << 32) return GP_ESHAPE;
   return GP_OK;
 }
@@ -130,8 +154,8 @@ int run_w4(int dtype, const void* x, const void* w_shuf, bool zeros, const float
   a.act = act;
   a.gated = gated ? 1 : 0;
   forget_hip_error();
-  return report_hip(dtype == GP_BF16 ? launch_w4_bf16(p, l.sg, a, stream) : launch_w4_f16(p, l.sg, a, stream),
-                    "kernel launch");
+  auto* launch = dtype == GP_BF16 ? (zeros ? launch_w4_bf16_z : launch_w4_bf16) : (zeros ? launch_w4_f16_z : launch_w4_f16);
+  return report_hip(launch(p, l.sg, a, stream), "kernel launch");
 }
 
 }  // namespace

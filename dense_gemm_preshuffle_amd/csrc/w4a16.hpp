@@ -11,16 +11,15 @@
 //   y += s * sum_group x (q - z).
 // A nibble u = q + 8 in 0 .. 15, read as an FP8 E4M3 code, is the number
 // u * 2^-9 (codes below 8 are the subnormals, 8 .. 15 the first binade), so one
-// conversion instruction with the scale 2^9 makes two operands.
-//   FP16: u is converted and 8 + z subtracted, exactly, on packed halves.
-//   BF16 has no packed subtract: the MFMA takes u itself, and the group's sum
-//     of x times (8 + z) is subtracted in fp32 before the scale. The sum of x
-//     comes from one more MFMA against ones, whose result stands in the lanes
-//     that need it and which serves every column block. The subtraction
-//     loses at most a few fp32 steps of a sum of at most 16 |x| per element,
-//     far below the output's rounding. Where x holds infinities (or the sums
-//     overflow) it gives NaN; such outputs are computed again, one by one, from
-//     the formula.
+// conversion instruction with the scale 2^9 makes two operands: 7 instructions
+// for 8 weights, which matters since the vector unit has about 80 instruction
+// slots per KiB of weights at the full HBM rate. The 8 is taken off by the matrix
+// instructions: a group's accumulator starts from sum x (-8), a product with a
+// constant operand whose result serves every column block; a zero point adds
+// z/8 of the same sum. What cancels there is at most 23 |x| per element
+// (16 |x| + |z| |x| with zero points) in fp32, far below the output's rounding.
+// Where x holds infinities, or the sums overflow, no finite number comes out;
+// such outputs are computed again, one by one, from the formula.
 //
 // Layout: 16 output columns x 128 K per block of 1 KiB. Lane l of a wave reads
 // its 16 bytes at 16 l: column l % 16, K piece l / 16; dword j holds the eight
@@ -31,7 +30,11 @@
 //
 // A workgroup owns NB column blocks and up to 16 MB rows; its waves split K in
 // whole blocks, each with two chunks of S blocks in flight, and their sums meet
-// in LDS in wave order (the same bits on every run).
+// in LDS in wave order (the same bits on every run). x comes row by row, 256
+// contiguous bytes for 16 lanes, and passes through a piece of LDS of the
+// wave's own (no barrier) to the MFMA's layout: read from memory in that layout
+// each of the 64 lanes touches another line of x, and the rows' loads took as
+// long as the weights' (16 x 4091 x 7168: 10.3 us).
 #pragma once
 
 #include "gp_common.hpp"
@@ -52,13 +55,9 @@ struct W4Args {
   int gated;           // gate and up blocks alternate
 };
 
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-
-// Eight nibbles -> eight 16-bit operands. BF16: u = q + 8. FP16: u + off
-// (off = -(8 + z) in both halves).
+// Eight nibbles u = q + 8 -> eight 16-bit operands.
 template <int DT>
-__device__ __forceinline__ v4i unpack_w4(int d, v2h off) {
+__device__ __forceinline__ v4i unpack_w4(int d) {
   const int lo = d & 0x0F0F0F0F, hi = (int)((uint32_t)d >> 4) & 0x0F0F0F0F;
   v4i o;
   if constexpr (DT == DT_BF16) {
@@ -67,14 +66,10 @@ __device__ __forceinline__ v4i unpack_w4(int d, v2h off) {
     o[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false));
     o[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true));
   } else {
-    const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.f, false);
-    const v2h b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.f, true);
-    const v2h c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.f, false);
-    const v2h e = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.f, true);
-    o[0] = __builtin_bit_cast(int, (v2h)(a + off));
-    o[1] = __builtin_bit_cast(int, (v2h)(b + off));
-    o[2] = __builtin_bit_cast(int, (v2h)(c + off));
-    o[3] = __builtin_bit_cast(int, (v2h)(e + off));
+    o[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.f, false));
+    o[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.f, true));
+    o[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.f, false));
+    o[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.f, true));
   }
   return o;
 }
@@ -104,14 +99,18 @@ __device__ __forceinline__ float w4_direct(const W4Args& p, uint32_t m, uint32_t
   return sum;
 }
 
-// ONE: a single row (M = 1): only the first result register of a block counts.
-template <int DT, int MB, int NB, int WAVES, int S, int SG, bool ZERO, bool ONE>
+// XL: 16-byte loads of x per lane and block: 1, 4, 8 or 16 serve 4, 16, 32 or
+// 64 rows; 0: a single row, one dword per lane.
+template <int DT, int XL, int NB, int WAVES, int S, int SG, bool ZERO>
 __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
+  constexpr bool ONE = XL == 0;
+  constexpr int ROWS = ONE ? 1 : 4 * XL;
+  constexpr int MB = (ROWS + 15) / 16;
   constexpr int NQ = MB * NB;
-  constexpr int R = ONE ? 1 : 4;
+  constexpr int R = ONE ? 1 : 4;        // result registers that hold rows
   constexpr int STEPS = 4 / SG;         // K steps of 32 per scale inside a block
-  static_assert(!ONE || MB == 1, "one row");
-  static_assert(WAVES * NQ * 64 * R * 4 <= 160 * 1024, "LDS budget");
+  static_assert(WAVES * (ROWS * 256 + NQ * 64 * R * 4) <= 160 * 1024, "LDS budget");
+  __shared__ __attribute__((aligned(16))) char xs[WAVES * ROWS * 256];
   __shared__ __attribute__((aligned(16))) float red[WAVES * NQ * 64 * R];
 
   const int tid = threadIdx.x;
@@ -124,23 +123,26 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
   if (cols % 8u == 0) bx = (bx % 8u) * (cols / 8u) + bx / 8u;   // a contiguous run of columns per XCD
   const uint32_t nb0 = bx * NB;
   const uint32_t nreal = min((uint32_t)NB, p.nblk - nb0);
-  const uint32_t m0 = blockIdx.x / cols * (16 * MB);
-  const uint32_t mrows = min(16u * MB, p.M - m0);
+  const uint32_t m0 = blockIdx.x / cols * ROWS;
+  const uint32_t mrows = min((uint32_t)ROWS, p.M - m0);
   const uint32_t kb0 = (uint32_t)((uint64_t)wave * kblk / WAVES), kb1 = (uint32_t)((uint64_t)(wave + 1) * kblk / WAVES);
   const int chunks = (int)((kb1 - kb0 + S - 1) / S);
 
+  // rows past M and column blocks past the last lie outside their resources
   constexpr uint32_t kOOB = 0x80000000u;
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + (size_t)m0 * Kb, mrows * Kb);
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w + (size_t)nb0 * kblk * 1024, nreal * kblk * 1024);
   const __amdgpu_buffer_rsrc_t rs = make_rsrc(p.s + (size_t)nb0 * sblk * (32 * SG), nreal * sblk * (32 * SG));
   const __amdgpu_buffer_rsrc_t rz =
       make_rsrc(ZERO ? p.z + (size_t)nb0 * sblk * (16 * SG) : nullptr, ZERO ? nreal * sblk * (16 * SG) : 0);
-  // rows past the last read it again (their results are not stored)
-  uint32_t x_off[MB];
-#pragma unroll
-  for (int mb = 0; mb < MB; ++mb) x_off[mb] = min((uint32_t)(mb * 16 + lane_lo), mrows - 1) * Kb + lane_hi * 16;
+  // x: load i of a lane is 16-byte piece lane % 16 of row 4 i + lane / 16. In
+  // LDS piece c of row m stands at c ^ (m % 16), so that the 16 rows of one
+  // piece, which an MFMA operand reads together, lie in different banks.
+  char* xw = xs + wave * ROWS * 256;
+  const uint32_t xcol = ONE ? 4 * lane : 16 * lane_lo;
+  const uint32_t x_off = (ONE ? 0 : lane_hi * Kb) + xcol;
 
-  v4i xf[2][S][4][MB], wf[2][S][NB];
+  v4i xr[2][S][XL > 0 ? XL : 1], wf[2][S][NB];
   uint32_t sf[2][S][NB][SG == 4 ? 2 : 1], zf[2][S][NB];
   v4f acc[MB][NB];
 #pragma unroll
@@ -148,78 +150,99 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = v4f{0.f, 0.f, 0.f, 0.f};
 
+  // The block's offset is scalar; bounds are checked on the lane's part alone,
+  // so what lies past the share of a wave (S > 1) or past K gets a lane offset
+  // outside the resource.
   auto load = [&](auto par_c, int ch) GP_INLINE {
     constexpr int par = decltype(par_c)::value;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const uint32_t b = kb0 + (uint32_t)ch * S + s;
-      const uint32_t skip = b < kb1 ? 0u : kOOB;   // uniform: past the wave's share
+      const uint32_t skip = S == 1 || b < kb1 ? 0u : kOOB;
+      const uint32_t xo = (256 * b + xcol < Kb ? x_off : kOOB) | skip;
+      if constexpr (ONE) xr[par][s][0][0] = buf_load4(rx, xo, 256 * b);
+#pragma unroll
+      for (int i = 0; i < XL; ++i) xr[par][s][i] = buf_load16(rx, xo + 4 * i * Kb, 256 * b);
+      const uint32_t g = (b >> p.sshift) * 16 * SG;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        wf[par][s][nb] = buf_load16_nt(rw, ((nb * kblk + b) * 1024 + lane * 16) | skip, 0);
-        const uint32_t g = ((nb * sblk + (b >> p.sshift)) * 16 + lane_lo) * SG;
-        if constexpr (SG == 1) sf[par][s][nb][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, (g * 2) | skip, 0, 0);
-        else if constexpr (SG == 2) sf[par][s][nb][0] = buf_load4(rs, (g * 2) | skip, 0);
+        wf[par][s][nb] = buf_load16_nt(rw, (nb * kblk * 1024 + lane * 16) | skip, b * 1024);
+        const uint32_t go = (nb * sblk * 16 + lane_lo) * SG;
+        if constexpr (SG == 1) sf[par][s][nb][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, (go * 2) | skip, g * 2, 0);
+        else if constexpr (SG == 2) sf[par][s][nb][0] = buf_load4(rs, (go * 2) | skip, g * 2);
         else {
-          const v2i t = buf_load8(rs, (g * 2) | skip, 0);
+          const v2i t = buf_load8(rs, (go * 2) | skip, g * 2);
           sf[par][s][nb][0] = (uint32_t)t[0];
           sf[par][s][nb][1] = (uint32_t)t[1];
         }
         if constexpr (ZERO) {
-          if constexpr (SG == 1) zf[par][s][nb] = __builtin_amdgcn_raw_buffer_load_b8(rz, g | skip, 0, 0);
-          else if constexpr (SG == 2) zf[par][s][nb] = __builtin_amdgcn_raw_buffer_load_b16(rz, g | skip, 0, 0);
-          else zf[par][s][nb] = buf_load4(rz, g | skip, 0);
+          if constexpr (SG == 1) zf[par][s][nb] = __builtin_amdgcn_raw_buffer_load_b8(rz, go | skip, g, 0);
+          else if constexpr (SG == 2) zf[par][s][nb] = __builtin_amdgcn_raw_buffer_load_b16(rz, go | skip, g, 0);
+          else zf[par][s][nb] = buf_load4(rz, go | skip, g);
         }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // K is whole steps of 32, not whole blocks
-        const uint32_t off = 256 * b + 64 * j, xskip = (b < kb1 && off < Kb) ? 0u : kOOB;
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb) xf[par][s][j][mb] = buf_load16(rx, (x_off[mb] + off) | xskip, 0);
       }
     }
   };
-  const v4i ones = v4i{0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
+  constexpr int kM8 = DT == DT_BF16 ? (int)0xC100C100 : (int)0xC800C800;
+  const v4i minus8 = v4i{kM8, kM8, kM8, kM8};
   auto compute = [&](auto par_c) GP_INLINE {
     constexpr int par = decltype(par_c)::value;
     static_for<0, S>([&](auto s_c) GP_INLINE {
       constexpr int s = decltype(s_c)::value;
+      if constexpr (ONE) *(int*)(xw + 4 * lane) = xr[par][s][0][0];
+#pragma unroll
+      for (int i = 0; i < XL; ++i) {
+        const int m = 4 * i + lane_hi;
+        *(v4i*)(xw + m * 256 + ((lane_lo ^ (m & 15)) * 16)) = xr[par][s][i];
+      }
+      int xg = 0;
       static_for<0, SG>([&](auto g_c) GP_INLINE {
         constexpr int g = decltype(g_c)::value;
-        v4f sum[MB];
-        if constexpr (DT == DT_BF16)
+        // rows past ROWS (a single row, or four) repeat; their results are not stored
+        v4i xf[STEPS][MB];
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j)
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb) {
-            sum[mb] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) sum[mb] = mfma<DT>(&xf[par][s][j][mb], &ones, sum[mb]);
+            const int c = 4 * (g * STEPS + j) + lane_hi;
+            const int m = ONE ? 0 : (mb * 16 + lane_lo) % ROWS;
+            xf[j][mb] = *(const v4i*)(xw + xg + m * 256 + ((c ^ (m & 15)) * 16));
           }
+        v4f sum[MB];   // -8 times the sum of x
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          sum[mb] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < STEPS; ++j) sum[mb] = mfma<DT>(&xf[j][mb], &minus8, sum[mb]);
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const uint32_t sw = sf[par][s][nb][g / 2];
           const float sc = half_to_float<DT>(SG == 1 ? sw : (g % 2 ? sw >> 16 : sw & 0xFFFFu));
-          const int off = ZERO ? 8 + (int)(int8_t)(zf[par][s][nb] >> (8 * g)) : 8;
-          v2h hoff;
-          if constexpr (DT == DT_F16) hoff[0] = hoff[1] = (_Float16)(-off);
+          const float z8 = ZERO ? 0.125f * (float)(int)(int8_t)(zf[par][s][nb] >> (8 * g)) : 0.f;
           v4f part[MB];
 #pragma unroll
-          for (int mb = 0; mb < MB; ++mb) part[mb] = v4f{0.f, 0.f, 0.f, 0.f};
+          for (int mb = 0; mb < MB; ++mb) part[mb] = sum[mb];
 #pragma unroll
-          for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
-            const v4i wv = unpack_w4<DT>(wf[par][s][nb][j], hoff);
+          for (int j = 0; j < STEPS; ++j) {
+            const v4i wv = unpack_w4<DT>(wf[par][s][nb][g * STEPS + j]);
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb) part[mb] = mfma<DT>(&xf[par][s][j][mb], &wv, part[mb]);
+            for (int mb = 0; mb < MB; ++mb) part[mb] = mfma<DT>(&xf[j][mb], &wv, part[mb]);
           }
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-              float t = part[mb][r];
-              if constexpr (DT == DT_BF16) t = fmaf(-(float)off, sum[mb][r], t);
-              acc[mb][nb][r] = fmaf(sc, t, acc[mb][nb][r]);
-            }
+            for (int r = 0; r < R; ++r)
+              acc[mb][nb][r] = fmaf(sc, ZERO ? fmaf(z8, sum[mb][r], part[mb][r]) : part[mb][r], acc[mb][nb][r]);
         }
+        // Left free, the compiler interleaves the groups of many rows until
+        // their operands no longer fit the registers: the next group's LDS
+        // address is made to depend on this group's results.
+        if constexpr (MB > 1 && SG > 1)
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) asm volatile("" : "+v"(xg), "+v"(acc[mb][nb]));
       });
     });
   };
@@ -245,41 +268,27 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
       for (int r = 0; r < R; ++r) red[((wave * NQ + mb * NB + nb) * R + r) * 64 + lane] = acc[mb][nb][r];
   __syncthreads();
 
-  // output blocks of the workgroup: row block mb, column block(s) c
+  // one wave per output block (row block mb, column block or pair c) and result
+  // register r
   const int per = p.gated ? NB / 2 : NB;
-  for (int q = wave; q < MB * per; q += WAVES) {
-    const int mb = q / per, c = q % per, b0 = p.gated ? 2 * c : c;
+  for (int q = wave; q < MB * per * R; q += WAVES) {
+    const int r = q % R, c = q / R % per, mb = q / R / per, b0 = p.gated ? 2 * c : c;
     const uint32_t nb = nb0 + b0;
-    if (nb >= p.nblk) continue;
-    auto total = [&](int blk, float* v) GP_INLINE {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float t = 0.f;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) t += red[((w * NQ + mb * NB + blk) * R + r) * 64 + lane];
-        v[r] = t;
-      }
-    };
-    float v[R], u[R];
-    total(b0, v);
-    if (p.gated) total(b0 + 1, u);
     const uint32_t n = (p.gated ? nb / 2 : nb) * 16 + lane_lo;
-    if (n >= p.N) continue;
-    const float bias = p.bias ? p.bias[n] : 0.f;
+    const uint32_t row = mb * 16 + 4 * lane_hi + r;
+    if (nb >= p.nblk || n >= p.N || row >= mrows) continue;
+    auto total = [&](int blk) GP_INLINE {
+      float t = 0.f;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint32_t row = mb * 16 + 4 * lane_hi + r;
-      if (row >= mrows) continue;
-      if constexpr (DT == DT_BF16) {
-        if (v[r] != v[r]) v[r] = w4_direct<DT, SG>(p, m0 + row, nb, lane_lo);
-        if (p.gated && u[r] != u[r]) u[r] = w4_direct<DT, SG>(p, m0 + row, nb + 1, lane_lo);
-      }
-      float o = 0.f;
-      with_act(p.act, [&](auto act_c) GP_INLINE { o = activate<decltype(act_c)::value>(v[r] + bias); });
-      if (p.gated) o *= u[r];
-      const uint32_t two = DT == DT_F16 ? pack_f16x2(o, 0.f) : pack_bf16x2(o, 0.f);
-      *(uint16_t*)(p.y + ((size_t)(m0 + row) * p.N + n) * 2) = (uint16_t)two;
-    }
+      for (int w = 0; w < WAVES; ++w) t += red[((w * NQ + mb * NB + blk) * R + r) * 64 + lane];
+      if (!(fabsf(t) <= 3.402823466e38f)) t = w4_direct<DT, SG>(p, m0 + row, nb0 + blk, lane_lo);
+      return t;
+    };
+    float o = total(b0) + (p.bias ? p.bias[n] : 0.f);
+    with_act(p.act, [&](auto act_c) GP_INLINE { o = activate<decltype(act_c)::value>(o); });
+    if (p.gated) o *= total(b0 + 1);
+    const uint32_t two = DT == DT_F16 ? pack_f16x2(o, 0.f) : pack_bf16x2(o, 0.f);
+    *(uint16_t*)(p.y + ((size_t)(m0 + row) * p.N + n) * 2) = (uint16_t)two;
   }
 }
 

@@ -446,7 +446,7 @@ int gemm_w4a16_preshuffle(int dtype, const void* q, const void* scales, const in
  *   w_shuf, has_zeros, group  as laid out (gated 0).
  *   bias                      device fp32 [N], or NULL.
  * All device pointers 16-byte aligned (GP_EINVAL). The same call gives the
- * same bits. Any M is served, more than 32 rows in blocks that read the
+ * same bits. Any M is served, more than 64 rows in blocks that read the
  * weights again.
  */
 int gemm_w4a16(int dtype, const void* x, const void* w_shuf, int has_zeros, const float* bias, int act, void* y,
