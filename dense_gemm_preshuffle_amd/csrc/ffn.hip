@@ -30,7 +30,7 @@ __global__ __launch_bounds__(256) void preshuffle_gated_kernel(const char* __res
 // ---- gated product ----
 struct GatedPlan {
   bool small = false;   // gated_small_kernel, else the tile kernel
-  int mb = 1, waves = 4;
+  GatedSmall variant;
   Plan tile;
 };
 
@@ -47,6 +47,15 @@ int check_gated(int dtype, int64_t M, int64_t F, int64_t H) {
 // kernel for [M][2F] outputs, the small gated kernel; otherwise the planner's
 // tile (every one it picks for these types has the gated epilogue, except the
 // 16-column waves of 16 x 64, a small-M shape).
+// Variants of the small kernel, F x H of 14336 x 4096 (896 pairs of column
+// blocks), 7184 x 4096 (449) and 4096 x 4096 (256) unless named, us on one
+// MI355X: up to 16 rows single pairs on 8 waves (1 x 7168 x 2048 10.8, pairs by
+// two 11.4); 32 rows two pairs on 4 waves from 512 pairs on, 39.2 against 45.2
+// on single ones, below single ones (256 pairs 15.0 against 21.2); 48 rows two
+// pairs on 4 waves 42.9 (on 8 waves 46.0), below 512 pairs on 8 waves (37 rows,
+// 449 pairs: 26.2, on 4 waves 27.4, single 27.9), below 384 single ones (18.4
+// against 23.5); 64 rows four pairs 45.0 (two 49.1), below 768 two (7168 x 2048
+// 16.5, single 17.8), below 384 single (20.4 against 24.9).
 int plan_gated(int dtype, int64_t M, int64_t F, int64_t H, GatedPlan* p) {
   const int r = check_gated(dtype, M, F, H);
   if (r) return r;
@@ -56,8 +65,12 @@ int plan_gated(int dtype, int64_t M, int64_t F, int64_t H, GatedPlan* p) {
     p->small = rc != GP_OK || p->tile.kernel != GP_KERNEL_TILE || p->tile.tn < 128;
   }
   if (p->small) {
-    p->mb = M > 32 ? 4 : M > 16 ? 2 : 1;
-    p->waves = 8;
+    GatedSmall& v = p->variant;
+    const int64_t pairs = F / 16;
+    v.xl = M == 1 ? 0 : M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : M <= 48 ? 6 : 8;
+    v.s = v.xl <= 2 || (v.xl == 4 && pairs < 512) ? 2 : 1;
+    v.pairs = v.xl <= 2 ? 1 : v.xl == 4 ? (pairs >= 512 ? 2 : 1) : v.xl == 8 && pairs >= 768 ? 4 : pairs >= 384 ? 2 : 1;
+    v.waves = v.xl <= 2 || (v.xl == 6 && v.pairs == 2 && pairs < 512) ? 8 : 4;
   }
   return GP_OK;
 }
@@ -230,7 +243,7 @@ int gemm_gated(int dtype, const void* x, const void* w_shuf, int act, void* h, v
     t.F = (uint32_t)F;
     t.Kb = (uint32_t)(2 * H);
     t.act = act;
-    e = dtype == GP_BF16 ? launch_gated_small_bf16(p.mb, p.waves, t, s) : launch_gated_small_f16(p.mb, p.waves, t, s);
+    e = dtype == GP_BF16 ? launch_gated_small_bf16(p.variant, t, s) : launch_gated_small_f16(p.variant, t, s);
   } else {
     TileArgs t;
     t.a = (const char*)x;

@@ -4,12 +4,15 @@
 //
 // B is the preshuffled gated layout: 16-column blocks alternate between gate
 // and up rows, so the P pairs of blocks a workgroup owns give it whole output
-// columns. Its WAVES waves split K in 64-byte blocks (in shares that differ by
-// at most one block, so that any K does), every wave keeps two chunks of S
-// blocks in flight, and the partial sums meet in LDS in wave order (the result
-// is the same on every run). Wave q < MB * P then joins gate and up of output
-// block q and stores it. A chunk that runs past the wave's share loads zeros
-// (an offset outside the buffer resource), which add nothing.
+// columns. Its WAVES waves split K in chunks of 64 elements (in shares that
+// differ by at most one, so that any K does), every wave keeps two groups of S
+// chunks in flight, and the partial sums meet in LDS in wave order (the result
+// is the same on every run), where a wave per output block joins gate and up
+// and stores it. x comes row by row, 128 contiguous bytes for 8 lanes,
+// and passes through a piece of LDS of the wave's own (no barrier) to the MFMA's
+// layout: read from memory in that layout each lane touches another line. What
+// lies past K or the wave's share is loaded as zeros (an offset outside the
+// buffer resource), which add nothing.
 #pragma once
 
 #include "gp_common.hpp"
@@ -26,13 +29,18 @@ struct GatedArgs {
   int act;            // Act
 };
 
-template <int DT, int MB, int P, int WAVES, int S>
+// XL: 16-byte loads of x per lane and chunk: 8 XL rows; 0: a single row.
+template <int DT, int XL, int P, int WAVES, int S>
 __global__ __launch_bounds__(WAVES * 64) void gated_small_kernel(GatedArgs p) {
+  constexpr bool ONE = XL == 0;
+  constexpr int ROWS = ONE ? 1 : 8 * XL;
+  constexpr int MB = (ROWS + 15) / 16;
   constexpr int NB = 2 * P;          // 16-column blocks of B per workgroup
   constexpr int NQ = MB * NB;        // 16 x 16 partial blocks per wave
-  static_assert(MB * P <= WAVES, "one output block per wave in the epilogue");
-  static_assert(WAVES * NQ * 1024 <= 160 * 1024, "LDS budget");
-  __shared__ __attribute__((aligned(16))) v4f red[WAVES * NQ * 64];
+  constexpr int XW = (ONE ? 2 : ROWS) * 128;   // LDS bytes of a wave's x (ONE: the idle lanes write past the row)
+  constexpr int LDS = WAVES * (XW > NQ * 1024 ? XW : NQ * 1024);
+  static_assert(LDS <= 160 * 1024, "LDS budget");
+  __shared__ __attribute__((aligned(16))) char lds[LDS];
 
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -44,87 +52,114 @@ __global__ __launch_bounds__(WAVES * 64) void gated_small_kernel(GatedArgs p) {
   if (cols % 8u == 0) bx = (bx % 8u) * (cols / 8u) + bx / 8u;
   const uint32_t pair0 = bx * P;
   const uint32_t npair = min((uint32_t)P, pairs - pair0);   // real pairs of this workgroup
-  const uint32_t m0 = blockIdx.x / cols * (16 * MB);
-  const uint32_t mrows = min(16u * MB, p.M - m0);
-  const uint32_t nblk = Kb / 64;
-  const uint32_t kb0 = (uint32_t)wave * nblk / WAVES, kb1 = (uint32_t)(wave + 1) * nblk / WAVES;
-  const int chunks = (int)((kb1 - kb0 + S - 1) / S);
+  const uint32_t m0 = blockIdx.x / cols * ROWS;
+  const uint32_t mrows = min((uint32_t)ROWS, p.M - m0);
+  const uint32_t nchunk = (Kb + 127) / 128;
+  const uint32_t kc0 = (uint32_t)wave * nchunk / WAVES, kc1 = (uint32_t)(wave + 1) * nchunk / WAVES;
+  const int groups = (int)((kc1 - kc0 + S - 1) / S);
 
   // rows past M and blocks past the last pair lie outside their resources
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + (size_t)m0 * Kb, mrows * Kb);
   const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.b + (size_t)pair0 * 32 * Kb, npair * 32 * Kb);
-  const uint32_t a_off = lane_lo * Kb + lane_hi * 16;
   constexpr uint32_t kOOB = 0x80000000u;
+  // x load i of a lane: 16-byte piece lane % 8 of row 8 i + lane / 8. Piece c of
+  // row m stands in LDS at c ^ (m / 2 % 8): the 16 rows of one piece, which an
+  // MFMA operand reads together, lie in different banks.
+  char* xw = lds + wave * XW;
+  const uint32_t xcol = ONE ? 4 * lane : 16 * (lane & 7);
+  const uint32_t x_off = ONE ? (lane < 32 ? xcol : kOOB) : (lane >> 3) * Kb + xcol;
 
-  v4i af[2][S][MB], bf[2][S][NB];
+  v4i xr[2][S][XL > 0 ? XL : 1], bf[2][S][2][NB];
   v4f acc[MB][NB];
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  auto load = [&](auto par_c, int ch) GP_INLINE {
+  // the chunk's offset is scalar; bounds are checked on the lane's part alone
+  auto load = [&](auto par_c, int gr) GP_INLINE {
     constexpr int par = decltype(par_c)::value;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const uint32_t k = kb0 + (uint32_t)ch * S + s;
-      const uint32_t skip = k < kb1 ? 0u : kOOB;   // uniform
+      const uint32_t k = kc0 + (uint32_t)gr * S + s;
+      const uint32_t skip = S == 1 || k < kc1 ? 0u : kOOB;   // uniform
+      const uint32_t skip1 = (S == 1 || k < kc1) && 128 * k + 64 < Kb ? 0u : kOOB;   // second half past K
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-        bf[par][s][nb] = buf_load16_nt(rb, (nb * 16 * Kb + k * 1024 + lane * 16) | skip, 0);
+      for (int nb = 0; nb < NB; ++nb) {
+        bf[par][s][0][nb] = buf_load16_nt(rb, (nb * 16 * Kb + lane * 16) | skip, k * 2048);
+        bf[par][s][1][nb] = buf_load16_nt(rb, (nb * 16 * Kb + lane * 16 + 1024) | skip1, k * 2048);
+      }
+      const uint32_t xo = (128 * k + xcol < Kb ? x_off : kOOB) | skip;
+      if constexpr (ONE) xr[par][s][0][0] = buf_load4(ra, xo, 128 * k);
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) af[par][s][mb] = buf_load16(ra, (a_off + mb * 16 * Kb + k * 64) | skip, 0);
+      for (int i = 0; i < XL; ++i) xr[par][s][i] = buf_load16(ra, xo + 8 * i * Kb, 128 * k);
     }
   };
   auto compute = [&](auto par_c) GP_INLINE {
     constexpr int par = decltype(par_c)::value;
 #pragma unroll
-    for (int s = 0; s < S; ++s)
+    for (int s = 0; s < S; ++s) {
+      if constexpr (ONE) *(int*)(xw + 4 * lane) = xr[par][s][0][0];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int i = 0; i < XL; ++i) {
+        const int m = 8 * i + (lane >> 3);
+        *(v4i*)(xw + m * 128 + (((lane & 7) ^ ((m >> 1) & 7)) * 16)) = xr[par][s][i];
+      }
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) acc[mb][nb] = mfma<DT>(&bf[par][s][nb], &af[par][s][mb], acc[mb][nb]);
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          const int m = ONE ? 0 : (mb * 16 + lane_lo) % ROWS;   // rows past ROWS repeat and are not stored
+          const v4i xf = *(const v4i*)(xw + m * 128 + (((4 * t + lane_hi) ^ ((m >> 1) & 7)) * 16));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = mfma<DT>(&bf[par][s][t][nb], &xf, acc[mb][nb]);
+        }
+    }
   };
   using P0 = std::integral_constant<int, 0>;
   using P1 = std::integral_constant<int, 1>;
-  load(P0{}, 0);
-  int ch = 0;
-  for (; ch + 2 <= chunks; ch += 2) {
-    load(P1{}, ch + 1);
-    compute(P0{});
-    if (ch + 2 < chunks) load(P0{}, ch + 2);
-    compute(P1{});
+  if (groups > 0) {
+    load(P0{}, 0);
+    int gr = 0;
+    for (; gr + 2 <= groups; gr += 2) {
+      load(P1{}, gr + 1);
+      compute(P0{});
+      if (gr + 2 < groups) load(P0{}, gr + 2);
+      compute(P1{});
+    }
+    if (gr < groups) compute(P0{});
   }
-  if (ch < chunks) compute(P0{});
 
+  __syncthreads();   // the sums take the place of the waves' x
+  v4f* red = (v4f*)lds;
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) red[(wave * NQ + mb * NB + nb) * 64 + lane] = acc[mb][nb];
   __syncthreads();
-  if (wave >= MB * P) return;
-  // this wave's output block: rows mb * 16 + lane_lo, columns pr * 16 + 4 * lane_hi + 0..3
-  const uint32_t mb = (uint32_t)wave / P, pr = (uint32_t)wave % P;
-  if (pr >= npair) return;
-  v4f g = red[(mb * NB + 2 * pr) * 64 + lane], u = red[(mb * NB + 2 * pr + 1) * 64 + lane];
+  // an output block per wave and turn: rows mb * 16 + lane_lo, columns
+  // pr * 16 + 4 * lane_hi + 0..3
+  for (uint32_t q = (uint32_t)wave; q < MB * P; q += WAVES) {
+    const uint32_t mb = q / P, pr = q % P, row = mb * 16 + lane_lo;
+    if (pr >= npair || row >= mrows) continue;
+    v4f g = red[(mb * NB + 2 * pr) * 64 + lane], u = red[(mb * NB + 2 * pr + 1) * 64 + lane];
 #pragma unroll
-  for (int w = 1; w < WAVES; ++w) {
-    g += red[(w * NQ + mb * NB + 2 * pr) * 64 + lane];
-    u += red[(w * NQ + mb * NB + 2 * pr + 1) * 64 + lane];
-  }
-  const uint32_t row = mb * 16 + lane_lo;
-  if (row >= mrows) return;
-  const size_t off = ((size_t)(m0 + row) * p.F + (pair0 + pr) * 16 + 4 * lane_hi) * 2;
-  v4f h;
-  with_act(p.act, [&](auto act_c) GP_INLINE {
-    constexpr int A = decltype(act_c)::value;
+    for (int w = 1; w < WAVES; ++w) {
+      g += red[(w * NQ + mb * NB + 2 * pr) * 64 + lane];
+      u += red[(w * NQ + mb * NB + 2 * pr + 1) * 64 + lane];
+    }
+    const size_t off = ((size_t)(m0 + row) * p.F + (pair0 + pr) * 16 + 4 * lane_hi) * 2;
+    v4f h;
+    with_act(p.act, [&](auto act_c) GP_INLINE {
+      constexpr int A = decltype(act_c)::value;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) h[r] = activate<A>(g[r]) * u[r];
-  });
-  *(v2i*)(p.c + off) = pack_out4<DT>(h);
-  if (p.gate) {
-    *(v2i*)(p.gate + off) = pack_out4<DT>(g);
-    *(v2i*)(p.up + off) = pack_out4<DT>(u);
+      for (int r = 0; r < 4; ++r) h[r] = activate<A>(g[r]) * u[r];
+    });
+    *(v2i*)(p.c + off) = pack_out4<DT>(h);
+    if (p.gate) {
+      *(v2i*)(p.gate + off) = pack_out4<DT>(g);
+      *(v2i*)(p.up + off) = pack_out4<DT>(u);
+    }
   }
 }
 

@@ -6,11 +6,17 @@
 
 namespace gp {
 
+// A variant of gated_small_kernel: x loads (0: one row, else rows / 8), column
+// pairs, waves, 64-element K chunks per group.
+struct GatedSmall {
+  int xl = 0, pairs = 1, waves = 8, s = 2;
+};
+
 // Each returns hipErrorInvalidValue if the variant is not compiled.
 hipError_t launch_gated_tile_bf16(int tm, int tn, int tkb, int pipe, const TileArgs& a, hipStream_t s);
 hipError_t launch_gated_tile_f16(int tm, int tn, int tkb, int pipe, const TileArgs& a, hipStream_t s);
-hipError_t launch_gated_small_bf16(int mb, int waves, const GatedArgs& a, hipStream_t s);
-hipError_t launch_gated_small_f16(int mb, int waves, const GatedArgs& a, hipStream_t s);
+hipError_t launch_gated_small_bf16(const GatedSmall& v, const GatedArgs& a, hipStream_t s);
+hipError_t launch_gated_small_f16(const GatedSmall& v, const GatedArgs& a, hipStream_t s);
 
 }  // namespace gp
 
@@ -22,24 +28,30 @@ hipError_t launch_gated_small_f16(int mb, int waves, const GatedArgs& a, hipStre
   }
 #define GP_GATED_CASE(DT, MS, TM, TN, TKB, PIPE) GP_GATED_CASE_IMPL(DT, MS, TM, TN, TKB, PIPE, false)
 #define GP_GATED_CASE_KSPLIT(DT, MS, TM, TN, TKB, PIPE) GP_GATED_CASE_IMPL(DT, MS, TM, TN, TKB, PIPE, true)
-#define GP_GATED_SMALL_CASE(DT, MB, P, W, S)                                                                   \
-  if (mb == MB && waves == W) {                                                                                \
-    const dim3 grid(((a.F / 16 + P - 1) / P) * ((a.M + 16 * MB - 1) / (16 * MB)));                              \
-    hipLaunchKernelGGL((gated_small_kernel<DT, MB, P, W, S>), grid, dim3(W * 64), 0, s, a);                    \
+#define GP_GATED_SMALL_CASE(DT, XL, P, W, S)                                                                   \
+  if (v.xl == XL && v.pairs == P && v.waves == W && v.s == S) {                                                \
+    constexpr uint32_t rows = XL == 0 ? 1 : 8 * XL;                                                            \
+    const dim3 grid(((a.F / 16 + P - 1) / P) * ((a.M + rows - 1) / rows));                                     \
+    hipLaunchKernelGGL((gated_small_kernel<DT, XL, P, W, S>), grid, dim3(W * 64), 0, s, a);                    \
     return hipGetLastError();                                                                                  \
   }
-// (rows / 16, column pairs, waves, 64-byte K blocks per chunk)
 #define GP_DEFINE_GATED(NAME, DT, TILES, KSPLIT)                                                               \
   hipError_t launch_gated_tile_##NAME(int tm, int tn, int tkb, int pipe, const TileArgs& a, hipStream_t s) {   \
     TILES(GP_GATED_CASE)                                                                                       \
     KSPLIT(GP_GATED_CASE_KSPLIT)                                                                               \
     return hipErrorInvalidValue;                                                                               \
   }                                                                                                            \
-  hipError_t launch_gated_small_##NAME(int mb, int waves, const GatedArgs& a, hipStream_t s) {                 \
-    GP_GATED_SMALL_CASE(DT, 1, 1, 4, 4)                                                                        \
-    GP_GATED_SMALL_CASE(DT, 1, 1, 8, 4)                                                                        \
-    GP_GATED_SMALL_CASE(DT, 2, 1, 4, 4)                                                                        \
-    GP_GATED_SMALL_CASE(DT, 2, 1, 8, 4)                                                                        \
-    GP_GATED_SMALL_CASE(DT, 4, 1, 8, 4)                                                                        \
+  hipError_t launch_gated_small_##NAME(const GatedSmall& v, const GatedArgs& a, hipStream_t s) {               \
+    GP_GATED_SMALL_CASE(DT, 0, 1, 8, 2)                                                                        \
+    GP_GATED_SMALL_CASE(DT, 1, 1, 8, 2)                                                                        \
+    GP_GATED_SMALL_CASE(DT, 2, 1, 8, 2)                                                                        \
+    GP_GATED_SMALL_CASE(DT, 4, 1, 4, 2)                                                                        \
+    GP_GATED_SMALL_CASE(DT, 4, 2, 4, 1)                                                                        \
+    GP_GATED_SMALL_CASE(DT, 6, 1, 4, 1)                                                                        \
+    GP_GATED_SMALL_CASE(DT, 6, 2, 8, 1)                                                                        \
+    GP_GATED_SMALL_CASE(DT, 6, 2, 4, 1)                                                                        \
+    GP_GATED_SMALL_CASE(DT, 8, 1, 4, 1)                                                                        \
+    GP_GATED_SMALL_CASE(DT, 8, 2, 4, 1)                                                                        \
+    GP_GATED_SMALL_CASE(DT, 8, 4, 4, 1)                                                                        \
     return hipErrorInvalidValue;                                                                               \
   }
