@@ -628,11 +628,14 @@ class W4Weights:
     """Laid-out 4-bit weights (gemm_w4a16_preshuffle): the device buffer and what it holds.
     N is the number of output columns (gated: F, from 2 F rows)."""
 
-    __slots__ = ("data", "dtype", "N", "K", "group", "has_zeros", "gated")
+    __slots__ = ("data", "dtype", "N", "K", "group", "has_zeros", "gated", "device", "gp_dtype")
 
     def __init__(self, data, dtype, N, K, group, has_zeros, gated):
         self.data, self.dtype, self.N, self.K = data, dtype, N, K
         self.group, self.has_zeros, self.gated = group, has_zeros, gated
+        # read once: a decode step's products take a few microseconds each
+        self.device = data.device
+        self.gp_dtype = next(k for k, v in _HALF.items() if str(dtype) == f"torch.{v}")
 
 
 def gemm_w4a16_weights_size(N: int, K: int, group: int, has_zeros=False, gated=False) -> int:
@@ -665,42 +668,39 @@ def gemm_w4a16_preshuffle(q, scales, zeros=None, group=128, gated=False, out=Non
     return W4Weights(out, scales.dtype, N // 2 if gated else N, K, group, zeros is not None, bool(gated))
 
 
-def _w4_args(where, x, weights, y, gated):
-    """Checks x and the weights of a 4-bit product."""
+def _w4_check(where, x, weights, y, bias, gated):
+    """x, the output and the bias fit the weights."""
     if weights.gated != gated:
         raise ValueError(f"{where}: the weights were laid out {'' if weights.gated else 'not '}gated")
-    M = x.shape[0]
-    _want(f"{where}: x", x, (M, weights.K), weights.dtype, weights.data.device)
+    _want(f"{where}: x", x, (x.shape[0], weights.K), weights.dtype, weights.device)
     if y is not None:
-        _want(f"{where}: output", y, (M, weights.N), weights.dtype, x.device)
-    import torch
+        _want(f"{where}: output", y, (x.shape[0], weights.N), weights.dtype, weights.device)
+    if bias is not None:
+        import torch
 
-    return M, (GP_BF16 if weights.dtype == torch.bfloat16 else GP_F16)
+        _want(f"{where}: bias", bias, (weights.N,), torch.float32, weights.device)
 
 
 def gemm_w4a16(x, weights: W4Weights, bias=None, act="none", y=None, stream=None):
     """y = act(x W^T + bias) on 4-bit weights: x [M, K] of the scales' type, bias fp32 [N] or None."""
-    import torch
-
-    M, dt = _w4_args("gemm_w4a16", x, weights, y, False)
-    if bias is not None:
-        _want("gemm_w4a16: bias", bias, (weights.N,), torch.float32, x.device)
-    with _on(stream, x.device):
-        y = torch.empty(M, weights.N, dtype=x.dtype, device=x.device) if y is None else y
-        _check(load_library().gemm_w4a16(dt, _ptr(x), _ptr(weights.data), int(weights.has_zeros), _ptr(bias),
-                                         _act(act), _ptr(y), M, weights.N, weights.K, weights.group,
-                                         _stream(stream)), "gemm_w4a16")
+    _w4_check("gemm_w4a16", x, weights, y, bias, False)
+    M, N = x.shape[0], weights.N
+    with _on(stream, weights.device):
+        if y is None:
+            y = x.new_empty((M, N))
+        _check(_lib.gemm_w4a16(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros, _ptr(bias),
+                               _act(act), y.data_ptr(), M, N, weights.K, weights.group, _stream(stream)), "gemm_w4a16")
     return y
 
 
 def gemm_w4a16_gated(x, weights: W4Weights, act="silu", h=None, stream=None):
     """h = act(x Wg^T) * (x Wu^T) on 4-bit weights laid out gated: x [M, K] of the scales' type."""
-    import torch
-
-    M, dt = _w4_args("gemm_w4a16_gated", x, weights, h, True)
-    with _on(stream, x.device):
-        h = torch.empty(M, weights.N, dtype=x.dtype, device=x.device) if h is None else h
-        _check(load_library().gemm_w4a16_gated(dt, _ptr(x), _ptr(weights.data), int(weights.has_zeros), _act(act),
-                                               _ptr(h), M, weights.N, weights.K, weights.group, _stream(stream)),
+    _w4_check("gemm_w4a16_gated", x, weights, h, None, True)
+    M, F = x.shape[0], weights.N
+    with _on(stream, weights.device):
+        if h is None:
+            h = x.new_empty((M, F))
+        _check(_lib.gemm_w4a16_gated(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros,
+                                     _act(act), h.data_ptr(), M, F, weights.K, weights.group, _stream(stream)),
                "gemm_w4a16_gated")
     return h

@@ -8,6 +8,7 @@
 #include "../../include/gemm_preshuffle.h"
 #include "host.hpp"
 #include "launch_gated.hpp"
+#include "launch_rows.hpp"
 #include "transpose.hpp"
 
 namespace gp {
@@ -76,15 +77,26 @@ int plan_gated(int dtype, int64_t M, int64_t F, int64_t H, GatedPlan* p) {
 }
 
 // ---- backward pass of a linear layer C[M][N] = A[M][K] B[N][K]^T ----
-// da = dc b: K axis N (gated: padded, since the call makes dc); b transposed
-// into the preshuffled layout.
-// db = dc^T a: K axis M, padded with zeros; dc transposed row-major, a
-// transposed into the preshuffled layout.
+// da = dc b: K axis N (gated: padded, since the call makes dc).
+// db = dc^T a: K axis M, padded with zeros.
+// From 65 to 4095 rows both run on the tile kernel's row-major form: da reads b
+// as it is; db is computed as (a^T dc)^T, which reads dc as it is, from a
+// transposed copy of a (the smaller operand), and is stored transposed.
+// Otherwise they run on the preshuffled kernels, from copies laid out for them:
+// b^T for da, dc^T and a^T for db. The copies cost bandwidth, the row-major
+// products 2 to 14% of the matrix rate, so that the copies pay off with many rows.
+// Gated backward M x F x H in us, row-major against copies: 64 x 1024 x 1024 20.9,
+// 19.6; 130 x 2064 x 2048 35, 43; 512 x 4096 x 4096 102, 121; 1024 x 8192 x 2048
+// 164, 186; 2000 x 7168 x 4096 471, 495; 4096 x 11008 x 4096 1260, 1225; 8192 x
+// 2048 x 2048 276, 264; 8192 x 14336 x 4096 3118, 2999 (copies and the pointwise
+// pass that also writes dc^T: 458 of these; the matrix unit is busy 88% of the
+// products' cycles at the 1.65 GHz that the power limit leaves).
 struct BackwardPlan {
   Plan da, db;
+  bool da_rows = false, db_rows = false;
   int64_t Mp = 0, Np = 0;
   // workspace: counters and partial sums of the two products (one after the
-  // other), then the transposed copies
+  // other), then the copies
   int64_t parts = 0, off_bt = 0, off_at = 0, off_ct = 0, off_d = 0, bytes = 0;
 };
 
@@ -101,6 +113,31 @@ int64_t pad_k(int64_t k) {
   return (k + unit - 1) / unit * unit;
 }
 
+// The planner's tile for [M][K] x [K][N], moved to one that the row-major form
+// has; false if there is none.
+bool plan_rows(int64_t M, int64_t N, int64_t Kb, Plan* p) {
+  if (M < 64 || N < 128 || Kb % 128) return false;   // smallest tile, whole K tiles
+  if (p->kernel != GP_KERNEL_TILE || p->tm < 64) {
+    p->kernel = GP_KERNEL_TILE;
+    p->tm = 64;
+    p->tn = 128;
+    p->ks = 1;
+  } else if (p->tn == 512) {
+    p->tn = 256;
+  }
+  p->tkb = 128;
+  if (p->ks > 1 && !((p->tm == 128 && p->tn == 256) || (p->tm == 64 && p->tn == 128))) p->ks = 1;
+  const int64_t kt = Kb / 128;
+  if (p->tm == 64 && p->tn == 128 && p->ks == 1) {
+    // as the planner: ranges of at least 1024 K elements until the grid fills
+    // the GPU
+    const int64_t tiles = ((M + 63) / 64) * ((N + 127) / 128);
+    while (p->ks < 16 && tiles * p->ks < 256 && kt % (2 * p->ks) == 0 && Kb / (2 * p->ks) >= 2048) p->ks *= 2;
+    if (tiles > kMaxSplitTiles) p->ks = 1;
+  }
+  return kt % p->ks == 0;
+}
+
 // gated: dc itself is made by the call ([M][Np] in the workspace).
 int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, bool gated, BackwardPlan* p) {
   if (M <= 0 || N <= 0 || K <= 0) return GP_EINVAL;
@@ -110,15 +147,21 @@ int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool
   p->Mp = pad_k(M);
   p->Np = gated ? pad_k(N) : N;
   if (!fits(p->Mp, 2 * K) || !fits(p->Np, 2 * K) || !fits(p->Mp, 2 * p->Np)) return GP_ESHAPE;
+  const bool between = M > 64 && M < 4096;
   int r;
   int64_t parts = 0;
   if (want_da) {
     if ((r = plan_gemm(dtype, M, K, p->Np, &p->da))) return r;
+    Plan rows = p->da;
+    if ((p->da_rows = between && plan_rows(M, K, 2 * p->Np, &rows))) p->da = rows;
     parts = std::max(parts, plan_workspace(p->da, M, K));
   }
   if (want_db) {
-    if ((r = plan_gemm(dtype, N, K, p->Mp, &p->db))) return r;
-    parts = std::max(parts, plan_workspace(p->db, N, K));
+    Plan rows;
+    p->db_rows = between && plan_gemm(dtype, K, N, p->Mp, &rows) == GP_OK && plan_rows(K, N, 2 * p->Mp, &rows);
+    if (p->db_rows) p->db = rows;
+    else if ((r = plan_gemm(dtype, N, K, p->Mp, &p->db))) return r;
+    parts = std::max(parts, p->db_rows ? plan_workspace(p->db, K, N) : plan_workspace(p->db, N, K));
   }
   int64_t at = p->parts = align256(parts);
   auto take = [&](int64_t bytes) {
@@ -126,11 +169,11 @@ int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool
     at += align256(bytes);
     return here;
   };
-  p->off_bt = take(want_da ? p->Np * K * 2 : 0);
+  p->off_bt = take(want_da && !p->da_rows ? p->Np * K * 2 : 0);
   p->off_at = take(want_db ? p->Mp * K * 2 : 0);
-  p->off_ct = take(want_db ? p->Mp * N * 2 : 0);
-  p->off_d = take(gated && want_da ? M * p->Np * 2 : 0);
-  p->bytes = at;
+  p->off_ct = take(want_db && !p->db_rows ? p->Mp * N * 2 : 0);
+  p->off_d = take(gated && (want_da || p->db_rows) ? M * p->Np * 2 : 0);
+  p->bytes = std::max<int64_t>(at, 256);   // never none: one rule for every caller
   return GP_OK;
 }
 
@@ -141,12 +184,42 @@ __global__ __launch_bounds__(256) void clear_words_kernel(uint32_t* p, uint32_t 
 
 uint32_t tiles64(int64_t R, int64_t C) { return (uint32_t)(((R + 63) / 64) * ((C + 63) / 64)); }
 
+// a [M][Kb / 2] (K fast) times b [rows][N] row-major, rows <= Kb / 2; c [M][N], or
+// with t [N][M].
+int launch_rows(int dtype, const Plan& p, const void* a, const void* b, void* c, int64_t M, int64_t N, int64_t Kb,
+                int64_t rows, int64_t ldb, bool t, char* ws, hipStream_t s) {
+  TileArgs g;
+  g.a = (const char*)a;
+  g.b = (const char*)b;
+  g.sa = g.sb = nullptr;
+  g.bias = nullptr;
+  g.c = (char*)c;
+  g.M = (uint32_t)M;
+  g.N = (uint32_t)N;
+  g.Kb = (uint32_t)Kb;
+  g.tiles_m = (uint32_t)((M + p.tm - 1) / p.tm);
+  g.tiles_n = (uint32_t)((N + p.tn - 1) / p.tn);
+  g.xcd = 1;
+  g.act = ACT_NONE;
+  g.gate = g.up = nullptr;
+  g.kb_rows = (uint32_t)rows;
+  g.ldb = (uint32_t)(2 * ldb);
+  g.ksplit = (uint32_t)p.ks;
+  g.cnt = p.ks > 1 ? (uint32_t*)ws : nullptr;
+  g.part = p.ks > 1 ? ws + kCounterBytes : nullptr;
+  forget_hip_error();
+  auto* launch = dtype == GP_BF16 ? (t ? launch_rows_t_bf16 : launch_rows_bf16) : (t ? launch_rows_t_f16 : launch_rows_f16);
+  return report_hip(launch(p.tm, p.tn, g, s), "kernel launch");
+}
+
 // Launches, in order, what has to run once the pointers are valid. dc: the
-// output gradient, or (gated) null with its transpose already in the
-// workspace. Stops at the first launch that fails.
+// output gradient, rows of ldc elements; or (gated) d in the workspace, with its
+// transpose already there where the plan reads one. Stops at the first launch
+// that fails.
 int run_backward(int dtype, const BackwardPlan& p, const void* dc, const void* a, const void* b, void* da, void* db,
-                 int64_t M, int64_t N, int64_t K, bool ct_ready, char* ws, hipStream_t s) {
+                 int64_t M, int64_t N, int64_t K, bool gated, char* ws, hipStream_t s) {
   int r;
+  const int64_t ldc = gated ? p.Np : N;
   if (p.parts > 0) {
     // arrival counters of the K splits: cleared here, so that the workspace
     // needs no state from earlier calls
@@ -155,24 +228,24 @@ int run_backward(int dtype, const BackwardPlan& p, const void* dc, const void* a
                        (uint32_t)(kCounterBytes / 4));
     if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
   }
-  if (da) {
+  auto transpose = [&](auto* kernel, const void* src, int64_t off, int64_t R, int64_t C, int64_t Kp) {
     forget_hip_error();
-    hipLaunchKernelGGL(preshuffle_t_kernel, dim3(tiles64(p.Np, K)), dim3(256), 0, s, (const char*)b, ws + p.off_bt,
-                       (uint32_t)N, (uint32_t)K, (uint32_t)p.Np, (uint32_t)((K + 63) / 64));
-    if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
+    hipLaunchKernelGGL(kernel, dim3(tiles64(Kp, C)), dim3(256), 0, s, (const char*)src, ws + off, (uint32_t)R,
+                       (uint32_t)C, (uint32_t)Kp, (uint32_t)((C + 63) / 64));
+    return report_hip(hipGetLastError(), "kernel launch");
+  };
+  if (da && p.da_rows) {
+    if ((r = launch_rows(dtype, p.da, dc, b, da, M, K, 2 * ldc, N, K, false, ws, s))) return r;
+  } else if (da) {
+    if ((r = transpose(preshuffle_t_kernel, b, p.off_bt, N, K, p.Np))) return r;
     if ((r = launch_gemm(dtype, p.da, dc, ws + p.off_bt, da, M, K, ws, s))) return r;
   }
-  if (db) {
-    forget_hip_error();
-    hipLaunchKernelGGL(preshuffle_t_kernel, dim3(tiles64(p.Mp, K)), dim3(256), 0, s, (const char*)a, ws + p.off_at,
-                       (uint32_t)M, (uint32_t)K, (uint32_t)p.Mp, (uint32_t)((K + 63) / 64));
-    if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
-    if (!ct_ready) {
-      forget_hip_error();
-      hipLaunchKernelGGL(transpose_kernel, dim3(tiles64(p.Mp, N)), dim3(256), 0, s, (const char*)dc, ws + p.off_ct,
-                         (uint32_t)M, (uint32_t)N, (uint32_t)p.Mp, (uint32_t)((N + 63) / 64));
-      if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
-    }
+  if (db && p.db_rows) {
+    if ((r = transpose(transpose_kernel, a, p.off_at, M, K, p.Mp))) return r;
+    if ((r = launch_rows(dtype, p.db, ws + p.off_at, dc, db, K, N, 2 * p.Mp, M, ldc, true, ws, s))) return r;
+  } else if (db) {
+    if ((r = transpose(preshuffle_t_kernel, a, p.off_at, M, K, p.Mp))) return r;
+    if (!gated && (r = transpose(transpose_kernel, dc, p.off_ct, M, N, p.Mp))) return r;
     if ((r = launch_gemm(dtype, p.db, ws + p.off_ct, ws + p.off_at, db, N, K, ws, s))) return r;
   }
   return GP_OK;
@@ -260,6 +333,7 @@ int gemm_gated(int dtype, const void* x, const void* w_shuf, int act, void* h, v
     t.act = act;
     t.gate = (char*)gate;
     t.up = (char*)up;
+    t.kb_rows = t.ldb = 0;
     t.ksplit = (uint32_t)p.tile.ks;
     t.cnt = p.tile.ks > 1 ? (uint32_t*)workspace : nullptr;
     t.part = p.tile.ks > 1 ? (char*)workspace + kCounterBytes : nullptr;
@@ -323,8 +397,8 @@ int gemm_gated_backward(int dtype, const void* dh, const void* gate, const void*
   t.dh = (const char*)dh;
   t.gate = (const char*)gate;
   t.up = (const char*)up;
-  t.d = dx ? ws + p.off_d : nullptr;
-  t.dt = dw ? ws + p.off_ct : nullptr;
+  t.d = dx || p.db_rows ? ws + p.off_d : nullptr;
+  t.dt = dw && !p.db_rows ? ws + p.off_ct : nullptr;
   t.M = (uint32_t)M;
   t.F = (uint32_t)F;
   t.Mp = (uint32_t)p.Mp;

@@ -52,6 +52,7 @@ struct TileArgs {
   int act;            // Act
   char* gate;         // EPI_GATED: [M][N/2] gate and up products to keep, or null
   char* up;
+  uint32_t kb_rows, ldb;  // EPI_ROWS: rows of B (K, below 16-bit elements of Kb: the rest are zeros), bytes per row
   // K split across workgroups (tile kernel): ksplit workgroups share each
   // tile, each taking a contiguous range of its K tiles; their partial sums
   // meet in `part` and the last one to finish adds them and stores the tile.
@@ -123,9 +124,11 @@ struct TileCfg {
   static constexpr int ABUF = TM * TKA + (APART ? 16 : 0);   // + a spare slot for idle lanes
   static constexpr int OB = (DT == DT_I8) ? 4 : 2;        // output element bytes
   static constexpr bool FSC = DT == DT_FP8 || DT == DT_I4;  // fp32 row / column scales
-  static constexpr int CCOLS = (EPI == EPI_GATED) ? TN / 2 : TN;   // stored columns
+  static constexpr bool ROWS = EPI == EPI_ROWS || EPI == EPI_ROWS_T;   // B row-major [K][N]
+  static constexpr int CCOLS = (EPI == EPI_GATED) ? TN / 2 : (EPI == EPI_ROWS_T) ? TM : TN;   // stored columns
+  static constexpr int CROWS = (EPI == EPI_ROWS_T) ? TN : TM;   // and rows
   static constexpr int CSTRIDE = CCOLS * OB + 16;         // padded C row in LDS
-  static constexpr int CBYTES = (EPI == EPI_DIRECT) ? 0 : TM * CSTRIDE;
+  static constexpr int CBYTES = (EPI == EPI_DIRECT) ? 0 : CROWS * CSTRIDE;
   static constexpr int SWP = (TKA >= 256) ? 1 : 256 / TKA;  // rows per 256-byte period
   static constexpr int SWM = ((CPR < 16) ? CPR : 16) - 1;   // chunk xor mask
   static constexpr int NSC = (DT == DT_FP4) ? 1 : 0;
@@ -201,7 +204,8 @@ struct TileCfg {
   // stops at 1: one FP8 fragment feeds NACC 32-cycle MFMAs, which covers an
   // LDS read on its own.
   static constexpr int ACCR = TM * TN / THREADS;
-  static constexpr int BREG = ST * KSTEPS * NACC * FRAG * 4 + (DT == DT_I4 ? NACC * 8 : 0);  // + widened INT4
+  static constexpr int BREG = ST * KSTEPS * NACC * FRAG * 4 + (DT == DT_I4 ? NACC * 8 : 0)   // + widened INT4,
+                              + (ROWS ? 8 : 0);                                              // sorting
   static constexpr int SREG = NSC ? MREP + NACC + 2 * ST * (SLA + SLB) + 4 * GPP : 0;
   static constexpr int RBASE = (ACCR > 128 ? 0 : ACCR) + BREG + SREG;
   static constexpr int RA = (AFRAG == 1 && RBASE + 12 <= 236) ? 2 : (RBASE + 2 * AFRAG * 4 <= 236) ? 1 : 0;
@@ -217,6 +221,8 @@ struct TileCfg {
   static_assert(WAVES == 4 || KG == 1, "8-wave tiles: one K group");
   static_assert(EPI != EPI_GATED || (MS == 16 && NACC % 2 == 0 && KG == 1 && (DT == DT_BF16 || DT == DT_F16)),
                 "gated epilogue: whole gate / up pairs of 16-column blocks per wave");
+  static_assert(!ROWS || (MS == 16 && (NACC == 2 || NACC == 4) && KG == 1 && PIPE != 0 && (DT == DT_BF16 || DT == DT_F16)),
+                "row-major B: 2 or 4 column blocks per wave");
 };
 
 // Tile (tm, tn) and K split z of this workgroup. With a K split the ksplit
@@ -254,6 +260,17 @@ __device__ __forceinline__ void tile_coords(const TileArgs& p, uint32_t& tm, uin
   tile_coords(p, tm, tn, z);
 }
 
+// Row-major B (EPI_ROWS, for the backward pass, whose K axis is the slow axis of
+// an operand): MFMA lane (column, K group g) needs 8 consecutive K of a column,
+// which are 8 rows of memory. Lane j of the 16 lanes of group g loads NACC
+// consecutive columns of each of those rows (4 or 8 bytes; 16 lanes 64 or 128
+// contiguous bytes) and sorts the 8 loads into NACC operands with byte
+// permutes: block ni of a wave is its columns NACC * j + ni. The same cache
+// lines as the preshuffled form (counted: 1.178e8 L1 reads of L2 in both on 8192
+// x 4096 x 28672), and no pass over B beforehand, but 4 times the load
+// instructions and the permutes: 1490 us there against 1310. Rows from kb_rows on read
+// zeros through the bounds of the resource, which count the lane's whole offset.
+//
 // SCH: the hot-loop schedule pinned by scheduling fences (the pages'
 // hot_loop_scheduler, GEMM Optimization Guide §5.3; Kernel Tuning Guide §5
 // "enable_scheduler"); false leaves the order of the loop body to the
@@ -295,7 +312,8 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
 
   // Buffer resources based at this workgroup's first A row / first B block.
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + (size_t)m0 * Ka, TM * Ka);
-  const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.b + (size_t)(n0 / 16) * 16 * Kb, TN * Kb);
+  const __amdgpu_buffer_rsrc_t rb = C::ROWS ? make_rsrc(p.b + n0 * 2, p.kb_rows * p.ldb - n0 * 2)
+                                            : make_rsrc(p.b + (size_t)(n0 / 16) * 16 * Kb, TN * Kb);
 
   // ---- per-lane constant offsets ----
   // A global -> LDS: thread tid moves chunk (tid % CPR) of rows tid / CPR + i * RPP.
@@ -363,7 +381,8 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
   // 16-column block c/16, lane j = c%16 of it; the lane's K piece is 16-byte
   // group g of a 64-byte K block: offset blk*16*Kb + k0*1024 + g*256 + j*16.
   const int bcol = wave * C::NPW + lrow;
-  const uint32_t b_off0 = (uint32_t)(bcol / 16) * 16u * Kb + (uint32_t)(bcol % 16) * 16u + (uint32_t)lgrp * 256u;
+  const uint32_t b_off0 = C::ROWS ? 8u * lgrp * p.ldb + (uint32_t)(wave * C::NPW + C::NACC * lrow) * 2u
+                                  : (uint32_t)(bcol / 16) * 16u * Kb + (uint32_t)(bcol % 16) * 16u + (uint32_t)lgrp * 256u;
   const uint32_t b_step = (uint32_t)(MS / 16) * 16u * Kb;  // next MFMA column block
   // K-step part of the B offset (uniform): MS = 16: K block s*(KB/64)+f; MS = 32:
   // step s covers K bytes [32s, 32s+32) = block s/2, groups 2*(s%2) + lgrp.
@@ -439,9 +458,35 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
   // B load q of a tile: K step q / (NACC*FRAG), column block (q / FRAG) % NACC, piece q % FRAG
   auto load_b = [&](auto par_c, int kt, int q) GP_INLINE {
     constexpr int par = decltype(par_c)::value;
+    if constexpr (C::ROWS) {
+      // K step q / 8, row q % 8 of the lane's K group: dword e holds columns
+      // 2 e, 2 e + 1; kept where sort_b leaves the operands
+      const uint32_t off = b_off0 + (uint32_t)(kt * (TKB / 2) + q / 8 * 32 + q % 8) * p.ldb;
+      const int s = q / 8, i = q % 8;
+      if constexpr (C::NACC == 2) {
+        bfr[par][s][i % 2][0][i / 2] = buf_load4(rb, off, 0);
+      } else {
+        const v2i t = buf_load8(rb, off, 0);
+        bfr[par][s][i % 2][0][i / 2] = t[0];
+        bfr[par][s][2 + i % 2][0][i / 2] = t[1];
+      }
+      return;
+    }
     const int s = q / (C::NACC * C::FRAG), ni = (q / C::FRAG) % C::NACC, f = q % C::FRAG;
     const uint32_t kbase = (uint32_t)kt * (TKB / 64) * 1024u;
     bfr[par][s][ni][f] = buf_load16(rb, b_off0 + b_koff(s, f), kbase + ni * b_step);
+  };
+  // Row-major B: rows 2 d and 2 d + 1 of a K group, in place, become dword d of
+  // the operands of two column blocks each
+  auto sort_b = [&](auto par_c, int s, int d) GP_INLINE {
+    constexpr int par = decltype(par_c)::value;
+    if constexpr (C::ROWS)
+#pragma unroll
+      for (int e = 0; e < C::NACC / 2; ++e) {
+        const uint32_t r0 = (uint32_t)bfr[par][s][2 * e][0][d], r1 = (uint32_t)bfr[par][s][2 * e + 1][0][d];
+        bfr[par][s][2 * e][0][d] = (int)__builtin_amdgcn_perm(r1, r0, 0x05040100u);
+        bfr[par][s][2 * e + 1][0][d] = (int)__builtin_amdgcn_perm(r1, r0, 0x07060302u);
+      }
   };
   // FP4: the WG's TM + TN scale rows of one K tile, SCB bytes each. A and B
   // rows use separate loads so that each load's buffer resource is uniform.
@@ -563,7 +608,7 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
   auto fence = [] {
     if constexpr (SCH) __builtin_amdgcn_sched_barrier(0);
   };
-  constexpr int NBL = C::KSTEPS * C::NACC * C::FRAG;       // B loads per tile
+  constexpr int NBL = C::KSTEPS * (C::ROWS ? 8 : C::NACC * C::FRAG);   // B loads per tile
   constexpr int NVMEM = C::ALOADS + NBL + C::SLOADS;        // global loads per tile
   auto compute = [&](auto par_c, int kt, auto&& issue_loads) GP_INLINE {
     constexpr int par = decltype(par_c)::value;
@@ -601,9 +646,24 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
 #pragma unroll
         for (int ni = 0; ni < C::NACC; ++ni) widen_int4(bfr[par][s][ni][0], blo[ni], bhi[ni]);
       }
+      if constexpr (C::ROWS) {
+        // the next step's operands are sorted among this step's last MFMAs
+        // (the next tile's B was loaded a tile ago): sorted right before their
+        // own, the matrix unit waited for them (8192 x 4096 x 28672: 1550 us
+        // instead of 1490)
+        static_assert(C::MREP >= 4, "a group of MFMAs per dword");
+        if constexpr (mi >= C::MREP - 4) {
+          if constexpr (s + 1 < C::KSTEPS) sort_b(par_c, s + 1, mi - (C::MREP - 4));
+          else sort_b(std::integral_constant<int, (par + 1) % C::ST>{}, 0, mi - (C::MREP - 4));
+        }
+      }
 #pragma unroll
       for (int ni = 0; ni < C::NACC; ++ni) {
-        if constexpr (DT == DT_FP4) {
+        if constexpr (EPI == EPI_ROWS) {
+          acc[mi][ni] = mma<DT, MS>(bfr[par][s][ni], a, acc[mi][ni]);
+        } else if constexpr (EPI == EPI_ROWS_T) {
+          acc[mi][ni] = mma<DT, MS>(a, bfr[par][s][ni], acc[mi][ni]);
+        } else if constexpr (DT == DT_FP4) {
           acc[mi][ni] = mma<DT, MS, s>(bfr[par][s][ni], a, acc[mi][ni], psb[ni], psa[mi]);
         } else if constexpr (DT == DT_I4) {
           // the widened values are 16 x the INT4 ones; the epilogue divides by 16
@@ -690,6 +750,9 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
   });
   store_s(0);
   if constexpr (C::SG > 1) static_for<0, C::NGL>([&](auto j_c) GP_INLINE { store_g1(j_c, 0, g0[decltype(j_c)::value]); });
+  if constexpr (C::ROWS)
+#pragma unroll
+    for (int d = 0; d < 4; ++d) sort_b(std::integral_constant<int, 0>{}, 0, d);
   if constexpr (C::ASYNC) {
     __builtin_amdgcn_sched_barrier(0);
     wait_vm(std::integral_constant<int, NBL + (C::ST - 2) * NVMEM>{});
@@ -938,6 +1001,48 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
       store_half(p.gate, [](Acc g, Acc) GP_INLINE -> v4f { return g; });
       store_half(p.up, [](Acc, Acc u) GP_INLINE -> v4f { return u; });
     }
+    return;
+  }
+
+  if constexpr (C::ROWS) {
+    // Through LDS (the A buffers are dead) for whole-row stores. EPI_ROWS: a
+    // lane holds, of row mi * 16 + elrow, the 4 NACC consecutive columns
+    // NACC * (4 elgrp + r) + ni; EPI_ROWS_T: of column NACC * elrow + ni the
+    // rows mi * 16 + 4 elgrp + r.
+    __syncthreads();
+#pragma unroll
+    for (int mi = 0; mi < C::MREP; ++mi) {
+      if constexpr (EPI == EPI_ROWS) {
+        char* d = lds + (mi * MS + elrow) * C::CSTRIDE + (wave * C::NPW + C::NACC * 4 * elgrp) * C::OB;
+#pragma unroll
+        for (int h = 0; h < C::NACC / 2; ++h) {   // 8 columns: two or four of r times ni
+          v4f v[2];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e / 4][e % 4] = acc[mi][(8 * h + e) % C::NACC][(8 * h + e) / C::NACC];
+          const v2i lo = pack_out4<DT>(v[0]), hi = pack_out4<DT>(v[1]);
+          *(v4i*)(d + 16 * h) = v4i{lo[0], lo[1], hi[0], hi[1]};
+        }
+      } else {
+#pragma unroll
+        for (int ni = 0; ni < C::NACC; ++ni)
+          *(v2i*)(lds + (wave * C::NPW + C::NACC * elrow + ni) * C::CSTRIDE + (mi * MS + 4 * elgrp) * C::OB) =
+              pack_out4<DT>(acc[mi][ni]);
+      }
+    }
+    __syncthreads();
+    constexpr bool T = EPI == EPI_ROWS_T;
+    constexpr int CH_ROW = C::CCOLS * C::OB / 16, TOTAL = C::CROWS * CH_ROW;
+    const uint32_t ldc = T ? p.M : p.N, rskip = T ? nskip : mskip, cskip = T ? mskip : nskip;
+    const size_t base = ((size_t)(T ? n0 : m0) * ldc + (T ? m0 : n0)) * C::OB;
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.c + base, ((C::CROWS - 1) * ldc + C::CCOLS) * C::OB);
+#pragma unroll
+    for (int i = 0; i < TOTAL / C::THREADS; ++i) {
+      const int q = i * C::THREADS + etid;
+      const uint32_t row = q / CH_ROW, col = (q % CH_ROW) * 8;
+      const v4i v = *(const v4i*)(lds + row * C::CSTRIDE + col * C::OB);
+      buf_store16(v, ro, (row >= rskip && col >= cskip) ? (row * ldc + col) * C::OB : 0x80000000u);
+    }
+    static_assert(!C::ROWS || TOTAL % C::THREADS == 0, "whole passes");
     return;
   }
 

@@ -44,9 +44,10 @@ enum DType : int { DT_I8 = 0, DT_FP8 = 1, DT_BF16 = 2, DT_FP4 = 3, DT_F16 = 4, D
 
 // Activations of the fused epilogue (values of the C ABI's GP_ACT_*).
 enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
-// EPI_GATED (not an option of the C ABI): pairs of column blocks are a gate
-// and an up product, and act(gate) * up is stored.
-enum Epi : int { EPI_DIRECT = 1, EPI_CSHUFFLE = 2, EPI_GATED = 3 };
+// Not options of the C ABI: EPI_GATED: pairs of column blocks are a gate and an
+// up product, and act(gate) * up is stored; EPI_ROWS: B is row-major [K][N] (see
+// the tile kernel); EPI_ROWS_T: so, and the output is stored transposed, [N][M].
+enum Epi : int { EPI_DIRECT = 1, EPI_CSHUFFLE = 2, EPI_GATED = 3, EPI_ROWS = 4, EPI_ROWS_T = 5 };
 
 // gfx9 buffer resource word 3 (32-bit raw buffer, bounds checked on num_records).
 constexpr int kRsrcWord3 = 0x00020000;

@@ -128,8 +128,8 @@ __device__ __forceinline__ void activate_grad(float g, float& value, float& slop
 // in fp32, rounded once to the 16-bit type the matrix products read (the
 // products' own results are rounded to it as well, so this adds at most as
 // much error again). Written as d [M][Np] (dg, du, then zeros from 2F to Np in
-// each row; null if dx is not wanted) and dt = d^T [2F][Mp], zeros from M to Mp (null if dw is
-// not wanted). F % 16 == 0.
+// each row; null if no product reads it) and dt = d^T [2F][Mp], zeros from M to
+// Mp (null likewise). F % 16 == 0.
 struct GateGradArgs {
   const char *dh, *gate, *up;
   char *d, *dt;

@@ -149,3 +149,11 @@
 #define GP_TILE_GATED_F16(X) GP_TILE_GATED_COMMON(X, DT_F16) X(DT_F16, 16, 64, 128, 64, 0)
 #define GP_TILE_GATED_KSPLIT_BF16(X) X(DT_BF16, 16, 128, 256, 128, 3) X(DT_BF16, 16, 64, 128, 128, 0)
 #define GP_TILE_GATED_KSPLIT_F16(X) X(DT_F16, 16, 128, 256, 128, 3) X(DT_F16, 16, 64, 128, 128, 0)
+
+// Row-major B (BF16 / FP16, 16 x 16 blocks, 128-byte K tiles): X(dtype,
+// epilogue, tile_m, tile_n, stages, able to split K across workgroups). Three
+// stages of the 128 x 256 tile's B do not fit its registers beside the operands
+// sorted from them.
+#define GP_TILE_ROWS(X, DT, EPI) \
+  X(DT, EPI, 256, 256, 3, false) X(DT, EPI, 128, 256, 2, false) X(DT, EPI, 64, 256, 3, false) \
+  X(DT, EPI, 128, 128, 3, false) X(DT, EPI, 64, 128, 3, false) X(DT, EPI, 128, 256, 2, true) X(DT, EPI, 64, 128, 3, true)
