@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/gemm_preshuffle.h"
@@ -79,11 +80,12 @@ int plan_gated(int dtype, int64_t M, int64_t F, int64_t H, GatedPlan* p) {
 // ---- backward pass of a linear layer C[M][N] = A[M][K] B[N][K]^T ----
 // da = dc b: K axis N (gated: padded, since the call makes dc).
 // db = dc^T a: K axis M, padded with zeros.
-// From 65 to 4095 rows both run on the tile kernel's row-major form: da reads b
+// Up to 4095 rows both run on the tile kernel's row-major form: da reads b
 // as it is; db is computed as (a^T dc)^T, which reads dc as it is, from a
 // transposed copy of a (the smaller operand), and is stored transposed.
-// Otherwise they run on the preshuffled kernels, from copies laid out for them:
-// b^T for da, dc^T and a^T for db. The copies cost bandwidth, the row-major
+// With more (or a K axis of dc that is not whole 128-byte tiles) they run on the
+// preshuffled kernels, from copies laid out for them: b^T for da, dc^T and a^T
+// for db. The copies cost bandwidth, the row-major
 // products 2 to 14% of the matrix rate, so that the copies pay off with many rows.
 // Gated backward M x F x H in us, row-major against copies: 64 x 1024 x 1024 20.9,
 // 19.6; 130 x 2064 x 2048 35, 43; 512 x 4096 x 4096 102, 121; 1024 x 8192 x 2048
@@ -113,29 +115,43 @@ int64_t pad_k(int64_t k) {
   return (k + unit - 1) / unit * unit;
 }
 
-// The planner's tile for [M][K] x [K][N], moved to one that the row-major form
-// has; false if there is none.
+// Tile and K split of the row-major form for [M][K] x [K][N], by the time
+//   4 + rounds * (K tiles * step + ends) + ranges * join   (us)
+// of the workgroups on 256 CUs, whose constants come from 23 shapes timed with
+// every tile and 1 to 16 ranges on one MI355X (M 32 to 4096, K 64 to 14336): the
+// model's choice was the fastest or within 8% of it on 20. step: one 128-byte K
+// tile; ends: filling the pipeline and storing the tile; join: writing a range's
+// partial tile and the last workgroup's reading it. Tiles of 128 columns share a
+// CU by two or three, so their rounds are counted in fractions. Some of the
+// measured pairs: 2000 x 4096 x 14336 206 on 256 x 256 in two, 232 on 128 x 256;
+// 161 x 2656 x 10624 29.6 on 64 x 128 in four (39.7 in three, 35.8 in eight);
+// transposed 4096 x 14336 x 128 42 on 128 x 128, 47 on 256 x 256.
 bool plan_rows(int64_t M, int64_t N, int64_t Kb, Plan* p) {
-  if (M < 64 || N < 128 || Kb % 128) return false;   // smallest tile, whole K tiles
-  if (p->kernel != GP_KERNEL_TILE || p->tm < 64) {
-    p->kernel = GP_KERNEL_TILE;
-    p->tm = 64;
-    p->tn = 128;
-    p->ks = 1;
-  } else if (p->tn == 512) {
-    p->tn = 256;
-  }
-  p->tkb = 128;
-  if (p->ks > 1 && !((p->tm == 128 && p->tn == 256) || (p->tm == 64 && p->tn == 128))) p->ks = 1;
+  if (Kb % 128) return false;   // whole K tiles
+  struct Tile { int tm, tn; double step, ends, join; };
+  static const Tile tiles[] = {{256, 256, 1.45, 10, 4.3}, {128, 256, 1.05, 5, 2.1}, {128, 128, 0.52, 2, 1.1},
+                               {64, 128, 0.40, 2, 0.55}};
   const int64_t kt = Kb / 128;
-  if (p->tm == 64 && p->tn == 128 && p->ks == 1) {
-    // as the planner: ranges of at least 1024 K elements until the grid fills
-    // the GPU
-    const int64_t tiles = ((M + 63) / 64) * ((N + 127) / 128);
-    while (p->ks < 16 && tiles * p->ks < 256 && kt % (2 * p->ks) == 0 && Kb / (2 * p->ks) >= 2048) p->ks *= 2;
-    if (tiles > kMaxSplitTiles) p->ks = 1;
+  double best = -1;
+  for (const Tile& t : tiles) {
+    const int64_t n = ((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn);
+    for (int64_t ks = 1; ks <= 16; ++ks) {
+      if (ks > 1 && (kt / ks < 4 || n * ks > 512)) break;
+      const double fill = (double)(n * ks) / 256;
+      const double rounds = std::max(1.0, t.tn == 128 ? fill : std::ceil(fill));
+      const double us = 4 + rounds * ((double)kt / ks * t.step + t.ends) + (ks > 1 ? ks * t.join : 0);
+      if (best >= 0 && us >= best) continue;
+      best = us;
+      *p = Plan();
+      p->kernel = GP_KERNEL_TILE;
+      p->tm = t.tm;
+      p->tn = t.tn;
+      p->tkb = 128;
+      p->ks = (int)ks;
+      p->Kb = Kb;
+    }
   }
-  return kt % p->ks == 0;
+  return true;
 }
 
 // gated: dc itself is made by the call ([M][Np] in the workspace).
@@ -147,20 +163,17 @@ int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool
   p->Mp = pad_k(M);
   p->Np = gated ? pad_k(N) : N;
   if (!fits(p->Mp, 2 * K) || !fits(p->Np, 2 * K) || !fits(p->Mp, 2 * p->Np)) return GP_ESHAPE;
-  const bool between = M > 64 && M < 4096;
+  const bool rows = M < 4096;
   int r;
   int64_t parts = 0;
   if (want_da) {
-    if ((r = plan_gemm(dtype, M, K, p->Np, &p->da))) return r;
-    Plan rows = p->da;
-    if ((p->da_rows = between && plan_rows(M, K, 2 * p->Np, &rows))) p->da = rows;
+    p->da_rows = rows && plan_rows(M, K, 2 * p->Np, &p->da);
+    if (!p->da_rows && (r = plan_gemm(dtype, M, K, p->Np, &p->da))) return r;
     parts = std::max(parts, plan_workspace(p->da, M, K));
   }
   if (want_db) {
-    Plan rows;
-    p->db_rows = between && plan_gemm(dtype, K, N, p->Mp, &rows) == GP_OK && plan_rows(K, N, 2 * p->Mp, &rows);
-    if (p->db_rows) p->db = rows;
-    else if ((r = plan_gemm(dtype, N, K, p->Mp, &p->db))) return r;
+    p->db_rows = rows && plan_rows(K, N, 2 * p->Mp, &p->db);
+    if (!p->db_rows && (r = plan_gemm(dtype, N, K, p->Mp, &p->db))) return r;
     parts = std::max(parts, p->db_rows ? plan_workspace(p->db, K, N) : plan_workspace(p->db, N, K));
   }
   int64_t at = p->parts = align256(parts);
@@ -175,11 +188,6 @@ int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool
   p->off_d = take(gated && (want_da || p->db_rows) ? M * p->Np * 2 : 0);
   p->bytes = std::max<int64_t>(at, 256);   // never none: one rule for every caller
   return GP_OK;
-}
-
-__global__ __launch_bounds__(256) void clear_words_kernel(uint32_t* p, uint32_t n) {
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  if (i < n) p[i] = 0u;
 }
 
 uint32_t tiles64(int64_t R, int64_t C) { return (uint32_t)(((R + 63) / 64) * ((C + 63) / 64)); }
@@ -213,40 +221,56 @@ int launch_rows(int dtype, const Plan& p, const void* a, const void* b, void* c,
 }
 
 // Launches, in order, what has to run once the pointers are valid. dc: the
-// output gradient, rows of ldc elements; or (gated) d in the workspace, with its
-// transpose already there where the plan reads one. Stops at the first launch
-// that fails.
-int run_backward(int dtype, const BackwardPlan& p, const void* dc, const void* a, const void* b, void* da, void* db,
-                 int64_t M, int64_t N, int64_t K, bool gated, char* ws, hipStream_t s) {
-  int r;
-  const int64_t ldc = gated ? p.Np : N;
+// output gradient, rows of ldc elements; gate: the pointwise backward that makes
+// it first (else null). Stops at the first launch that fails.
+int run_backward(int dtype, const BackwardPlan& p, const GateGradArgs* gate, const void* dc, const void* a,
+                 const void* b, void* da, void* db, int64_t M, int64_t N, int64_t K, char* ws, hipStream_t s) {
+  const int64_t ldc = gate ? p.Np : N;
+  PrepArgs t = {};
+  uint64_t blocks = 0;
+  if (gate) {
+    t.gate = *gate;
+    blocks = t.gate.blocks = tiles64(p.Mp, t.gate.F);
+  }
+  int jobs = 0;
+  auto copy = [&](const void* src, int64_t off, int64_t R, int64_t C, int64_t Kp, bool preshuffled) {
+    CopyJob& j = t.copy[jobs++];
+    j.src = (const char*)src;
+    j.dst = ws + off;
+    j.R = (uint32_t)R;
+    j.C = (uint32_t)C;
+    j.Kp = (uint32_t)Kp;
+    j.tiles_c = (uint32_t)((C + 63) / 64);
+    j.blocks = tiles64(Kp, C);
+    j.preshuffled = preshuffled;
+    blocks += j.blocks;
+  };
+  if (da && !p.da_rows) copy(b, p.off_bt, N, K, p.Np, true);
+  if (db) copy(a, p.off_at, M, K, p.Mp, !p.db_rows);
+  if (db && !p.db_rows && !gate) copy(dc, p.off_ct, M, N, p.Mp, false);
   if (p.parts > 0) {
     // arrival counters of the K splits: cleared here, so that the workspace
     // needs no state from earlier calls
+    t.cnt = (uint32_t*)ws;
+    t.ncnt = (uint32_t)(kCounterBytes / 4);
+    blocks = std::max<uint64_t>(blocks, 16);
+  }
+  int r;
+  if (blocks > 0) {
     forget_hip_error();
-    hipLaunchKernelGGL(clear_words_kernel, dim3((uint32_t)(kCounterBytes / 4 / 256)), dim3(256), 0, s, (uint32_t*)ws,
-                       (uint32_t)(kCounterBytes / 4));
+    if (dtype == GP_BF16) hipLaunchKernelGGL((prep_kernel<DT_BF16>), dim3((uint32_t)blocks), dim3(256), 0, s, t);
+    else hipLaunchKernelGGL((prep_kernel<DT_F16>), dim3((uint32_t)blocks), dim3(256), 0, s, t);
     if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
   }
-  auto transpose = [&](auto* kernel, const void* src, int64_t off, int64_t R, int64_t C, int64_t Kp) {
-    forget_hip_error();
-    hipLaunchKernelGGL(kernel, dim3(tiles64(Kp, C)), dim3(256), 0, s, (const char*)src, ws + off, (uint32_t)R,
-                       (uint32_t)C, (uint32_t)Kp, (uint32_t)((C + 63) / 64));
-    return report_hip(hipGetLastError(), "kernel launch");
-  };
-  if (da && p.da_rows) {
-    if ((r = launch_rows(dtype, p.da, dc, b, da, M, K, 2 * ldc, N, K, false, ws, s))) return r;
-  } else if (da) {
-    if ((r = transpose(preshuffle_t_kernel, b, p.off_bt, N, K, p.Np))) return r;
-    if ((r = launch_gemm(dtype, p.da, dc, ws + p.off_bt, da, M, K, ws, s))) return r;
+  if (da) {
+    r = p.da_rows ? launch_rows(dtype, p.da, dc, b, da, M, K, 2 * ldc, N, K, false, ws, s)
+                  : launch_gemm(dtype, p.da, dc, ws + p.off_bt, da, M, K, ws, s);
+    if (r) return r;
   }
-  if (db && p.db_rows) {
-    if ((r = transpose(transpose_kernel, a, p.off_at, M, K, p.Mp))) return r;
-    if ((r = launch_rows(dtype, p.db, ws + p.off_at, dc, db, K, N, 2 * p.Mp, M, ldc, true, ws, s))) return r;
-  } else if (db) {
-    if ((r = transpose(preshuffle_t_kernel, a, p.off_at, M, K, p.Mp))) return r;
-    if (!gated && (r = transpose(transpose_kernel, dc, p.off_ct, M, N, p.Mp))) return r;
-    if ((r = launch_gemm(dtype, p.db, ws + p.off_ct, ws + p.off_at, db, N, K, ws, s))) return r;
+  if (db) {
+    r = p.db_rows ? launch_rows(dtype, p.db, ws + p.off_at, dc, db, K, N, 2 * p.Mp, M, ldc, true, ws, s)
+                  : launch_gemm(dtype, p.db, ws + p.off_ct, ws + p.off_at, db, N, K, ws, s);
+    if (r) return r;
   }
   return GP_OK;
 }
@@ -363,7 +387,7 @@ int gemm_backward(int dtype, const void* dc, const void* a, const void* b, void*
   if (!workspace || (int64_t)workspace_bytes < p.bytes) return GP_EWORKSPACE;
   if (!is_aligned16(workspace)) return GP_EINVAL;
   if ((r = require_gfx950())) return r;
-  return run_backward(dtype, p, dc, a, b, da, db, M, N, K, false, (char*)workspace, (hipStream_t)stream);
+  return run_backward(dtype, p, nullptr, dc, a, b, da, db, M, N, K, (char*)workspace, (hipStream_t)stream);
 }
 
 int gemm_gated_backward_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, int want_dx, int want_dw,
@@ -392,7 +416,6 @@ int gemm_gated_backward(int dtype, const void* dh, const void* gate, const void*
   if (!is_aligned16(workspace)) return GP_EINVAL;
   if ((r = require_gfx950())) return r;
   char* ws = (char*)workspace;
-  const hipStream_t s = (hipStream_t)stream;
   GateGradArgs t;
   t.dh = (const char*)dh;
   t.gate = (const char*)gate;
@@ -405,12 +428,7 @@ int gemm_gated_backward(int dtype, const void* dh, const void* gate, const void*
   t.Np = (uint32_t)p.Np;
   t.tiles_c = (uint32_t)((F + 63) / 64);
   t.act = act;
-  forget_hip_error();
-  const dim3 grid(tiles64(p.Mp, F));
-  if (dtype == GP_BF16) hipLaunchKernelGGL((gate_grad_kernel<DT_BF16>), grid, dim3(256), 0, s, t);
-  else hipLaunchKernelGGL((gate_grad_kernel<DT_F16>), grid, dim3(256), 0, s, t);
-  if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
-  return run_backward(dtype, p, ws + p.off_d, x, w, dx, dw, M, 2 * F, H, true, ws, s);
+  return run_backward(dtype, p, &t, ws + p.off_d, x, w, dx, dw, M, 2 * F, H, ws, (hipStream_t)stream);
 }
 
 }  // extern "C"

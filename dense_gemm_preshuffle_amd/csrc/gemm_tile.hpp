@@ -205,7 +205,7 @@ struct TileCfg {
   // LDS read on its own.
   static constexpr int ACCR = TM * TN / THREADS;
   static constexpr int BREG = ST * KSTEPS * NACC * FRAG * 4 + (DT == DT_I4 ? NACC * 8 : 0)   // + widened INT4,
-                              + (ROWS ? 8 : 0);                                              // sorting
+                              + (ROWS ? 16 : 0);                                             // sorting, row offsets
   static constexpr int SREG = NSC ? MREP + NACC + 2 * ST * (SLA + SLB) + 4 * GPP : 0;
   static constexpr int RBASE = (ACCR > 128 ? 0 : ACCR) + BREG + SREG;
   static constexpr int RA = (AFRAG == 1 && RBASE + 12 <= 236) ? 2 : (RBASE + 2 * AFRAG * 4 <= 236) ? 1 : 0;
@@ -300,19 +300,32 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
   uint32_t tm, tn, kz;
   tile_coords(p, tm, tn, kz);
   uint32_t m0 = tm * TM, n0 = tn * TN, mskip, nskip;
-  edge_shift(m0, mskip, TM, p.M);
-  edge_shift(n0, nskip, TN, p.N);
+  if constexpr (C::ROWS) {
+    // a matrix smaller than the tile: rows of A past it read zeros, what B
+    // holds past a row falls into columns that are not stored
+    if (p.M >= TM) edge_shift(m0, mskip, TM, p.M);
+    else mskip = 0;
+    if (p.N >= TN) edge_shift(n0, nskip, TN, p.N);
+    else nskip = 0;
+  } else {
+    edge_shift(m0, mskip, TM, p.M);
+    edge_shift(n0, nskip, TN, p.N);
+  }
   const uint32_t Kb = p.Kb;
   const uint32_t Ka = Kb * C::AKB;   // bytes per row of A
   // K tiles of this workgroup: split kz of ksplit equal ranges; of this group:
-  // [kt0, kt0 + KT) (the planner makes ksplit * KG divide the K tiles)
-  const int KTS = (int)(Kb / TKB) / (KS ? (int)p.ksplit : 1);
-  const int KT = KTS / KG;
-  const int kt0 = __builtin_amdgcn_readfirstlane((int)kz * KTS + grp * KT);
+  // [kt0, kt0 + KT) (the planner makes ksplit * KG divide the K tiles). With a
+  // row-major B the ranges may differ by a tile.
+  const int KALL = (int)(Kb / TKB);
+  const int KTS = KALL / (KS ? (int)p.ksplit : 1);
+  const int kr0 = KS && C::ROWS ? (int)kz * KALL / (int)p.ksplit : (int)kz * KTS;
+  const int KT = (KS && C::ROWS ? ((int)kz + 1) * KALL / (int)p.ksplit - kr0 : KTS) / KG;
+  const int kt0 = __builtin_amdgcn_readfirstlane(kr0 + grp * KT);
 
   // Buffer resources based at this workgroup's first A row / first B block.
-  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + (size_t)m0 * Ka, TM * Ka);
-  const __amdgpu_buffer_rsrc_t rb = C::ROWS ? make_rsrc(p.b + n0 * 2, p.kb_rows * p.ldb - n0 * 2)
+  const uint32_t a_rows = C::ROWS ? min((uint32_t)TM, p.M) : (uint32_t)TM;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + (size_t)m0 * Ka, a_rows * Ka);
+  const __amdgpu_buffer_rsrc_t rb = C::ROWS ? make_rsrc(p.b + (size_t)n0 * 2, p.kb_rows * p.ldb - n0 * 2)
                                             : make_rsrc(p.b + (size_t)(n0 / 16) * 16 * Kb, TN * Kb);
 
   // ---- per-lane constant offsets ----
@@ -452,7 +465,7 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
   };
   auto load_a_dma = [&](int stage, int kt, int i) GP_INLINE {
     if constexpr (C::ASYNC)
-      lds_dma16(p.a + (size_t)m0 * Ka, TM * Ka, glds + stage * C::ABUF + (i * C::WAVES + wave) * 1024,
+      lds_dma16(p.a + (size_t)m0 * Ka, a_rows * Ka, glds + stage * C::ABUF + (i * C::WAVES + wave) * 1024,
                 (DMA_STEP ? a_dma[0] + i * RPD * Ka : a_dma[DMA_STEP ? 0 : i]) + kt * C::TKA);
   };
   // B load q of a tile: K step q / (NACC*FRAG), column block (q / FRAG) % NACC, piece q % FRAG
@@ -1033,6 +1046,7 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
     constexpr bool T = EPI == EPI_ROWS_T;
     constexpr int CH_ROW = C::CCOLS * C::OB / 16, TOTAL = C::CROWS * CH_ROW;
     const uint32_t ldc = T ? p.M : p.N, rskip = T ? nskip : mskip, cskip = T ? mskip : nskip;
+    const uint32_t rend = T ? p.N : p.M;   // (the columns' end is ldc: whole 16-byte pieces, a row of 32)
     const size_t base = ((size_t)(T ? n0 : m0) * ldc + (T ? m0 : n0)) * C::OB;
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.c + base, ((C::CROWS - 1) * ldc + C::CCOLS) * C::OB);
 #pragma unroll
@@ -1040,7 +1054,7 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
       const int q = i * C::THREADS + etid;
       const uint32_t row = q / CH_ROW, col = (q % CH_ROW) * 8;
       const v4i v = *(const v4i*)(lds + row * C::CSTRIDE + col * C::OB);
-      buf_store16(v, ro, (row >= rskip && col >= cskip) ? (row * ldc + col) * C::OB : 0x80000000u);
+      buf_store16(v, ro, (row >= rskip && col >= cskip && row < rend && col < ldc) ? (row * ldc + col) * C::OB : 0x80000000u);
     }
     static_assert(!C::ROWS || TOTAL % C::THREADS == 0, "whole passes");
     return;

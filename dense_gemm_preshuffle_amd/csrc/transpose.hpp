@@ -34,33 +34,6 @@ struct Tile64 {
   }
 };
 
-// dst = preshuffled layout of B = src^T: src [R][C] row-major, B[n = c][k = r],
-// k from R to Kp (a multiple of 32) filled with zeros. C % 16 == 0.
-__global__ __launch_bounds__(256) void preshuffle_t_kernel(const char* __restrict__ src, char* __restrict__ dst,
-                                                           uint32_t R, uint32_t C, uint32_t Kp, uint32_t tiles_c) {
-  __shared__ __attribute__((aligned(16))) Tile64 t;
-  const uint32_t c0 = blockIdx.x % tiles_c * 64u, r0 = blockIdx.x / tiles_c * 64u;
-  const int q = threadIdx.x & 7, rp = threadIdx.x >> 3;
-  const uint32_t r = r0 + 2 * rp, c = c0 + 8 * q;
-  v4i a = v4i{0, 0, 0, 0}, b = a;
-  if (c < C) {
-    const char* p = src + ((size_t)r * C + c) * 2;
-    if (r < R) a = *(const v4i*)p;
-    if (r + 1 < R) b = *(const v4i*)(p + (size_t)C * 2);
-  }
-  t.put(q, rp, a, b);
-  __syncthreads();
-  // chunk (16-column block nb, 32-row block kb, group g, column j) of the tile
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int x = i * 256 + threadIdx.x;
-    const int j = x & 15, g = (x >> 4) & 3, kb = (x >> 6) & 1, nb = x >> 7;
-    if (c0 + nb * 16 >= C || r0 + kb * 32 >= Kp) continue;
-    const size_t blk = (size_t)(c0 / 16 + nb) * (Kp / 32) + r0 / 32 + kb;
-    *(v4i*)(dst + (blk * 64 + g * 16 + j) * 16) = t.get(nb * 16 + j, kb * 4 + g);
-  }
-}
-
 // the transposed tile as rows c0 .. c0 + 63 of dst [C][Kp], columns r0 .. r0 + 63
 __device__ __forceinline__ void store_transposed(const Tile64& t, char* dst, uint32_t c0, uint32_t r0, uint32_t C,
                                                  uint32_t Kp) {
@@ -73,22 +46,40 @@ __device__ __forceinline__ void store_transposed(const Tile64& t, char* dst, uin
   }
 }
 
-// dst [C][Kp] = src^T, src [R][C], columns from R to Kp zeros. C % 8 == 0.
-__global__ __launch_bounds__(256) void transpose_kernel(const char* __restrict__ src, char* __restrict__ dst,
-                                                        uint32_t R, uint32_t C, uint32_t Kp, uint32_t tiles_c) {
-  __shared__ __attribute__((aligned(16))) Tile64 t;
-  const uint32_t c0 = blockIdx.x % tiles_c * 64u, r0 = blockIdx.x / tiles_c * 64u;
+// A transposed copy of src [R][C] (C % 16 == 0), rows from R to Kp (a multiple
+// of 32) taken as zeros: dst [C][Kp], or (preshuffled) the layout of B = src^T,
+// B[n = c][k = r].
+struct CopyJob {
+  const char* src;
+  char* dst;
+  uint32_t R, C, Kp, tiles_c, blocks;   // 64 x 64 tiles per row of tiles, and in all
+  uint32_t preshuffled;
+};
+__device__ __forceinline__ void copy_tile(Tile64& t, const CopyJob& p, uint32_t block) {
+  const uint32_t c0 = block % p.tiles_c * 64u, r0 = block / p.tiles_c * 64u;
   const int q = threadIdx.x & 7, rp = threadIdx.x >> 3;
   const uint32_t r = r0 + 2 * rp, c = c0 + 8 * q;
   v4i a = v4i{0, 0, 0, 0}, b = a;
-  if (c < C) {
-    const char* p = src + ((size_t)r * C + c) * 2;
-    if (r < R) a = *(const v4i*)p;
-    if (r + 1 < R) b = *(const v4i*)(p + (size_t)C * 2);
+  if (c < p.C) {
+    const char* s = p.src + ((size_t)r * p.C + c) * 2;
+    if (r < p.R) a = *(const v4i*)s;
+    if (r + 1 < p.R) b = *(const v4i*)(s + (size_t)p.C * 2);
   }
   t.put(q, rp, a, b);
   __syncthreads();
-  store_transposed(t, dst, c0, r0, C, Kp);
+  if (!p.preshuffled) {
+    store_transposed(t, p.dst, c0, r0, p.C, p.Kp);
+    return;
+  }
+  // chunk (16-column block nb, 32-row block kb, group g, column j) of the tile
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int x = i * 256 + threadIdx.x;
+    const int j = x & 15, g = (x >> 4) & 3, kb = (x >> 6) & 1, nb = x >> 7;
+    if (c0 + nb * 16 >= p.C || r0 + kb * 32 >= p.Kp) continue;
+    const size_t blk = (size_t)(c0 / 16 + nb) * (p.Kp / 32) + r0 / 32 + kb;
+    *(v4i*)(p.dst + (blk * 64 + g * 16 + j) * 16) = t.get(nb * 16 + j, kb * 4 + g);
+  }
 }
 
 template <int DT>
@@ -133,13 +124,12 @@ __device__ __forceinline__ void activate_grad(float g, float& value, float& slop
 struct GateGradArgs {
   const char *dh, *gate, *up;
   char *d, *dt;
-  uint32_t M, F, Mp, Np, tiles_c;
+  uint32_t M, F, Mp, Np, tiles_c, blocks;   // 64 x 64 tiles per row of tiles, and in all
   int act;
 };
 template <int DT>
-__global__ __launch_bounds__(256) void gate_grad_kernel(GateGradArgs p) {
-  __shared__ __attribute__((aligned(16))) Tile64 tg, tu;
-  const uint32_t c0 = blockIdx.x % p.tiles_c * 64u, r0 = blockIdx.x / p.tiles_c * 64u;
+__device__ __forceinline__ void gate_grad_tile(Tile64& tg, Tile64& tu, const GateGradArgs& p, uint32_t block) {
+  const uint32_t c0 = block % p.tiles_c * 64u, r0 = block / p.tiles_c * 64u;
   const int q = threadIdx.x & 7, rp = threadIdx.x >> 3;
   const uint32_t r = r0 + 2 * rp, c = c0 + 8 * q;
   v4i in[3][2], dg[2], du[2];
@@ -196,6 +186,36 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateGradArgs p) {
   __syncthreads();
   store_transposed(tg, p.dt, c0, r0, p.F, p.Mp);
   store_transposed(tu, p.dt + (size_t)p.F * p.Mp * 2, c0, r0, p.F, p.Mp);
+}
+
+// Everything the backward products need beforehand, in one launch (a launch costs
+// the host as much as a small pass takes): the pointwise backward, up to three
+// copies, and the arrival counters of K splits set to zero.
+struct PrepArgs {
+  GateGradArgs gate;   // blocks 0: none
+  CopyJob copy[3];     // blocks 0: none
+  uint32_t* cnt;       // null: none
+  uint32_t ncnt;
+};
+template <int DT>
+__global__ __launch_bounds__(256) void prep_kernel(PrepArgs p) {
+  __shared__ __attribute__((aligned(16))) Tile64 t0, t1;
+  if (p.cnt)
+    for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < p.ncnt; i += gridDim.x * 256u) p.cnt[i] = 0u;
+  uint32_t b = blockIdx.x;
+  if (b < p.gate.blocks) {
+    gate_grad_tile<DT>(t0, t1, p.gate, b);
+    return;
+  }
+  b -= p.gate.blocks;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (b < p.copy[i].blocks) {
+      copy_tile(t0, p.copy[i], b);
+      return;
+    }
+    b -= p.copy[i].blocks;
+  }
 }
 
 }  // namespace gp
