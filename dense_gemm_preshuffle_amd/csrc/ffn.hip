@@ -80,19 +80,17 @@ int plan_gated(int dtype, int64_t M, int64_t F, int64_t H, GatedPlan* p) {
 // ---- backward pass of a linear layer C[M][N] = A[M][K] B[N][K]^T ----
 // da = dc b: K axis N (gated: padded, since the call makes dc).
 // db = dc^T a: K axis M, padded with zeros.
-// Up to 4095 rows both run on the tile kernel's row-major form: da reads b
-// as it is; db is computed as (a^T dc)^T, which reads dc as it is, from a
-// transposed copy of a (the smaller operand), and is stored transposed.
-// With more (or a K axis of dc that is not whole 128-byte tiles) they run on the
-// preshuffled kernels, from copies laid out for them: b^T for da, dc^T and a^T
-// for db. The copies cost bandwidth, the row-major
-// products 2 to 14% of the matrix rate, so that the copies pay off with many rows.
-// Gated backward M x F x H in us, row-major against copies: 64 x 1024 x 1024 20.9,
-// 19.6; 130 x 2064 x 2048 35, 43; 512 x 4096 x 4096 102, 121; 1024 x 8192 x 2048
-// 164, 186; 2000 x 7168 x 4096 471, 495; 4096 x 11008 x 4096 1260, 1225; 8192 x
-// 2048 x 2048 276, 264; 8192 x 14336 x 4096 3118, 2999 (copies and the pointwise
-// pass that also writes dc^T: 458 of these; the matrix unit is busy 88% of the
-// products' cycles at the 1.65 GHz that the power limit leaves).
+// Either runs on the tile kernel's row-major form: da reads b as it is; db is
+// computed as (a^T dc)^T, which reads dc as it is, from a transposed copy of a
+// (the smaller operand), and is stored transposed. Or on the preshuffled kernels,
+// from copies laid out for them: b^T for da, dc^T and a^T for db. The copies cost
+// bandwidth, the row-major products up to 14% of the matrix rate, so that the
+// copies pay off with many rows; which one, plan_rows estimates. Gated backward M
+// x F x H in us, row-major against copies: 130 x 2064 x 2048 30, 43; 512 x 4096 x
+// 4096 93, 121; 2000 x 7168 x 4096 440, 495; 4096 x 11008 x 4096 1260, 1225; 8192 x
+// 14336 x 4096 3118, 2999 (copies and the pointwise pass that also writes dc^T:
+// 458 of these; the matrix unit is busy 88% of the products' cycles at the 1.65
+// GHz that the power limit leaves).
 struct BackwardPlan {
   Plan da, db;
   bool da_rows = false, db_rows = false;
@@ -115,31 +113,38 @@ int64_t pad_k(int64_t k) {
   return (k + unit - 1) / unit * unit;
 }
 
-// Tile and K split of the row-major form for [M][K] x [K][N], by the time
-//   4 + rounds * (K tiles * step + ends) + ranges * join   (us)
-// of the workgroups on 256 CUs, whose constants come from 23 shapes timed with
-// every tile and 1 to 16 ranges on one MI355X (M 32 to 4096, K 64 to 14336): the
-// model's choice was the fastest or within 8% of it on 20. step: one 128-byte K
-// tile; ends: filling the pipeline and storing the tile; join: writing a range's
-// partial tile and the last workgroup's reading it. Tiles of 128 columns share a
-// CU by two or three, so their rounds are counted in fractions. Some of the
-// measured pairs: 2000 x 4096 x 14336 206 on 256 x 256 in two, 232 on 128 x 256;
-// 161 x 2656 x 10624 29.6 on 64 x 128 in four (39.7 in three, 35.8 in eight);
-// transposed 4096 x 14336 x 128 42 on 128 x 128, 47 on 256 x 256.
-bool plan_rows(int64_t M, int64_t N, int64_t Kb, Plan* p) {
+// Time of a product [M][K] x [K][N] on the tile kernel in us, by the model
+//   4 + rounds * (K tiles per range * step + ends) + ranges * join
+// of its workgroups on 256 CUs. The constants come from 36 shapes of the
+// row-major form timed with every tile and 1 to 16 ranges on one MI355X (M 32 to
+// 4096, K 64 to 31744); the tile and ranges it prefers were the fastest or within
+// 8% of it on 31. step: a 128-byte K tile; ends: filling the pipeline and storing
+// the tile; join: writing a range's partial tile and the last workgroup's reading
+// it. Two workgroups on a CU take as long as one after the other, so a started
+// round counts whole. Some of the pairs: 2000 x 4096 x 14336 206 on 256 x 256 in
+// two ranges, 232 on 128 x 256; 161 x 2656 x 10624 29.6 on 64 x 128 in four (39.7
+// in three, 35.8 in eight); transposed 4096 x 14336 x 128 42 on 128 x 128, 47 on
+// 256 x 256. On preshuffled operands a step takes about 0.85 of it.
+struct TileTime { int tm, tn; double step, ends, join; };
+constexpr TileTime kTileTimes[] = {{256, 256, 1.45, 10, 4.3}, {128, 256, 1.05, 5, 2.1}, {128, 128, 0.52, 2, 1.1},
+                                   {64, 128, 0.40, 2, 0.55}};
+double tile_us(const TileTime& t, int64_t M, int64_t N, int64_t Kb, int64_t ks, double speed) {
+  const double fill = (double)(((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn) * ks) / 256;
+  const double rounds = fill <= 4 ? std::ceil(fill) : fill + 0.5;
+  return 4 + rounds * ((double)Kb / 128 / ks * t.step * speed + t.ends) + (ks > 1 ? ks * t.join : 0);
+}
+
+// Tile and K ranges of the row-major form, where it is expected to take less
+// time than the preshuffled plan `other` (null: none) with `copied` bytes of
+// copies at the card's 4.9 TB/s; else false.
+bool plan_rows(int64_t M, int64_t N, int64_t Kb, const Plan* other, double copied, Plan* p) {
   if (Kb % 128) return false;   // whole K tiles
-  struct Tile { int tm, tn; double step, ends, join; };
-  static const Tile tiles[] = {{256, 256, 1.45, 10, 4.3}, {128, 256, 1.05, 5, 2.1}, {128, 128, 0.52, 2, 1.1},
-                               {64, 128, 0.40, 2, 0.55}};
-  const int64_t kt = Kb / 128;
   double best = -1;
-  for (const Tile& t : tiles) {
-    const int64_t n = ((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn);
+  for (const TileTime& t : kTileTimes) {
+    const int64_t n = ((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn), kt = Kb / 128;
     for (int64_t ks = 1; ks <= 16; ++ks) {
-      if (ks > 1 && (kt / ks < 4 || n * ks > 512)) break;
-      const double fill = (double)(n * ks) / 256;
-      const double rounds = std::max(1.0, t.tn == 128 ? fill : std::ceil(fill));
-      const double us = 4 + rounds * ((double)kt / ks * t.step + t.ends) + (ks > 1 ? ks * t.join : 0);
+      if (ks > 1 && (kt / ks < 4 || n * ks > 1024)) break;
+      const double us = tile_us(t, M, N, Kb, ks, 1.0);
       if (best >= 0 && us >= best) continue;
       best = us;
       *p = Plan();
@@ -151,6 +156,9 @@ bool plan_rows(int64_t M, int64_t N, int64_t Kb, Plan* p) {
       p->Kb = Kb;
     }
   }
+  if (!other || other->kernel != GP_KERNEL_TILE) return true;
+  for (const TileTime& t : kTileTimes)
+    if (t.tm == other->tm && t.tn == other->tn) return best <= tile_us(t, M, N, Kb, other->ks, 0.85) + copied / 4.9e6;
   return true;
 }
 
@@ -163,17 +171,25 @@ int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool
   p->Mp = pad_k(M);
   p->Np = gated ? pad_k(N) : N;
   if (!fits(p->Mp, 2 * K) || !fits(p->Np, 2 * K) || !fits(p->Mp, 2 * p->Np)) return GP_ESHAPE;
-  const bool rows = M < 4096;
   int r;
   int64_t parts = 0;
+  Plan copies;
   if (want_da) {
-    p->da_rows = rows && plan_rows(M, K, 2 * p->Np, &p->da);
-    if (!p->da_rows && (r = plan_gemm(dtype, M, K, p->Np, &p->da))) return r;
+    r = plan_gemm(dtype, M, K, p->Np, &copies);
+    p->da_rows = plan_rows(M, K, 2 * p->Np, r ? nullptr : &copies, 4.0 * p->Np * K, &p->da);
+    if (!p->da_rows) {
+      if (r) return r;
+      p->da = copies;
+    }
     parts = std::max(parts, plan_workspace(p->da, M, K));
   }
   if (want_db) {
-    p->db_rows = rows && plan_rows(K, N, 2 * p->Mp, &p->db);
-    if (!p->db_rows && (r = plan_gemm(dtype, N, K, p->Mp, &p->db))) return r;
+    r = plan_gemm(dtype, N, K, p->Mp, &copies);
+    p->db_rows = plan_rows(K, N, 2 * p->Mp, r ? nullptr : &copies, (gated ? 2.0 : 4.0) * p->Mp * N, &p->db);
+    if (!p->db_rows) {
+      if (r) return r;
+      p->db = copies;
+    }
     parts = std::max(parts, p->db_rows ? plan_workspace(p->db, K, N) : plan_workspace(p->db, N, K));
   }
   int64_t at = p->parts = align256(parts);
