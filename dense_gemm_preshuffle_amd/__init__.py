@@ -488,9 +488,10 @@ def gemm_gated_preshuffle(w, dtype, out=None, stream=None):
     if F2 % 2:
         raise ValueError("gemm_gated_preshuffle: w holds F gate rows and F up rows")
     _want("gemm_gated_preshuffle: w", w, (F2, H), t)
+    n = 2 * F2 * (-(-H // 64) * 64)    # K is filled up to whole 128-byte tiles
     if out is None:
-        out = torch.empty(2 * F2 * H, dtype=torch.uint8, device=w.device)
-    _want("gemm_gated_preshuffle: out", out, (2 * F2 * H,), torch.uint8, w.device)
+        out = torch.empty(n, dtype=torch.uint8, device=w.device)
+    _want("gemm_gated_preshuffle: out", out, (n,), torch.uint8, w.device)
     _check(load_library().gemm_gated_preshuffle(_ptr(w), _ptr(out), F2 // 2, H, dt, _stream(stream)),
            "gemm_gated_preshuffle")
     return out
@@ -518,9 +519,10 @@ def gemm_gated(dtype, x, w_shuf, act="silu", save=False, h=None, gate=None, up=N
 
     dt, t = _half(dtype)
     M, H = x.shape
-    F = _nbytes(w_shuf) // (4 * H) if H else 0
+    Hp = -(-H // 64) * 64
+    F = _nbytes(w_shuf) // (4 * Hp) if H else 0
     _want("gemm_gated: x", x, (M, H), t)
-    _want("gemm_gated: w_shuf", w_shuf, (4 * F * H,), torch.uint8, x.device)
+    _want("gemm_gated: w_shuf", w_shuf, (4 * F * Hp,), torch.uint8, x.device)
     with _on(stream, x.device):
         h = torch.empty(M, F, dtype=t, device=x.device) if h is None else h
         if save:

@@ -943,7 +943,7 @@ int launch(int in_dtype, const Plan& p, const void* a, const void* b, const void
     t.xcd = p.xcd == 1 ? 1u : 0u;
     t.act = act;
     t.gate = t.up = nullptr;
-    t.kb_rows = t.ldb = 0;
+    t.ka = t.kb_rows = t.ldb = 0;
     t.ksplit = (uint32_t)p.ks;
     t.cnt = p.ks > 1 ? (uint32_t*)ws : nullptr;
     t.part = p.ks > 1 ? (char*)ws + kCounterBytes : nullptr;

@@ -25,7 +25,8 @@ struct GatedArgs {
   char* c;            // [M][F]
   char* gate;         // [M][F] products to keep, or null
   char* up;
-  uint32_t M, F, Kb;  // Kb = bytes per row of K
+  uint32_t M, F;
+  uint32_t Ka, Kb;    // bytes of K per row of x, and of the weights (whole 128-byte chunks, zeros past Ka)
   int act;            // Act
 };
 
@@ -45,7 +46,7 @@ __global__ __launch_bounds__(WAVES * 64) void gated_small_kernel(GatedArgs p) {
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lane = tid & 63, lane_lo = lane & 15, lane_hi = lane >> 4;
-  const uint32_t Kb = p.Kb;
+  const uint32_t Ka = p.Ka, Kb = p.Kb;
   // each XCD takes a contiguous run of column blocks (whole lines of h per L2)
   const uint32_t pairs = p.F / 16, cols = (pairs + P - 1) / P;
   uint32_t bx = blockIdx.x % cols;
@@ -54,12 +55,12 @@ __global__ __launch_bounds__(WAVES * 64) void gated_small_kernel(GatedArgs p) {
   const uint32_t npair = min((uint32_t)P, pairs - pair0);   // real pairs of this workgroup
   const uint32_t m0 = blockIdx.x / cols * ROWS;
   const uint32_t mrows = min((uint32_t)ROWS, p.M - m0);
-  const uint32_t nchunk = (Kb + 127) / 128;
+  const uint32_t nchunk = Kb / 128;
   const uint32_t kc0 = (uint32_t)wave * nchunk / WAVES, kc1 = (uint32_t)(wave + 1) * nchunk / WAVES;
   const int groups = (int)((kc1 - kc0 + S - 1) / S);
 
   // rows past M and blocks past the last pair lie outside their resources
-  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + (size_t)m0 * Kb, mrows * Kb);
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + (size_t)m0 * Ka, mrows * Ka);
   const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.b + (size_t)pair0 * 32 * Kb, npair * 32 * Kb);
   constexpr uint32_t kOOB = 0x80000000u;
   // x load i of a lane: 16-byte piece lane % 8 of row 8 i + lane / 8. Piece c of
@@ -67,7 +68,7 @@ __global__ __launch_bounds__(WAVES * 64) void gated_small_kernel(GatedArgs p) {
   // MFMA operand reads together, lie in different banks.
   char* xw = lds + wave * XW;
   const uint32_t xcol = ONE ? 4 * lane : 16 * (lane & 7);
-  const uint32_t x_off = ONE ? (lane < 32 ? xcol : kOOB) : (lane >> 3) * Kb + xcol;
+  const uint32_t x_off = ONE ? (lane < 32 ? xcol : kOOB) : (lane >> 3) * Ka + xcol;
 
   v4i xr[2][S][XL > 0 ? XL : 1], bf[2][S][2][NB];
   v4f acc[MB][NB];
@@ -83,16 +84,15 @@ __global__ __launch_bounds__(WAVES * 64) void gated_small_kernel(GatedArgs p) {
     for (int s = 0; s < S; ++s) {
       const uint32_t k = kc0 + (uint32_t)gr * S + s;
       const uint32_t skip = S == 1 || k < kc1 ? 0u : kOOB;   // uniform
-      const uint32_t skip1 = (S == 1 || k < kc1) && 128 * k + 64 < Kb ? 0u : kOOB;   // second half past K
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         bf[par][s][0][nb] = buf_load16_nt(rb, (nb * 16 * Kb + lane * 16) | skip, k * 2048);
-        bf[par][s][1][nb] = buf_load16_nt(rb, (nb * 16 * Kb + lane * 16 + 1024) | skip1, k * 2048);
+        bf[par][s][1][nb] = buf_load16_nt(rb, (nb * 16 * Kb + lane * 16 + 1024) | skip, k * 2048);
       }
-      const uint32_t xo = (128 * k + xcol < Kb ? x_off : kOOB) | skip;
+      const uint32_t xo = (128 * k + xcol < Ka ? x_off : kOOB) | skip;
       if constexpr (ONE) xr[par][s][0][0] = buf_load4(ra, xo, 128 * k);
 #pragma unroll
-      for (int i = 0; i < XL; ++i) xr[par][s][i] = buf_load16(ra, xo + 8 * i * Kb, 128 * k);
+      for (int i = 0; i < XL; ++i) xr[par][s][i] = buf_load16(ra, xo + 8 * i * Ka, 128 * k);
     }
   };
   auto compute = [&](auto par_c) GP_INLINE {

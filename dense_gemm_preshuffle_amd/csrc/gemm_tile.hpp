@@ -52,6 +52,7 @@ struct TileArgs {
   int act;            // Act
   char* gate;         // EPI_GATED: [M][N/2] gate and up products to keep, or null
   char* up;
+  uint32_t ka;        // EPI_GATED, EPI_ROWS: bytes per row of A (at most Kb; K past them reads zeros)
   uint32_t kb_rows, ldb;  // EPI_ROWS: rows of B (K, below 16-bit elements of Kb: the rest are zeros), bytes per row
   // K split across workgroups (tile kernel): ksplit workgroups share each
   // tile, each taking a contiguous range of its K tiles; their partial sums
@@ -312,7 +313,10 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
     edge_shift(n0, nskip, TN, p.N);
   }
   const uint32_t Kb = p.Kb;
-  const uint32_t Ka = Kb * C::AKB;   // bytes per row of A
+  // bytes per row of A; AMASK: K is filled up to whole tiles beside A, whose
+  // rows end earlier
+  constexpr bool AMASK = C::ROWS || EPI == EPI_GATED;
+  const uint32_t Ka = AMASK ? p.ka : Kb * C::AKB;
   // K tiles of this workgroup: split kz of ksplit equal ranges; of this group:
   // [kt0, kt0 + KT) (the planner makes ksplit * KG divide the K tiles). With a
   // row-major B the ranges may differ by a tile.
@@ -373,6 +377,8 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
     }
   }
   static_assert(!C::ASYNC || RPD * C::ALOADS == TM, "LDS DMA covers the A tile");
+  // byte of K (in the tile) of this lane's chunks
+  const uint32_t a_col = (((wave * 64 + lane) % C::CPR) ^ (((wave * 64 + lane) / C::CPR / C::SWP) & C::SWM)) * 16;
   // A K byte (within one MFMA step) of the lane's 16-byte piece f. W4A8: the
   // B piece of lane group g holds K elements [32g, 32g+32) of the step's 128,
   // its low nibbles the first 16 (first MFMA), its high nibbles the rest.
@@ -454,7 +460,10 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
     for (int ni = 0; ni < C::NACC; ++ni) acc[mi][ni] = Acc{};
 
   auto load_a = [&](int kt, int i) GP_INLINE {
-    if constexpr (!C::ASYNC) a_st[i] = buf_load16(ra, a_on(i) ? a_ld0 : kOOB, kt * C::TKA + i * RPP * Ka);
+    if constexpr (!C::ASYNC) {
+      const bool on = a_on(i) && (!AMASK || (uint32_t)(kt * C::TKA + ach * 16) < Ka);
+      a_st[i] = buf_load16(ra, on ? a_ld0 : kOOB, kt * C::TKA + i * RPP * Ka);
+    }
   };
   auto store_a = [&](int par) GP_INLINE {
     if constexpr (C::ASYNC) return;
@@ -464,9 +473,14 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
       *(v4i*)(base + (a_on(i) ? a_wr_off(i) : (uint32_t)(TM * C::TKA))) = a_st[i];
   };
   auto load_a_dma = [&](int stage, int kt, int i) GP_INLINE {
-    if constexpr (C::ASYNC)
-      lds_dma16(p.a + (size_t)m0 * Ka, a_rows * Ka, glds + stage * C::ABUF + (i * C::WAVES + wave) * 1024,
-                (DMA_STEP ? a_dma[0] + i * RPD * Ka : a_dma[DMA_STEP ? 0 : i]) + kt * C::TKA);
+    if constexpr (C::ASYNC) {
+      uint32_t off = (DMA_STEP ? a_dma[0] + i * RPD * Ka : a_dma[DMA_STEP ? 0 : i]) + kt * C::TKA;
+      if constexpr (AMASK) {
+        static_assert(DMA_STEP, "one column per lane");
+        if (!(a_col + kt * C::TKA < Ka)) off = kOOB;
+      }
+      lds_dma16(p.a + (size_t)m0 * Ka, a_rows * Ka, glds + stage * C::ABUF + (i * C::WAVES + wave) * 1024, off);
+    }
   };
   // B load q of a tile: K step q / (NACC*FRAG), column block (q / FRAG) % NACC, piece q % FRAG
   auto load_b = [&](auto par_c, int kt, int q) GP_INLINE {

@@ -4,6 +4,6 @@
 
 namespace gp {
 
-GP_DEFINE_GATED(bf16, DT_BF16, GP_TILE_GATED_BF16, GP_TILE_GATED_KSPLIT_BF16)
+GP_DEFINE_GATED(bf16, DT_BF16)
 
 }  // namespace gp

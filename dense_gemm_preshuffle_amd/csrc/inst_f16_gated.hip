@@ -4,6 +4,6 @@
 
 namespace gp {
 
-GP_DEFINE_GATED(f16, DT_F16, GP_TILE_GATED_F16, GP_TILE_GATED_KSPLIT_F16)
+GP_DEFINE_GATED(f16, DT_F16)
 
 }  // namespace gp

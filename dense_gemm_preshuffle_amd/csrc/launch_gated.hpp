@@ -35,10 +35,10 @@ hipError_t launch_gated_small_f16(const GatedSmall& v, const GatedArgs& a, hipSt
     hipLaunchKernelGGL((gated_small_kernel<DT, XL, P, W, S>), grid, dim3(W * 64), 0, s, a);                    \
     return hipGetLastError();                                                                                  \
   }
-#define GP_DEFINE_GATED(NAME, DT, TILES, KSPLIT)                                                               \
+#define GP_DEFINE_GATED(NAME, DT)                                                                              \
   hipError_t launch_gated_tile_##NAME(int tm, int tn, int tkb, int pipe, const TileArgs& a, hipStream_t s) {   \
-    TILES(GP_GATED_CASE)                                                                                       \
-    KSPLIT(GP_GATED_CASE_KSPLIT)                                                                               \
+    GP_TILE_GATED(GP_GATED_CASE, DT)                                                                           \
+    GP_TILE_GATED_KSPLIT(GP_GATED_CASE_KSPLIT, DT)                                                             \
     return hipErrorInvalidValue;                                                                               \
   }                                                                                                            \
   hipError_t launch_gated_small_##NAME(const GatedSmall& v, const GatedArgs& a, hipStream_t s) {               \

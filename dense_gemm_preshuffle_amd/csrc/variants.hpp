@@ -140,15 +140,12 @@
   GP_SPLITK_I8(Y) GP_SPLITK_FP8(Y) GP_SPLITK_BF16(Y) GP_SPLITK_FP4(Y) GP_SPLITK_F16(Y) GP_SPLITK_I4(Y)
 #define GP_WIDE_ALL(W) GP_WIDE_I8(W) GP_WIDE_FP8(W) GP_WIDE_BF16(W) GP_WIDE_FP4(W) GP_WIDE_F16(W)
 
-// Gated epilogue (BF16 / FP16): the tiles the planner picks for these types
-// (16 x 16 blocks; see the lists above), in the same fields.
-#define GP_TILE_GATED_COMMON(X, DT) \
-  X(DT, 16, 32, 128, 128, 0) X(DT, 16, 128, 256, 64, 0) X(DT, 16, 256, 256, 128, 3) X(DT, 16, 128, 512, 128, 3) \
-  X(DT, 16, 128, 256, 128, 3) X(DT, 16, 64, 256, 128, 3) X(DT, 16, 128, 128, 128, 3) X(DT, 16, 64, 128, 128, 3)
-#define GP_TILE_GATED_BF16(X) GP_TILE_GATED_COMMON(X, DT_BF16)
-#define GP_TILE_GATED_F16(X) GP_TILE_GATED_COMMON(X, DT_F16) X(DT_F16, 16, 64, 128, 64, 0)
-#define GP_TILE_GATED_KSPLIT_BF16(X) X(DT_BF16, 16, 128, 256, 128, 3) X(DT_BF16, 16, 64, 128, 128, 0)
-#define GP_TILE_GATED_KSPLIT_F16(X) X(DT_F16, 16, 128, 256, 128, 3) X(DT_F16, 16, 64, 128, 128, 0)
+// Gated epilogue (BF16 / FP16): the tiles the planner picks for these types and
+// whole 128-byte K tiles (16 x 16 blocks; see the lists above), in the same fields.
+#define GP_TILE_GATED(X, DT) \
+  X(DT, 16, 32, 128, 128, 0) X(DT, 16, 256, 256, 128, 3) X(DT, 16, 128, 256, 128, 3) \
+  X(DT, 16, 64, 256, 128, 3) X(DT, 16, 128, 128, 128, 3) X(DT, 16, 64, 128, 128, 3)
+#define GP_TILE_GATED_KSPLIT(X, DT) X(DT, 16, 128, 256, 128, 3) X(DT, 16, 64, 128, 128, 0)
 
 // Row-major B (BF16 / FP16, 16 x 16 blocks, 128-byte K tiles): X(dtype,
 // epilogue, tile_m, tile_n, stages, able to split K across workgroups). Three

@@ -358,9 +358,10 @@ int gemm_plan_ws(int in_dtype, int64_t M, int64_t N, int64_t K, const gemm_opts*
  * free, F % 16 == 0, H % 32 == 0 (else GP_ESHAPE), every matrix below 2^31
  * bytes; the buffers of one type (GP_BF16 or GP_F16, else GP_EDTYPE).
  *
- * gemm_gated_preshuffle -- w [2F][H] -> w_shuf (4 F H bytes, no overlap): the
- * layout of gemm_preshuffle_b with 16-row blocks of gate and up alternating,
- * so that one lane of a product ends up with both factors of its outputs.
+ * gemm_gated_preshuffle -- w [2F][H] -> w_shuf (4 F H' bytes, H' = H rounded up
+ * to a multiple of 64; no overlap): the layout of gemm_preshuffle_b with 16-row
+ * blocks of gate and up alternating, so that one lane of a product ends up with
+ * both factors of its outputs, and zeros from H to H'.
  */
 int gemm_gated_preshuffle(const void* w, void* w_shuf, int64_t F, int64_t H, int dtype, void* stream);
 
