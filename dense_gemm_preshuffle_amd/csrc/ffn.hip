@@ -30,6 +30,57 @@ __global__ __launch_bounds__(256) void preshuffle_gated_kernel(const char* __res
   *(v4i*)(dst + (size_t)x * 16u) = col < Ka ? *(const v4i*)(w + (size_t)row * Ka + col) : v4i{0, 0, 0, 0};
 }
 
+// ---- tiles ----
+// Time of a product [M][K] x [K][N] on the tile kernel in us, by the model
+//   start + rounds * (K tiles per range * step + ends) + ranges * join
+// of its workgroups on 256 CUs. step: a 128-byte K tile; ends: filling the
+// pipeline and storing the tile; join: writing a range's partial tile and the last
+// workgroup's reading it. Two workgroups on a CU take as long as one after the
+// other, so a started round counts whole. The constants come from timing every
+// tile with 1 to 16 ranges on one MI355X:
+//   row-major B: 36 shapes (M 32 to 4096, K 64 to 31744); the choice was the
+//     fastest or within 8% of it on 31. 2000 x 4096 x 14336 206 on 256 x 256 in two
+//     ranges, 232 on 128 x 256; 161 x 2656 x 10624 29.6 on 64 x 128 in four (39.7 in
+//     three, 35.8 in eight); transposed 4096 x 14336 x 128 42 on 128 x 128, 47 on
+//     256 x 256.
+//   gated: 14 shapes (M 70 to 7133, K 320 to 8192); within 5% on 13. 259 x 4384 x
+//     6592 37.0 on 128 x 256 in four ranges, 38.8 on 128 x 128 in two; 509 x 14336 x
+//     4096 57.8 on 128 x 256, 62.4 on 128 x 128, 63.1 on 256 x 256 in two; 1910 x
+//     10720 x 448 25.6 on 128 x 128, 34.3 on 256 x 256.
+struct TileTime { int tm, tn; double step, ends, join; };
+constexpr TileTime kRowsTimes[] = {{256, 256, 1.45, 10, 4.3}, {128, 256, 1.05, 5, 2.1}, {128, 128, 0.52, 2, 1.1},
+                                   {64, 128, 0.40, 2, 0.55}};
+constexpr TileTime kGatedTimes[] = {{256, 256, 1.15, 9, 4.3}, {128, 256, 0.75, 4, 2.6}, {128, 128, 0.5, 1.5, 1.2},
+                                    {64, 128, 0.38, 1, 0.8}};
+double tile_us(const TileTime& t, int64_t M, int64_t N, int64_t Kb, int64_t ks, double speed = 1.0) {
+  const double fill = (double)(((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn) * ks) / 256;
+  const double rounds = fill <= 4 ? std::ceil(fill) : fill + 0.5;
+  return 3.5 + rounds * ((double)Kb / 128 / ks * t.step * speed + t.ends) + (ks > 1 ? ks * t.join : 0);
+}
+// The tile and K ranges of least time, and that time; below 0 if no tile fits.
+// inside: tiles no larger than the matrix.
+double choose_tile_us(const TileTime (&times)[4], int64_t M, int64_t N, int64_t Kb, bool inside, Plan* p) {
+  double best = -1;
+  for (const TileTime& t : times) {
+    if (inside && (t.tm > M || t.tn > N)) continue;
+    const int64_t n = ((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn), kt = Kb / 128;
+    for (int64_t ks = 1; ks <= 16; ++ks) {
+      if (ks > 1 && (kt / ks < 4 || n * ks > 1024)) break;
+      const double us = tile_us(t, M, N, Kb, ks);
+      if (best >= 0 && us >= best) continue;
+      best = us;
+      *p = Plan();
+      p->kernel = GP_KERNEL_TILE;
+      p->tm = t.tm;
+      p->tn = t.tn;
+      p->tkb = 128;
+      p->ks = (int)ks;
+      p->Kb = Kb;
+    }
+  }
+  return best;
+}
+
 // ---- gated product ----
 struct GatedPlan {
   bool small = false;   // gated_small_kernel, else the tile kernel
@@ -50,10 +101,8 @@ int check_gated(int dtype, int64_t M, int64_t F, int64_t H) {
   return GP_OK;
 }
 
-// Up to 64 rows, and above wherever the GEMM planner takes its small-M
-// kernel for [M][2F] outputs, the small gated kernel; otherwise the planner's
-// tile (every one it picks for these types has the gated epilogue, except the
-// 16-column waves of 16 x 64, a small-M shape).
+// Up to 64 rows, and above where no tile fits into [M][2F], the small gated
+// kernel; otherwise a tile.
 // Variants of the small kernel, F x H of 14336 x 4096 (896 pairs of column
 // blocks), 7184 x 4096 (449) and 4096 x 4096 (256) unless named, us on one
 // MI355X: up to 16 rows single pairs on 8 waves (1 x 7168 x 2048 10.8, pairs by
@@ -67,10 +116,7 @@ int plan_gated(int dtype, int64_t M, int64_t F, int64_t H, GatedPlan* p) {
   const int r = check_gated(dtype, M, F, H);
   if (r) return r;
   p->small = M <= 64;
-  if (!p->small) {
-    const int rc = plan_gemm(dtype, M, 2 * F, whole_k(H), &p->tile);
-    p->small = rc != GP_OK || p->tile.kernel != GP_KERNEL_TILE || p->tile.tn < 128;
-  }
+  if (!p->small) p->small = choose_tile_us(kGatedTimes, M, 2 * F, 2 * whole_k(H), true, &p->tile) < 0;
   if (p->small) {
     GatedSmall& v = p->variant;
     const int64_t pairs = F / 16;
@@ -118,51 +164,15 @@ int64_t pad_k(int64_t k) {
   return (k + unit - 1) / unit * unit;
 }
 
-// Time of a product [M][K] x [K][N] on the tile kernel in us, by the model
-//   4 + rounds * (K tiles per range * step + ends) + ranges * join
-// of its workgroups on 256 CUs. The constants come from 36 shapes of the
-// row-major form timed with every tile and 1 to 16 ranges on one MI355X (M 32 to
-// 4096, K 64 to 31744); the tile and ranges it prefers were the fastest or within
-// 8% of it on 31. step: a 128-byte K tile; ends: filling the pipeline and storing
-// the tile; join: writing a range's partial tile and the last workgroup's reading
-// it. Two workgroups on a CU take as long as one after the other, so a started
-// round counts whole. Some of the pairs: 2000 x 4096 x 14336 206 on 256 x 256 in
-// two ranges, 232 on 128 x 256; 161 x 2656 x 10624 29.6 on 64 x 128 in four (39.7
-// in three, 35.8 in eight); transposed 4096 x 14336 x 128 42 on 128 x 128, 47 on
-// 256 x 256. On preshuffled operands a step takes about 0.85 of it.
-struct TileTime { int tm, tn; double step, ends, join; };
-constexpr TileTime kTileTimes[] = {{256, 256, 1.45, 10, 4.3}, {128, 256, 1.05, 5, 2.1}, {128, 128, 0.52, 2, 1.1},
-                                   {64, 128, 0.40, 2, 0.55}};
-double tile_us(const TileTime& t, int64_t M, int64_t N, int64_t Kb, int64_t ks, double speed) {
-  const double fill = (double)(((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn) * ks) / 256;
-  const double rounds = fill <= 4 ? std::ceil(fill) : fill + 0.5;
-  return 4 + rounds * ((double)Kb / 128 / ks * t.step * speed + t.ends) + (ks > 1 ? ks * t.join : 0);
-}
-
 // Tile and K ranges of the row-major form, where it is expected to take less
 // time than the preshuffled plan `other` (null: none) with `copied` bytes of
-// copies at the card's 4.9 TB/s; else false.
+// copies at the card's 4.9 TB/s; else false. On preshuffled operands a step takes
+// about 0.85 of the row-major one.
 bool plan_rows(int64_t M, int64_t N, int64_t Kb, const Plan* other, double copied, Plan* p) {
-  double best = -1;
-  for (const TileTime& t : kTileTimes) {
-    const int64_t n = ((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn), kt = Kb / 128;
-    for (int64_t ks = 1; ks <= 16; ++ks) {
-      if (ks > 1 && (kt / ks < 4 || n * ks > 1024)) break;
-      const double us = tile_us(t, M, N, Kb, ks, 1.0);
-      if (best >= 0 && us >= best) continue;
-      best = us;
-      *p = Plan();
-      p->kernel = GP_KERNEL_TILE;
-      p->tm = t.tm;
-      p->tn = t.tn;
-      p->tkb = 128;
-      p->ks = (int)ks;
-      p->Kb = Kb;
-    }
-  }
+  const double us = choose_tile_us(kRowsTimes, M, N, Kb, false, p);
   if (!other || other->kernel != GP_KERNEL_TILE) return true;
-  for (const TileTime& t : kTileTimes)
-    if (t.tm == other->tm && t.tn == other->tn) return best <= tile_us(t, M, N, Kb, other->ks, 0.85) + copied / 4.9e6;
+  for (const TileTime& t : kRowsTimes)
+    if (t.tm == other->tm && t.tn == other->tn) return us <= tile_us(t, M, N, Kb, other->ks, 0.85) + copied / 4.9e6;
   return true;
 }
 
@@ -384,8 +394,8 @@ int gemm_gated(int dtype, const void* x, const void* w_shuf, int act, void* h, v
     t.ksplit = (uint32_t)p.tile.ks;
     t.cnt = p.tile.ks > 1 ? (uint32_t*)workspace : nullptr;
     t.part = p.tile.ks > 1 ? (char*)workspace + kCounterBytes : nullptr;
-    e = dtype == GP_BF16 ? launch_gated_tile_bf16(p.tile.tm, p.tile.tn, p.tile.tkb, p.tile.pipe, t, s)
-                         : launch_gated_tile_f16(p.tile.tm, p.tile.tn, p.tile.tkb, p.tile.pipe, t, s);
+    e = dtype == GP_BF16 ? launch_gated_tile_bf16(p.tile.tm, p.tile.tn, t, s)
+                         : launch_gated_tile_f16(p.tile.tm, p.tile.tn, t, s);
   }
   return report_hip(e, "kernel launch");
 }

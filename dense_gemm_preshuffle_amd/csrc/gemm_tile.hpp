@@ -319,11 +319,12 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
   const uint32_t Ka = AMASK ? p.ka : Kb * C::AKB;
   // K tiles of this workgroup: split kz of ksplit equal ranges; of this group:
   // [kt0, kt0 + KT) (the planner makes ksplit * KG divide the K tiles). With a
-  // row-major B the ranges may differ by a tile.
+  // row-major B or the gated epilogue the ranges may differ by a tile.
+  constexpr bool UNEVEN = C::ROWS || EPI == EPI_GATED;
   const int KALL = (int)(Kb / TKB);
   const int KTS = KALL / (KS ? (int)p.ksplit : 1);
-  const int kr0 = KS && C::ROWS ? (int)kz * KALL / (int)p.ksplit : (int)kz * KTS;
-  const int KT = (KS && C::ROWS ? ((int)kz + 1) * KALL / (int)p.ksplit - kr0 : KTS) / KG;
+  const int kr0 = KS && UNEVEN ? (int)kz * KALL / (int)p.ksplit : (int)kz * KTS;
+  const int KT = (KS && UNEVEN ? ((int)kz + 1) * KALL / (int)p.ksplit - kr0 : KTS) / KG;
   const int kt0 = __builtin_amdgcn_readfirstlane(kr0 + grp * KT);
 
   // Buffer resources based at this workgroup's first A row / first B block.

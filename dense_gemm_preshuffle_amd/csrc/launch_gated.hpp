@@ -13,21 +13,20 @@ struct GatedSmall {
 };
 
 // Each returns hipErrorInvalidValue if the variant is not compiled.
-hipError_t launch_gated_tile_bf16(int tm, int tn, int tkb, int pipe, const TileArgs& a, hipStream_t s);
-hipError_t launch_gated_tile_f16(int tm, int tn, int tkb, int pipe, const TileArgs& a, hipStream_t s);
+hipError_t launch_gated_tile_bf16(int tm, int tn, const TileArgs& a, hipStream_t s);
+hipError_t launch_gated_tile_f16(int tm, int tn, const TileArgs& a, hipStream_t s);
 hipError_t launch_gated_small_bf16(const GatedSmall& v, const GatedArgs& a, hipStream_t s);
 hipError_t launch_gated_small_f16(const GatedSmall& v, const GatedArgs& a, hipStream_t s);
 
 }  // namespace gp
 
-#define GP_GATED_CASE_IMPL(DT, MS, TM, TN, TKB, PIPE, KSV)                                                     \
-  if (tm == TM && tn == TN && tkb == TKB && pipe == PIPE && (a.ksplit > 1) == KSV) {                           \
-    hipLaunchKernelGGL((gemm_tile_kernel<DT, MS, TM, TN, TKB, EPI_GATED, PIPE, false, 1, true, KSV>),          \
+#define GP_GATED_CASE_IMPL(DT, TM, TN, KSV)                                                                    \
+  if (tm == TM && tn == TN && (a.ksplit > 1) == KSV) {                                                         \
+    hipLaunchKernelGGL((gemm_tile_kernel<DT, 16, TM, TN, 128, EPI_GATED, 3, false, 1, true, KSV>),             \
                        dim3(a.tiles_m * a.tiles_n * a.ksplit), dim3(64 * tile_waves(TM, TN)), 0, s, a);        \
     return hipGetLastError();                                                                                  \
   }
-#define GP_GATED_CASE(DT, MS, TM, TN, TKB, PIPE) GP_GATED_CASE_IMPL(DT, MS, TM, TN, TKB, PIPE, false)
-#define GP_GATED_CASE_KSPLIT(DT, MS, TM, TN, TKB, PIPE) GP_GATED_CASE_IMPL(DT, MS, TM, TN, TKB, PIPE, true)
+#define GP_GATED_CASE(DT, TM, TN) GP_GATED_CASE_IMPL(DT, TM, TN, false) GP_GATED_CASE_IMPL(DT, TM, TN, true)
 #define GP_GATED_SMALL_CASE(DT, XL, P, W, S)                                                                   \
   if (v.xl == XL && v.pairs == P && v.waves == W && v.s == S) {                                                \
     constexpr uint32_t rows = XL == 0 ? 1 : 8 * XL;                                                            \
@@ -36,9 +35,8 @@ hipError_t launch_gated_small_f16(const GatedSmall& v, const GatedArgs& a, hipSt
     return hipGetLastError();                                                                                  \
   }
 #define GP_DEFINE_GATED(NAME, DT)                                                                              \
-  hipError_t launch_gated_tile_##NAME(int tm, int tn, int tkb, int pipe, const TileArgs& a, hipStream_t s) {   \
+  hipError_t launch_gated_tile_##NAME(int tm, int tn, const TileArgs& a, hipStream_t s) {                      \
     GP_TILE_GATED(GP_GATED_CASE, DT)                                                                           \
-    GP_TILE_GATED_KSPLIT(GP_GATED_CASE_KSPLIT, DT)                                                             \
     return hipErrorInvalidValue;                                                                               \
   }                                                                                                            \
   hipError_t launch_gated_small_##NAME(const GatedSmall& v, const GatedArgs& a, hipStream_t s) {               \

@@ -140,12 +140,9 @@
   GP_SPLITK_I8(Y) GP_SPLITK_FP8(Y) GP_SPLITK_BF16(Y) GP_SPLITK_FP4(Y) GP_SPLITK_F16(Y) GP_SPLITK_I4(Y)
 #define GP_WIDE_ALL(W) GP_WIDE_I8(W) GP_WIDE_FP8(W) GP_WIDE_BF16(W) GP_WIDE_FP4(W) GP_WIDE_F16(W)
 
-// Gated epilogue (BF16 / FP16): the tiles the planner picks for these types and
-// whole 128-byte K tiles (16 x 16 blocks; see the lists above), in the same fields.
-#define GP_TILE_GATED(X, DT) \
-  X(DT, 16, 32, 128, 128, 0) X(DT, 16, 256, 256, 128, 3) X(DT, 16, 128, 256, 128, 3) \
-  X(DT, 16, 64, 256, 128, 3) X(DT, 16, 128, 128, 128, 3) X(DT, 16, 64, 128, 128, 3)
-#define GP_TILE_GATED_KSPLIT(X, DT) X(DT, 16, 128, 256, 128, 3) X(DT, 16, 64, 128, 128, 0)
+// Gated epilogue (BF16 / FP16, 16 x 16 blocks, 128-byte K tiles, 3 stages): X(dtype,
+// tile_m, tile_n), each with and without a K split across workgroups.
+#define GP_TILE_GATED(X, DT) X(DT, 256, 256) X(DT, 128, 256) X(DT, 128, 128) X(DT, 64, 128)
 
 // Row-major B (BF16 / FP16, 16 x 16 blocks, 128-byte K tiles): X(dtype,
 // epilogue, tile_m, tile_n, stages, able to split K across workgroups). Three
