@@ -29,6 +29,7 @@ points have the names of the C ABI (include/gemm_preshuffle.h):
     gemm_w4a16_preshuffle(q, scales, zeros, group)   -> W4Weights, 4-bit weights laid out with their scales
     gemm_w4a16(x, weights, bias, act)                -> act(x W^T + bias) (BF16 / FP16 activations)
     gemm_w4a16_gated(x, weights, act)                -> act(x Wg^T) * (x Wu^T) on 4-bit weights
+    w4a16_workspace(M, weights)                      -> a device workspace of these (None: none needed)
 
 Tensors: A is [M, K] (INT8 / FP8 as any 1-byte dtype, BF16 / FP16 as
 bfloat16 / float16 or a 2-byte integer view, MXFP4 as uint8 [M, K/2]; W4A8:
@@ -51,7 +52,7 @@ __all__ = [
     "gemm_gated_preshuffle", "gemm_gated", "gemm_gated_workspace_size", "gated_workspace", "gemm_gated_backward",
     "gemm_gated_backward_workspace_size", "gated_backward_workspace", "gemm_backward", "gemm_backward_workspace_size",
     "backward_workspace", "W4Weights", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle", "gemm_w4a16",
-    "gemm_w4a16_gated", "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE",
+    "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "w4a16_workspace", "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE",
     "KERNEL_SPLITK", "KERNEL_WIDE",
 ]
 
@@ -157,6 +158,8 @@ def load_library():
     lib.gemm_w4a16_preshuffle.argtypes = [ci, vp, vp, vp, vp, i64, i64, ci, ci, vp]
     lib.gemm_w4a16.argtypes = [ci, vp, vp, ci, vp, ci, vp, i64, i64, i64, ci, vp]
     lib.gemm_w4a16_gated.argtypes = [ci, vp, vp, ci, ci, vp, i64, i64, i64, ci, vp]
+    lib.gemm_w4a16_workspace_size.argtypes = [i64, i64, i64, ci, ci, psz]
+    lib.gemm_w4a16_ws.argtypes = [ci, vp, vp, ci, vp, ci, vp, i64, i64, i64, ci, ci, vp, sz, vp]
     lib.gemm_status_string.argtypes = [ci]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_last_hip_error.argtypes = []
@@ -167,7 +170,7 @@ def load_library():
               "gemm_plan", "gemm_plan_ws", "gemm_workspace_size", "gemm_ex_ws", "gemm_ex_noalloc", "gemm_gated_preshuffle", "gemm_gated",
               "gemm_gated_workspace_size", "gemm_gated_backward", "gemm_gated_backward_workspace_size",
               "gemm_backward", "gemm_backward_workspace_size", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle",
-              "gemm_w4a16", "gemm_w4a16_gated"):
+              "gemm_w4a16", "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "gemm_w4a16_ws"):
         getattr(lib, f).restype = ci
     _lib = lib
     return lib
@@ -683,26 +686,52 @@ def _w4_check(where, x, weights, y, bias, gated):
         _want(f"{where}: bias", bias, (weights.N,), torch.float32, weights.device)
 
 
-def gemm_w4a16(x, weights: W4Weights, bias=None, act="none", y=None, stream=None):
-    """y = act(x W^T + bias) on 4-bit weights: x [M, K] of the scales' type, bias fp32 [N] or None."""
-    _w4_check("gemm_w4a16", x, weights, y, bias, False)
+def gemm_w4a16_workspace_size(M: int, N: int, K: int, group: int, gated=False) -> int:
+    """Host-only: workspace bytes with which a 4-bit product of these sizes (gated: N is F) may split K
+    across workgroups (0: it does not)."""
+    return _size("gemm_w4a16_workspace_size", M, N, K, group, int(gated))
+
+
+def w4a16_workspace(M: int, weights: W4Weights):
+    """A zero-filled device workspace for products of M rows on these weights (None when none is needed).
+    Zero once here; every call leaves its counters zero again. Calls that may overlap need one each."""
+    import torch
+
+    n = gemm_w4a16_workspace_size(M, weights.N, weights.K, weights.group, weights.gated)
+    return torch.zeros(n, dtype=torch.uint8, device=weights.device) if n else None
+
+
+def _w4_run(where, x, weights, bias, act, y, workspace, stream):
     M, N = x.shape[0], weights.N
     with _on(stream, weights.device):
         if y is None:
             y = x.new_empty((M, N))
-        _check(_lib.gemm_w4a16(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros, _ptr(bias),
-                               _act(act), y.data_ptr(), M, N, weights.K, weights.group, _stream(stream)), "gemm_w4a16")
+        if workspace is None and M > 16 and weights.K > 8192:
+            # else a split saves no more than making and clearing a workspace costs (about 5 us)
+            workspace = w4a16_workspace(M, weights)
+        if workspace is not None:
+            status = _lib.gemm_w4a16_ws(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros,
+                                        _ptr(bias), _act(act), y.data_ptr(), M, N, weights.K, weights.group,
+                                        weights.gated, workspace.data_ptr(), _nbytes(workspace), _stream(stream))
+        elif weights.gated:
+            status = _lib.gemm_w4a16_gated(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros,
+                                           _act(act), y.data_ptr(), M, N, weights.K, weights.group, _stream(stream))
+        else:
+            status = _lib.gemm_w4a16(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros,
+                                     _ptr(bias), _act(act), y.data_ptr(), M, N, weights.K, weights.group,
+                                     _stream(stream))
+        _check(status, where)
     return y
 
 
-def gemm_w4a16_gated(x, weights: W4Weights, act="silu", h=None, stream=None):
+def gemm_w4a16(x, weights: W4Weights, bias=None, act="none", y=None, workspace=None, stream=None):
+    """y = act(x W^T + bias) on 4-bit weights: x [M, K] of the scales' type, bias fp32 [N] or None.
+    workspace: from w4a16_workspace, kept by callers of few rows on a long K."""
+    _w4_check("gemm_w4a16", x, weights, y, bias, False)
+    return _w4_run("gemm_w4a16", x, weights, bias, act, y, workspace, stream)
+
+
+def gemm_w4a16_gated(x, weights: W4Weights, act="silu", h=None, workspace=None, stream=None):
     """h = act(x Wg^T) * (x Wu^T) on 4-bit weights laid out gated: x [M, K] of the scales' type."""
     _w4_check("gemm_w4a16_gated", x, weights, h, None, True)
-    M, F = x.shape[0], weights.N
-    with _on(stream, weights.device):
-        if h is None:
-            h = x.new_empty((M, F))
-        _check(_lib.gemm_w4a16_gated(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros,
-                                     _act(act), h.data_ptr(), M, F, weights.K, weights.group, _stream(stream)),
-               "gemm_w4a16_gated")
-    return h
+    return _w4_run("gemm_w4a16_gated", x, weights, None, act, h, workspace, stream)

@@ -85,6 +85,7 @@ double choose_tile_us(const TileTime (&times)[4], int64_t M, int64_t N, int64_t 
 struct GatedPlan {
   bool small = false;   // gated_small_kernel, else the tile kernel
   GatedSmall variant;
+  int64_t ks = 1, tiles = 0, bytes = 0;   // small kernel: K ranges, workgroups of one, workspace
   Plan tile;
 };
 
@@ -124,6 +125,14 @@ int plan_gated(int dtype, int64_t M, int64_t F, int64_t H, GatedPlan* p) {
     v.s = v.xl <= 2 || (v.xl == 4 && pairs < 512) ? 2 : 1;
     v.pairs = v.xl <= 2 ? 1 : v.xl == 4 ? (pairs >= 512 ? 2 : 1) : v.xl == 8 && pairs >= 768 ? 4 : pairs >= 384 ? 2 : 1;
     v.waves = v.xl <= 2 || (v.xl == 6 && v.pairs == 2 && pairs < 512) ? 8 : 4;
+    const int64_t rows = v.xl == 0 ? 1 : 8 * v.xl;
+    p->tiles = ((pairs + v.pairs - 1) / v.pairs) * ((M + rows - 1) / rows);
+    if (p->tiles >= (int64_t)1 << 22) return GP_ESHAPE;   // threads of a grid
+    const double step_us = v.xl <= 2 ? 0.5 : v.xl == 4 ? 0.35 : 0.65;
+    p->ks = split_small((double)whole_k(H) / 64 / v.waves, step_us, p->tiles);
+    if (p->ks > 1) p->bytes = kCounterBytes + p->tiles * p->ks * ((rows + 15) / 16 * v.pairs * 2048);
+  } else {
+    p->bytes = plan_workspace(p->tile, M, 2 * F);
   }
   return GP_OK;
 }
@@ -339,7 +348,7 @@ int gemm_gated_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, size_t
   GatedPlan p;
   const int r = plan_gated(dtype, M, F, H, &p);
   if (r) return r;
-  *bytes = p.small ? 0 : (size_t)plan_workspace(p.tile, M, 2 * F);
+  *bytes = (size_t)p.bytes;
   return GP_OK;
 }
 
@@ -351,9 +360,8 @@ int gemm_gated(int dtype, const void* x, const void* w_shuf, int act, void* h, v
   GatedPlan p;
   int r = plan_gated(dtype, M, F, H, &p);
   if (r) return r;
-  const int64_t need = p.small ? 0 : plan_workspace(p.tile, M, 2 * F);
-  if (need > 0) {
-    if (!workspace || (int64_t)workspace_bytes < need) return GP_EWORKSPACE;
+  if (p.bytes > 0) {
+    if (!workspace || (int64_t)workspace_bytes < p.bytes) return GP_EWORKSPACE;
     if (!is_aligned16(workspace)) return GP_EINVAL;
   }
   if ((r = require_gfx950())) return r;
@@ -372,6 +380,9 @@ int gemm_gated(int dtype, const void* x, const void* w_shuf, int act, void* h, v
     t.Ka = (uint32_t)(2 * H);
     t.Kb = (uint32_t)(2 * whole_k(H));
     t.act = act;
+    t.ksplit = (uint32_t)p.ks;
+    t.cnt = p.ks > 1 ? (uint32_t*)workspace : nullptr;
+    t.part = p.ks > 1 ? (char*)workspace + kCounterBytes : nullptr;
     e = dtype == GP_BF16 ? launch_gated_small_bf16(p.variant, t, s) : launch_gated_small_f16(p.variant, t, s);
   } else {
     TileArgs t;

@@ -28,6 +28,11 @@ struct GatedArgs {
   uint32_t M, F;
   uint32_t Ka, Kb;    // bytes of K per row of x, and of the weights (whole 128-byte chunks, zeros past Ka)
   int act;            // Act
+  // K split across workgroups (few column blocks, long K): ksplit workgroups share
+  // a tile, the last to arrive adds their sums in order and stores it
+  uint32_t ksplit;    // 1: no split
+  char* part;         // [tiles][ksplit][row blocks * P][gate, up][64] v4f
+  uint32_t* cnt;      // [tiles] arrival counters: zero before and after
 };
 
 // XL: 16-byte loads of x per lane and chunk: 8 XL rows; 0: a single row.
@@ -49,14 +54,16 @@ __global__ __launch_bounds__(WAVES * 64) void gated_small_kernel(GatedArgs p) {
   const uint32_t Ka = p.Ka, Kb = p.Kb;
   // each XCD takes a contiguous run of column blocks (whole lines of h per L2)
   const uint32_t pairs = p.F / 16, cols = (pairs + P - 1) / P;
-  uint32_t bx = blockIdx.x % cols;
+  const uint32_t tiles = gridDim.x / p.ksplit, tile = blockIdx.x % tiles, kz = blockIdx.x / tiles;
+  uint32_t bx = tile % cols;
   if (cols % 8u == 0) bx = (bx % 8u) * (cols / 8u) + bx / 8u;
   const uint32_t pair0 = bx * P;
   const uint32_t npair = min((uint32_t)P, pairs - pair0);   // real pairs of this workgroup
-  const uint32_t m0 = blockIdx.x / cols * ROWS;
+  const uint32_t m0 = tile / cols * ROWS;
   const uint32_t mrows = min((uint32_t)ROWS, p.M - m0);
   const uint32_t nchunk = Kb / 128;
-  const uint32_t kc0 = (uint32_t)wave * nchunk / WAVES, kc1 = (uint32_t)(wave + 1) * nchunk / WAVES;
+  const uint32_t share = kz * WAVES + wave, shares = p.ksplit * WAVES;   // of K's chunks
+  const uint32_t kc0 = share * nchunk / shares, kc1 = (share + 1) * nchunk / shares;
   const int groups = (int)((kc1 - kc0 + S - 1) / S);
 
   // rows past M and blocks past the last pair lie outside their resources
@@ -139,14 +146,40 @@ __global__ __launch_bounds__(WAVES * 64) void gated_small_kernel(GatedArgs p) {
   __syncthreads();
   // an output block per wave and turn: rows mb * 16 + lane_lo, columns
   // pr * 16 + 4 * lane_hi + 0..3
+  auto sum_waves = [&](uint32_t q, v4f& g, v4f& u) GP_INLINE {
+    const uint32_t at = q / P * NB + 2 * (q % P);
+    g = red[at * 64 + lane];
+    u = red[(at + 1) * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+      g += red[(w * NQ + at) * 64 + lane];
+      u += red[(w * NQ + at + 1) * 64 + lane];
+    }
+  };
+  constexpr uint32_t PB = MB * P * 2048;   // bytes of one workgroup's sums
+  const __amdgpu_buffer_rsrc_t rp = make_rsrc(p.part + (size_t)tile * p.ksplit * PB, p.ksplit > 1 ? p.ksplit * PB : 0);
+  if (p.ksplit > 1) {
+    for (uint32_t q = (uint32_t)wave; q < MB * P; q += WAVES) {
+      v4f g, u;
+      sum_waves(q, g, u);
+      buf_store16_coh(__builtin_bit_cast(v4i, g), rp, kz * PB + q * 2048 + lane * 16);
+      buf_store16_coh(__builtin_bit_cast(v4i, u), rp, kz * PB + q * 2048 + 1024 + lane * 16);
+    }
+    // (the word is written after a barrier: the sums in LDS are done with)
+    if (!last_to_arrive(p.cnt + tile, p.ksplit, (volatile uint32_t*)lds)) return;
+  }
   for (uint32_t q = (uint32_t)wave; q < MB * P; q += WAVES) {
     const uint32_t mb = q / P, pr = q % P, row = mb * 16 + lane_lo;
     if (pr >= npair || row >= mrows) continue;
-    v4f g = red[(mb * NB + 2 * pr) * 64 + lane], u = red[(mb * NB + 2 * pr + 1) * 64 + lane];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) {
-      g += red[(w * NQ + mb * NB + 2 * pr) * 64 + lane];
-      u += red[(w * NQ + mb * NB + 2 * pr + 1) * 64 + lane];
+    v4f g, u;
+    if (p.ksplit > 1) {
+      g = u = v4f{0.f, 0.f, 0.f, 0.f};
+      for (uint32_t z = 0; z < p.ksplit; ++z) {
+        g += __builtin_bit_cast(v4f, buf_load16_coh(rp, z * PB + q * 2048 + lane * 16));
+        u += __builtin_bit_cast(v4f, buf_load16_coh(rp, z * PB + q * 2048 + 1024 + lane * 16));
+      }
+    } else {
+      sum_waves(q, g, u);
     }
     const size_t off = ((size_t)(m0 + row) * p.F + (pair0 + pr) * 16 + 4 * lane_hi) * 2;
     v4f h;

@@ -116,6 +116,27 @@ __device__ __forceinline__ void buf_store16_coh(v4i v, __amdgpu_buffer_rsrc_t r,
   __builtin_amdgcn_raw_buffer_store_b128(v, r, voff, 0, kPolicySC1);
 }
 
+__device__ __forceinline__ float buf_load4_coh(__amdgpu_buffer_rsrc_t r, uint32_t voff) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, voff, 0, kPolicySC1));
+}
+__device__ __forceinline__ void buf_store4_coh(float v, __amdgpu_buffer_rsrc_t r, uint32_t voff) {
+  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, v), r, voff, 0, kPolicySC1);
+}
+// Called by every thread of a workgroup that has stored its partial sums with the
+// coherent policy: true in the last of `n` workgroups to get here, whose loads with
+// that policy then see the partial sums of all. No workgroup waits for another. The
+// counter is zero before and after. `word` is LDS that no thread uses from its
+// call on.
+__device__ __forceinline__ bool last_to_arrive(uint32_t* counter, uint32_t n, volatile uint32_t* word) {
+  __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xF << 8));   // vmcnt(0): this thread's stores are complete
+  __syncthreads();
+  if (threadIdx.x == 0) *word = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (__builtin_amdgcn_readfirstlane(*word) != n - 1) return false;
+  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return true;
+}
+
 // Non-temporal (streaming) variants: cache policy bit 1 (nt) on gfx950.
 constexpr int kPolicyNT = 2;
 __device__ __forceinline__ v4i buf_load16_nt(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {

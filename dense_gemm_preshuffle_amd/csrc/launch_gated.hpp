@@ -30,7 +30,7 @@ hipError_t launch_gated_small_f16(const GatedSmall& v, const GatedArgs& a, hipSt
 #define GP_GATED_SMALL_CASE(DT, XL, P, W, S)                                                                   \
   if (v.xl == XL && v.pairs == P && v.waves == W && v.s == S) {                                                \
     constexpr uint32_t rows = XL == 0 ? 1 : 8 * XL;                                                            \
-    const dim3 grid(((a.F / 16 + P - 1) / P) * ((a.M + rows - 1) / rows));                                     \
+    const dim3 grid(((a.F / 16 + P - 1) / P) * ((a.M + rows - 1) / rows) * a.ksplit);                          \
     hipLaunchKernelGGL((gated_small_kernel<DT, XL, P, W, S>), grid, dim3(W * 64), 0, s, a);                    \
     return hipGetLastError();                                                                                  \
   }

@@ -22,7 +22,7 @@ hipError_t launch_w4_f16_z(const W4Plan& p, int sg, const W4Args& a, hipStream_t
 #define GP_W4_KERNEL(DT, XL, NB, W, S, SGV, ZV)                                                                \
   if (sg == SGV) {                                                                                             \
     constexpr uint32_t rows = XL == 0 ? 1 : 4 * XL;                                                            \
-    const dim3 grid(((a.nblk + NB - 1) / NB) * ((a.M + rows - 1) / rows));                                     \
+    const dim3 grid(((a.nblk + NB - 1) / NB) * ((a.M + rows - 1) / rows) * a.ksplit);                          \
     hipLaunchKernelGGL((w4a16_kernel<DT, XL, NB, W, S, SGV, ZV>), grid, dim3(W * 64), 0, s, a);                \
     return hipGetLastError();                                                                                  \
   }

@@ -103,7 +103,9 @@ __global__ __launch_bounds__(256) void layout_w4_kernel(W4LayoutArgs p) {
 //     (pairs 18.8, single 25.5), 4091 x 7168 in groups of 64 8.0 on single ones
 //     (pairs 9.5); 32 rows 14336 x 8192 19.0 on fours (25.9, 40.9), 4096 x 4096
 //     7.6 on single ones (8.7); 64 rows 14336 x 8192 33.9 on fours (46.5).
-int plan_w4(int64_t M, const W4Layout& l, bool gated, W4Plan* p) {
+// split: with a workspace, K is split where few column blocks leave CUs idle.
+struct W4Split { int64_t ks = 1, bytes = 0; };
+int plan_w4(int64_t M, const W4Layout& l, bool gated, bool split, W4Plan* p, W4Split* k) {
   p->xl = M == 1 ? 0 : M <= 4 ? 1 : M <= 16 ? 4 : M <= 32 ? 8 : 16;
   if (p->xl <= 1) {
     const bool many = l.nblk > 512;
@@ -123,11 +125,16 @@ int plan_w4(int64_t M, const W4Layout& l, bool gated, W4Plan* p) {
   const int64_t rows = p->xl == 0 ? 1 : 4 * p->xl;
   const int64_t wgs = ((l.nblk + p->nb - 1) / p->nb) * ((M + rows - 1) / rows);
   if (wgs * p->waves * 64 >= (int64_t)1 << 32) return GP_ESHAPE;
+  if (split) {
+    const double step_us = p->xl <= 1 ? 0.45 : p->xl == 4 ? 0.55 : p->xl == 8 ? 1.0 : 1.9;
+    k->ks = split_small((double)l.kblk / p->waves, step_us, wgs);
+    if (k->ks > 1) k->bytes = kCounterBytes + wgs * k->ks * ((rows + 15) / 16 * p->nb * (p->xl == 0 ? 256 : 1024));
+  }
   return GP_OK;
 }
 
 int run_w4(int dtype, const void* x, const void* w_shuf, bool zeros, const float* bias, int act, void* y, int64_t M,
-           int64_t N, int64_t K, int group, bool gated, hipStream_t stream) {
+           int64_t N, int64_t K, int group, bool gated, bool split, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (!x || !w_shuf || !y || !is_aligned16(x) || !is_aligned16(w_shuf) || !is_aligned16(y) || !is_aligned16(bias))
     return GP_EINVAL;
   if (M <= 0 || act < GP_ACT_NONE || act > GP_ACT_GELU) return GP_EINVAL;
@@ -137,7 +144,12 @@ int run_w4(int dtype, const void* x, const void* w_shuf, bool zeros, const float
   int r = layout_w4(gated ? 2 * N : N, K, group, zeros, gated, &l);
   if (r) return r;
   W4Plan p;
-  if ((r = plan_w4(M, l, gated, &p))) return r;
+  W4Split k;
+  if ((r = plan_w4(M, l, gated, split, &p, &k))) return r;
+  if (k.ks > 1) {
+    if (!ws || (int64_t)ws_bytes < k.bytes) return GP_EWORKSPACE;
+    if (!is_aligned16(ws)) return GP_EINVAL;
+  }
   if ((r = require_gfx950())) return r;
   W4Args a;
   a.x = (const char*)x;
@@ -153,6 +165,9 @@ int run_w4(int dtype, const void* x, const void* w_shuf, bool zeros, const float
   a.sshift = (uint32_t)l.sshift;
   a.act = act;
   a.gated = gated ? 1 : 0;
+  a.ksplit = (uint32_t)k.ks;
+  a.cnt = k.ks > 1 ? (uint32_t*)ws : nullptr;
+  a.part = k.ks > 1 ? (char*)ws + kCounterBytes : nullptr;
   forget_hip_error();
   auto* launch = dtype == GP_BF16 ? (zeros ? launch_w4_bf16_z : launch_w4_bf16) : (zeros ? launch_w4_f16_z : launch_w4_f16);
   return report_hip(launch(p, l.sg, a, stream), "kernel launch");
@@ -215,12 +230,35 @@ int gemm_w4a16_preshuffle(int dtype, const void* q, const void* scales, const in
 
 int gemm_w4a16(int dtype, const void* x, const void* w_shuf, int has_zeros, const float* bias, int act, void* y,
                int64_t M, int64_t N, int64_t K, int group, void* stream) {
-  return run_w4(dtype, x, w_shuf, has_zeros != 0, bias, act, y, M, N, K, group, false, (hipStream_t)stream);
+  return run_w4(dtype, x, w_shuf, has_zeros != 0, bias, act, y, M, N, K, group, false, false, nullptr, 0,
+                (hipStream_t)stream);
 }
 
 int gemm_w4a16_gated(int dtype, const void* x, const void* w_shuf, int has_zeros, int act, void* h, int64_t M,
                      int64_t F, int64_t K, int group, void* stream) {
-  return run_w4(dtype, x, w_shuf, has_zeros != 0, nullptr, act, h, M, F, K, group, true, (hipStream_t)stream);
+  return run_w4(dtype, x, w_shuf, has_zeros != 0, nullptr, act, h, M, F, K, group, true, false, nullptr, 0,
+                (hipStream_t)stream);
+}
+
+int gemm_w4a16_workspace_size(int64_t M, int64_t N, int64_t K, int group, int gated, size_t* bytes) {
+  if (!bytes || M <= 0) return GP_EINVAL;
+  if (M >= kMaxBytes || N >= kMaxBytes / 2) return GP_ESHAPE;
+  W4Layout l;
+  int r = layout_w4(gated ? 2 * N : N, K, group, false, gated != 0, &l);
+  if (r) return r;
+  W4Plan p;
+  W4Split k;
+  if ((r = plan_w4(M, l, gated != 0, true, &p, &k))) return r;
+  *bytes = (size_t)k.bytes;
+  return GP_OK;
+}
+
+int gemm_w4a16_ws(int dtype, const void* x, const void* w_shuf, int has_zeros, const float* bias, int act, void* y,
+                  int64_t M, int64_t N, int64_t K, int group, int gated, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  if (gated && bias) return GP_EINVAL;
+  return run_w4(dtype, x, w_shuf, has_zeros != 0, bias, act, y, M, N, K, group, gated != 0, true, workspace,
+                workspace_bytes, (hipStream_t)stream);
 }
 
 }  // extern "C"

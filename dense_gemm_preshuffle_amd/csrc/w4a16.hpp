@@ -53,6 +53,11 @@ struct W4Args {
   uint32_t sshift;     // log2 of 128-element blocks per scale (0: one or several scales per block)
   int act;             // Act
   int gated;           // gate and up blocks alternate
+  // K split across workgroups (few column blocks, long K): ksplit workgroups share
+  // a tile, the last to arrive adds their sums in order and stores it
+  uint32_t ksplit;     // 1: no split
+  char* part;          // [tiles][ksplit][row blocks * NB][result registers][64] fp32
+  uint32_t* cnt;       // [tiles] arrival counters: zero before and after
 };
 
 // Eight nibbles u = q + 8 -> eight 16-bit operands.
@@ -119,13 +124,15 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
   const uint32_t K = p.K, Kb = 2 * K;
   const uint32_t kblk = (K + 127) / 128, sblk = (kblk + (1u << p.sshift) - 1) >> p.sshift;
   const uint32_t cols = (p.nblk + NB - 1) / NB;
-  uint32_t bx = blockIdx.x % cols;
+  const uint32_t tiles = gridDim.x / p.ksplit, tile = blockIdx.x % tiles, kz = blockIdx.x / tiles;
+  uint32_t bx = tile % cols;
   if (cols % 8u == 0) bx = (bx % 8u) * (cols / 8u) + bx / 8u;   // a contiguous run of columns per XCD
   const uint32_t nb0 = bx * NB;
   const uint32_t nreal = min((uint32_t)NB, p.nblk - nb0);
-  const uint32_t m0 = blockIdx.x / cols * ROWS;
+  const uint32_t m0 = tile / cols * ROWS;
   const uint32_t mrows = min((uint32_t)ROWS, p.M - m0);
-  const uint32_t kb0 = (uint32_t)((uint64_t)wave * kblk / WAVES), kb1 = (uint32_t)((uint64_t)(wave + 1) * kblk / WAVES);
+  const uint32_t share = kz * WAVES + wave, shares = p.ksplit * WAVES;   // of K's blocks
+  const uint32_t kb0 = share * kblk / shares, kb1 = (share + 1) * kblk / shares;
   const int chunks = (int)((kb1 - kb0 + S - 1) / S);
 
   // rows past M and column blocks past the last lie outside their resources
@@ -268,6 +275,18 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
       for (int r = 0; r < R; ++r) red[((wave * NQ + mb * NB + nb) * R + r) * 64 + lane] = acc[mb][nb][r];
   __syncthreads();
 
+  constexpr uint32_t PB = NQ * R * 256;   // bytes of one workgroup's sums
+  const __amdgpu_buffer_rsrc_t rp = make_rsrc(p.part + (size_t)tile * p.ksplit * PB, p.ksplit > 1 ? p.ksplit * PB : 0);
+  auto sum_waves = [&](int qr) GP_INLINE {   // block and register qr
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) t += red[(w * NQ * R + qr) * 64 + lane];
+    return t;
+  };
+  if (p.ksplit > 1) {
+    for (int qr = wave; qr < NQ * R; qr += WAVES) buf_store4_coh(sum_waves(qr), rp, kz * PB + qr * 256 + lane * 4);
+    if (!last_to_arrive(p.cnt + tile, p.ksplit, (volatile uint32_t*)xs)) return;   // (x is done with)
+  }
   // one wave per output block (row block mb, column block or pair c) and result
   // register r
   const int per = p.gated ? NB / 2 : NB;
@@ -278,9 +297,12 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
     const uint32_t row = mb * 16 + 4 * lane_hi + r;
     if (nb >= p.nblk || n >= p.N || row >= mrows) continue;
     auto total = [&](int blk) GP_INLINE {
+      const int qr = (mb * NB + blk) * R + r;
       float t = 0.f;
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) t += red[((w * NQ + mb * NB + blk) * R + r) * 64 + lane];
+      if (p.ksplit > 1)
+        for (uint32_t z = 0; z < p.ksplit; ++z) t += buf_load4_coh(rp, z * PB + qr * 256 + lane * 4);
+      else
+        t = sum_waves(qr);
       if (!(fabsf(t) <= 3.402823466e38f)) t = w4_direct<DT, SG>(p, m0 + row, nb0 + blk, lane_lo);
       return t;
     };

@@ -458,6 +458,21 @@ int gemm_w4a16(int dtype, const void* x, const void* w_shuf, int has_zeros, cons
 int gemm_w4a16_gated(int dtype, const void* x, const void* w_shuf, int has_zeros, int act, void* h, int64_t M,
                      int64_t F, int64_t K, int group, void* stream);
 
+/*
+ * gemm_w4a16_ws -- gemm_w4a16, or with gated = 1 gemm_w4a16_gated (N is F, no
+ * bias), with a workspace, which lets the call split K across workgroups where
+ * few output columns and a long K leave CUs idle.
+ *   workspace   as for gemm_ex_ws (its first 64 KiB zero before the first call
+ *               and left zero by each; calls that may overlap need one each), at
+ *               least gemm_w4a16_workspace_size bytes; may be NULL where that is 0.
+ */
+int gemm_w4a16_ws(int dtype, const void* x, const void* w_shuf, int has_zeros, const float* bias, int act, void* y,
+                  int64_t M, int64_t N, int64_t K, int group, int gated, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/* Host-only: the workspace bytes of gemm_w4a16_ws for these sizes (0: none). */
+int gemm_w4a16_workspace_size(int64_t M, int64_t N, int64_t K, int group, int gated, size_t* bytes);
+
 /* Static, human-readable description of a gp_status value. */
 const char* gemm_status_string(int status);
 
