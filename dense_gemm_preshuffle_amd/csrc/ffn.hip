@@ -153,11 +153,11 @@ int plan_gated(int dtype, int64_t M, int64_t F, int64_t H, GatedPlan* p) {
 // GHz that the power limit leaves).
 struct BackwardPlan {
   Plan da, db;
-  bool da_rows = false, db_rows = false;
+  bool da_rows = false, db_rows = false, pair = false;   // pair: both in one launch
   int64_t Mp = 0, Np = 0;
-  // workspace: counters and partial sums of the two products (one after the
-  // other), then the copies
-  int64_t parts = 0, off_bt = 0, off_at = 0, off_ct = 0, off_d = 0, bytes = 0;
+  // workspace: counters and partial sums of the two products (the same ones after
+  // each other; in a pair db's after da's), then the copies
+  int64_t parts = 0, db_part = 0, off_bt = 0, off_at = 0, off_ct = 0, off_d = 0, bytes = 0;
 };
 
 int64_t align256(int64_t v) { return (v + 255) & ~(int64_t)255; }
@@ -177,12 +177,48 @@ int64_t pad_k(int64_t k) {
 // time than the preshuffled plan `other` (null: none) with `copied` bytes of
 // copies at the card's 4.9 TB/s; else false. On preshuffled operands a step takes
 // about 0.85 of the row-major one.
-bool plan_rows(int64_t M, int64_t N, int64_t Kb, const Plan* other, double copied, Plan* p) {
-  const double us = choose_tile_us(kRowsTimes, M, N, Kb, false, p);
+bool plan_rows(int64_t M, int64_t N, int64_t Kb, const Plan* other, double copied, Plan* p, double* took) {
+  const double us = *took = choose_tile_us(kRowsTimes, M, N, Kb, false, p);
   if (!other || other->kernel != GP_KERNEL_TILE) return true;
   for (const TileTime& t : kRowsTimes)
     if (t.tm == other->tm && t.tn == other->tn) return us <= tile_us(t, M, N, Kb, other->ks, 0.85) + copied / 4.9e6;
   return true;
+}
+
+// Both products in one launch, on 64 x 128 tiles: a [Ma][Na] over Ka K tiles, b
+// likewise. The workgroups share the CUs, so the time is that of all their work, or
+// of the longest:
+//   3.5 + max(sum of (K tiles * 0.4 + 0.6) / 256, longest) + joins   (us)
+// within 15% of 15 of 19 measured shapes; taken where it is 15% below the two
+// products' times (it also saves a launch). Products of M x F x H, one launch
+// against two: 130 x 2064 x 2048 16.8, 22.7; 1116 x 672 x 480 9.5, 17.4; 57 x 3392 x
+// 2080 18.2, 23.0; 606 x 4896 x 448 30.3, 33.6; 682 x 5808 x 608 40.2, 39.7.
+bool plan_pair(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t Nb, int64_t Kb, double apart, Plan* a, Plan* b) {
+  const int64_t ta = ((Ma + 63) / 64) * ((Na + 127) / 128), tb = ((Mb + 63) / 64) * ((Nb + 127) / 128);
+  if (ta + tb > 2048) return false;   // 71 x 6592 x 2784 (4576 tiles) 74 us, apart on larger tiles 66
+  double best = 0.85 * apart;
+  bool found = false;
+  for (int64_t x = 1; x <= 16 && (x == 1 || (Ka / x >= 4 && ta * x <= 1024)); ++x)
+    for (int64_t y = 1; y <= 16 && (y == 1 || (Kb / y >= 4 && tb * y <= 1024)); ++y) {
+      const double wa = 0.4 * (double)Ka / x + 0.6, wb = 0.4 * (double)Kb / y + 0.6;
+      const double us = 3.5 + std::max({(ta * x * wa + tb * y * wb) / 256, wa, wb}) + (x > 1 ? 0.55 * x : 0) +
+                        (y > 1 ? 0.55 * y : 0);
+      if (us >= best) continue;
+      best = us;
+      found = true;
+      for (Plan* p : {a, b}) {
+        *p = Plan();
+        p->kernel = GP_KERNEL_TILE;
+        p->tm = 64;
+        p->tn = 128;
+        p->tkb = 128;
+      }
+      a->ks = (int)x;
+      a->Kb = Ka * 128;
+      b->ks = (int)y;
+      b->Kb = Kb * 128;
+    }
+  return found;
 }
 
 // gated: dc itself is made by the call ([M][Np] in the workspace).
@@ -194,26 +230,24 @@ int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool
   p->Mp = pad_k(M);
   p->Np = gated ? pad_k(N) : N;
   if (!fits(p->Mp, 2 * K) || !fits(p->Np, 2 * K) || !fits(p->Mp, 2 * p->Np)) return GP_ESHAPE;
-  int r;
-  int64_t parts = 0;
+  // both products are planned whichever are wanted, so that an output has the same
+  // bits with and without the other
   Plan copies;
-  if (want_da) {
-    r = plan_gemm(dtype, M, K, p->Np, &copies);
-    p->da_rows = plan_rows(M, K, 2 * whole_k(p->Np), r ? nullptr : &copies, 4.0 * p->Np * K, &p->da);
-    if (!p->da_rows) {
-      if (r) return r;
-      p->da = copies;
-    }
-    parts = std::max(parts, plan_workspace(p->da, M, K));
-  }
-  if (want_db) {
-    r = plan_gemm(dtype, N, K, p->Mp, &copies);
-    p->db_rows = plan_rows(K, N, 2 * p->Mp, r ? nullptr : &copies, (gated ? 2.0 : 4.0) * p->Mp * N, &p->db);
-    if (!p->db_rows) {
-      if (r) return r;
-      p->db = copies;
-    }
-    parts = std::max(parts, p->db_rows ? plan_workspace(p->db, K, N) : plan_workspace(p->db, N, K));
+  double us_a = 0, us_b = 0;
+  int r = plan_gemm(dtype, M, K, p->Np, &copies);
+  p->da_rows = plan_rows(M, K, 2 * whole_k(p->Np), r ? nullptr : &copies, 4.0 * p->Np * K, &p->da, &us_a);
+  if (!p->da_rows) p->da = copies;
+  r = plan_gemm(dtype, N, K, p->Mp, &copies);
+  p->db_rows = plan_rows(K, N, 2 * p->Mp, r ? nullptr : &copies, (gated ? 2.0 : 4.0) * p->Mp * N, &p->db, &us_b);
+  if (!p->db_rows) p->db = copies;
+  p->pair = p->da_rows && p->db_rows &&
+            plan_pair(M, K, whole_k(p->Np) / 64, K, N, p->Mp / 64, us_a + us_b, &p->da, &p->db) && want_da && want_db;
+  const int64_t part_a = want_da ? plan_workspace(p->da, M, K) : 0;
+  const int64_t part_b = want_db ? (p->db_rows ? plan_workspace(p->db, K, N) : plan_workspace(p->db, N, K)) : 0;
+  int64_t parts = std::max(part_a, part_b);
+  if (p->pair && parts > 0) {
+    p->db_part = std::max(part_a, kCounterBytes);
+    parts = p->db_part + part_b;   // (which counts the counters once more)
   }
   int64_t at = p->parts = align256(parts);
   auto take = [&](int64_t bytes) {
@@ -232,9 +266,9 @@ int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool
 uint32_t tiles64(int64_t R, int64_t C) { return (uint32_t)(((R + 63) / 64) * ((C + 63) / 64)); }
 
 // a [M][lda] (K fast) times b [rows][N] row-major, K filled up to p.Kb bytes with
-// zeros past lda and rows; c [M][N], or with t [N][M].
-int launch_rows(int dtype, const Plan& p, const void* a, int64_t lda, const void* b, void* c, int64_t M, int64_t N,
-                int64_t rows, int64_t ldb, bool t, char* ws, hipStream_t s) {
+// zeros past lda and rows; c [M][N], or (transposed form) [N][M].
+TileArgs rows_args(const Plan& p, const void* a, int64_t lda, const void* b, void* c, int64_t M, int64_t N,
+                   int64_t rows, int64_t ldb, char* counters, char* part) {
   TileArgs g;
   g.a = (const char*)a;
   g.b = (const char*)b;
@@ -253,11 +287,9 @@ int launch_rows(int dtype, const Plan& p, const void* a, int64_t lda, const void
   g.kb_rows = (uint32_t)rows;
   g.ldb = (uint32_t)(2 * ldb);
   g.ksplit = (uint32_t)p.ks;
-  g.cnt = p.ks > 1 ? (uint32_t*)ws : nullptr;
-  g.part = p.ks > 1 ? ws + kCounterBytes : nullptr;
-  forget_hip_error();
-  auto* launch = dtype == GP_BF16 ? (t ? launch_rows_t_bf16 : launch_rows_bf16) : (t ? launch_rows_t_f16 : launch_rows_f16);
-  return report_hip(launch(p.tm, p.tn, g, s), "kernel launch");
+  g.cnt = p.ks > 1 ? (uint32_t*)counters : nullptr;
+  g.part = p.ks > 1 ? part : nullptr;
+  return g;
 }
 
 // Launches, in order, what has to run once the pointers are valid. dc: the
@@ -302,13 +334,31 @@ int run_backward(int dtype, const BackwardPlan& p, const GateGradArgs* gate, con
     else hipLaunchKernelGGL((prep_kernel<DT_F16>), dim3((uint32_t)blocks), dim3(256), 0, s, t);
     if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
   }
+  const bool bf16 = dtype == GP_BF16;
+  TileArgs ra = {}, rb = {};
+  if (da && p.da_rows) ra = rows_args(p.da, dc, ldc, b, da, M, K, N, K, ws, ws + kCounterBytes);
+  if (db && p.db_rows) rb = rows_args(p.db, ws + p.off_at, p.Mp, dc, db, K, N, M, ldc, ws, ws + kCounterBytes);
+  if (p.pair) {
+    // db's counters follow da's, its partial sums da's
+    if (p.db.ks > 1) {
+      rb.cnt = (uint32_t*)ws + ra.tiles_m * ra.tiles_n;
+      rb.part = ws + p.db_part;
+    }
+    forget_hip_error();
+    return report_hip(bf16 ? launch_pair_bf16(ra, rb, s) : launch_pair_f16(ra, rb, s), "kernel launch");
+  }
+  auto launch_rows = [&](const Plan& plan, const TileArgs& g, bool t) {
+    forget_hip_error();
+    auto* launch = bf16 ? (t ? launch_rows_t_bf16 : launch_rows_bf16) : (t ? launch_rows_t_f16 : launch_rows_f16);
+    return report_hip(launch(plan.tm, plan.tn, g, s), "kernel launch");
+  };
   if (da) {
-    r = p.da_rows ? launch_rows(dtype, p.da, dc, ldc, b, da, M, K, N, K, false, ws, s)
+    r = p.da_rows ? launch_rows(p.da, ra, false)
                   : launch_gemm(dtype, p.da, dc, ws + p.off_bt, da, M, K, ws, s);
     if (r) return r;
   }
   if (db) {
-    r = p.db_rows ? launch_rows(dtype, p.db, ws + p.off_at, p.Mp, dc, db, K, N, M, ldc, true, ws, s)
+    r = p.db_rows ? launch_rows(p.db, rb, true)
                   : launch_gemm(dtype, p.db, ws + p.off_ct, ws + p.off_at, db, N, K, ws, s);
     if (r) return r;
   }

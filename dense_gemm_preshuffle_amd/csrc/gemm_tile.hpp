@@ -229,8 +229,7 @@ struct TileCfg {
 // Tile (tm, tn) and K split z of this workgroup. With a K split the ksplit
 // workgroups of one tile are consecutive in the logical order, so with the
 // XCD-aware order they run on the same XCD and meet in its L2.
-__device__ __forceinline__ void tile_coords(const TileArgs& p, uint32_t& tm, uint32_t& tn, uint32_t& z) {
-  const uint32_t w = blockIdx.x;
+__device__ __forceinline__ void tile_coords(const TileArgs& p, uint32_t w, uint32_t& tm, uint32_t& tn, uint32_t& z) {
   const uint32_t T = p.tiles_m * p.tiles_n;
   const uint32_t S = p.ksplit;
   const uint32_t G = T * S;
@@ -258,7 +257,7 @@ __device__ __forceinline__ void tile_coords(const TileArgs& p, uint32_t& tm, uin
 }
 __device__ __forceinline__ void tile_coords(const TileArgs& p, uint32_t& tm, uint32_t& tn) {
   uint32_t z;
-  tile_coords(p, tm, tn, z);
+  tile_coords(p, blockIdx.x, tm, tn, z);
 }
 
 // Row-major B (EPI_ROWS, for the backward pass, whose K axis is the slow axis of
@@ -278,12 +277,11 @@ __device__ __forceinline__ void tile_coords(const TileArgs& p, uint32_t& tm, uin
 // compiler (same instructions, no fences between the MFMA groups).
 // KS: the variant that can split K across workgroups (p.ksplit > 1); the
 // others assume p.ksplit == 1 and carry no code for the cross-workgroup sum.
-template <int DT, int MS, int TM, int TN, int TKB, int EPI, int PIPE, bool FUSED, int KG, bool SCH = true,
-          bool KS = false>
-__global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, TN, KG)) void gemm_tile_kernel(TileArgs p) {
+// w: the workgroup's index among the product's, lds: C::LDS bytes.
+template <int DT, int MS, int TM, int TN, int TKB, int EPI, int PIPE, bool FUSED, int KG, bool SCH, bool KS>
+__device__ __forceinline__ void gemm_tile_body(const TileArgs& p, uint32_t w, char* lds) {
   using C = TileCfg<DT, MS, TM, TN, TKB, EPI, PIPE, FUSED, KG>;
   using Acc = typename Mma<DT, MS>::Acc;
-  __shared__ __attribute__((aligned(16))) char lds[C::LDS];
 
   // K group of this wave and the thread index inside its group; everything
   // below indexes by the group-local thread and wave
@@ -299,7 +297,7 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
   const int lgrp = lane / MS;
 
   uint32_t tm, tn, kz;
-  tile_coords(p, tm, tn, kz);
+  tile_coords(p, w, tm, tn, kz);
   uint32_t m0 = tm * TM, n0 = tn * TN, mskip, nskip;
   if constexpr (C::ROWS) {
     // a matrix smaller than the tile: rows of A past it read zeros, what B
@@ -854,7 +852,8 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
   // the arrival is counted (a relaxed agent-scope atomic), and the last
   // workgroup loads them only after reading the count: so no cache-wide
   // write-back or invalidate (what a __threadfence costs) is needed. ----
-  if constexpr (KS) {
+  // (The row-major form's split kernels also serve a single range.)
+  if constexpr (KS) if (!C::ROWS || p.ksplit > 1) {
     constexpr int NCH = C::MREP * C::NACC * (C::NREG / 4);   // 4-register chunks per lane
     using V4 = std::conditional_t<DT == DT_I8 || DT == DT_I4, v4i, v4f>;
     const uint32_t tile = tm * p.tiles_n + tn;
@@ -1121,6 +1120,29 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
   };
   if constexpr (FUSED) with_act(p.act, store_tile);
   else store_tile(std::integral_constant<int, ACT_NONE>{});
+}
+
+template <int DT, int MS, int TM, int TN, int TKB, int EPI, int PIPE, bool FUSED, int KG, bool SCH = true,
+          bool KS = false>
+__global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, TN, KG)) void gemm_tile_kernel(TileArgs p) {
+  __shared__ __attribute__((aligned(16))) char lds[TileCfg<DT, MS, TM, TN, TKB, EPI, PIPE, FUSED, KG>::LDS];
+  gemm_tile_body<DT, MS, TM, TN, TKB, EPI, PIPE, FUSED, KG, SCH, KS>(p, blockIdx.x, lds);
+}
+
+// Both products of a backward pass in one launch, on 64 x 128 tiles, for sizes at
+// which either alone leaves CUs idle: workgroups [0, na) compute a (EPI_ROWS),
+// those from na8 on (na rounded up to a multiple of 8, the XCDs) b (EPI_ROWS_T).
+struct PairArgs {
+  TileArgs a, b;
+  uint32_t na, na8;
+};
+template <int DT>
+__global__ __launch_bounds__(256, 2) void gemm_pair_kernel(PairArgs p) {
+  constexpr int LA = TileCfg<DT, 16, 64, 128, 128, EPI_ROWS, 3>::LDS, LB = TileCfg<DT, 16, 64, 128, 128, EPI_ROWS_T, 3>::LDS;
+  __shared__ __attribute__((aligned(16))) char lds[LA > LB ? LA : LB];
+  const uint32_t w = blockIdx.x;
+  if (w < p.na) gemm_tile_body<DT, 16, 64, 128, 128, EPI_ROWS, 3, false, 1, true, true>(p.a, w, lds);
+  else if (w >= p.na8) gemm_tile_body<DT, 16, 64, 128, 128, EPI_ROWS_T, 3, false, 1, true, true>(p.b, w - p.na8, lds);
 }
 
 }  // namespace gp
