@@ -221,11 +221,11 @@ def _dt(x) -> int:
 def _stream(stream):
     """The handle of a stream argument: None is torch's current stream, an int a handle, else a torch stream."""
     if stream is None:
-        import torch
+        from torch import _C
 
         # the handle alone: making the Stream object of torch.cuda.current_stream()
         # took 2.6 us of the 9 us that a small product's call spent on the host
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -427,6 +427,7 @@ def gemm_ex_noalloc(dtype, a, b_shuf, c, scale_a=None, scale_b=None, bias=None, 
 _HALF = {GP_BF16: "bfloat16", GP_F16: "float16"}
 
 
+@functools.lru_cache(maxsize=None)
 def _half(dtype):
     """(gp_dtype, torch dtype) of a BF16 / FP16 operator."""
     import torch
@@ -437,10 +438,14 @@ def _half(dtype):
     return dt, getattr(torch, _HALF[dt])
 
 
+def _fits(t, shape, dtype, device) -> bool:
+    """A contiguous tensor of this shape and type on this device."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device
+
+
 def _want(where, t, shape, dtype, device=None):
     """A given tensor is a contiguous device tensor of this shape and type."""
-    if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda
-            and (device is None or t.device == device)):
+    if t.is_cuda and _fits(t, shape, dtype, t.device if device is None else device):
         return
     if (not t.is_cuda or tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()
             or (device is not None and t.device != device)):
@@ -522,24 +527,26 @@ def gemm_gated(dtype, x, w_shuf, act="silu", save=False, h=None, gate=None, up=N
 
     dt, t = _half(dtype)
     M, H = x.shape
+    device = x.device
     Hp = -(-H // 64) * 64
     F = _nbytes(w_shuf) // (4 * Hp) if H else 0
     _want("gemm_gated: x", x, (M, H), t)
-    _want("gemm_gated: w_shuf", w_shuf, (4 * F * Hp,), torch.uint8, x.device)
-    with _on(stream, x.device):
-        h = torch.empty(M, F, dtype=t, device=x.device) if h is None else h
+    _want("gemm_gated: w_shuf", w_shuf, (4 * F * Hp,), torch.uint8, device)
+    if not save and (gate is not None or up is not None):
+        raise ValueError("gemm_gated: gate and up are written with save=True")
+    for name, v in (("h", h), ("gate", gate), ("up", up)):
+        if v is not None and not _fits(v, (M, F), t, device):
+            _want(f"gemm_gated: {name}", v, (M, F), t, device)
+    with _on(stream, device):
+        h = x.new_empty((M, F)) if h is None else h
         if save:
-            gate = torch.empty_like(h) if gate is None else gate
-            up = torch.empty_like(h) if up is None else up
-        elif gate is not None or up is not None:
-            raise ValueError("gemm_gated: gate and up are written with save=True")
-        for name, v in (("h", h), ("gate", gate), ("up", up)):
-            if v is not None:
-                _want(f"gemm_gated: {name}", v, (M, F), t, x.device)
+            gate = x.new_empty((M, F)) if gate is None else gate
+            up = x.new_empty((M, F)) if up is None else up
         if workspace is None:
-            workspace = gated_workspace(dt, M, F, H, x.device)
-        _check(load_library().gemm_gated(dt, _ptr(x), _ptr(w_shuf), _act(act), _ptr(h), _ptr(gate), _ptr(up), M, F, H,
-                                         _ptr(workspace), _nbytes(workspace), _stream(stream)), "gemm_gated")
+            workspace = gated_workspace(dt, M, F, H, device)
+    status = load_library().gemm_gated(dt, x.data_ptr(), w_shuf.data_ptr(), _act(act), h.data_ptr(), _ptr(gate), _ptr(up), M, F, H,
+                             _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check(status, "gemm_gated")
     return (h, gate, up) if save else h
 
 
@@ -561,8 +568,6 @@ def gemm_gated_backward(dtype, dh, gate, up, x, w, act="silu", want_dx=True, wan
     """(dx [M, H], dw [2F, H]) of gemm_gated from dh and the kept gate and up
     ([M, F]); w [2F, H] row-major. An output that is not wanted is None, and the
     operand that it alone needs (w for dx, x for dw) may be None."""
-    import torch
-
     dt, t = _half(dtype)
     M, F = dh.shape
     dev = dh.device
@@ -570,14 +575,16 @@ def gemm_gated_backward(dtype, dh, gate, up, x, w, act="silu", want_dx=True, wan
         raise ValueError("gemm_gated_backward: no output wanted")
     if (want_dx and w is None) or (want_dw and x is None):
         raise ValueError("gemm_gated_backward: dx needs w, dw needs x")
+    if not dh.is_cuda:
+        raise ValueError("gemm_gated_backward: dh is not a device tensor")
     H = w.shape[1] if w is not None else x.shape[1]
     for name, v, shape in (("dh", dh, (M, F)), ("gate", gate, (M, F)), ("up", up, (M, F)), ("x", x, (M, H)),
                            ("w", w, (2 * F, H)), ("dx", dx, (M, H)), ("dw", dw, (2 * F, H))):
-        if v is not None:
+        if v is not None and not _fits(v, shape, t, dev):
             _want(f"gemm_gated_backward: {name}", v, shape, t, dev)
     with _on(stream, dev):
-        dx = (torch.empty(M, H, dtype=t, device=dev) if dx is None else dx) if want_dx else None
-        dw = (torch.empty(2 * F, H, dtype=t, device=dev) if dw is None else dw) if want_dw else None
+        dx = (dh.new_empty((M, H)) if dx is None else dx) if want_dx else None
+        dw = (dh.new_empty((2 * F, H)) if dw is None else dw) if want_dw else None
         if workspace is None:
             workspace = gated_backward_workspace(dt, M, F, H, want_dx, want_dw, dev)
         _check(load_library().gemm_gated_backward(dt, _ptr(dh), _ptr(gate), _ptr(up), _ptr(x), _ptr(w), _act(act),
@@ -603,8 +610,6 @@ def gemm_backward(dtype, dc, a, b, want_da=True, want_db=True, da=None, db=None,
     """(da [M, K], db [N, K]) of C = A B^T from dc [M, N]; a [M, K] and b [N, K]
     row-major. An output that is not wanted is None, and the operand that it
     alone needs (b for da, a for db) may be None."""
-    import torch
-
     dt, t = _half(dtype)
     M, N = dc.shape
     dev = dc.device
@@ -612,14 +617,16 @@ def gemm_backward(dtype, dc, a, b, want_da=True, want_db=True, da=None, db=None,
         raise ValueError("gemm_backward: no output wanted")
     if (want_da and b is None) or (want_db and a is None):
         raise ValueError("gemm_backward: da needs b, db needs a")
+    if not dc.is_cuda:
+        raise ValueError("gemm_backward: dc is not a device tensor")
     K = b.shape[1] if b is not None else a.shape[1]
     for name, v, shape in (("dc", dc, (M, N)), ("a", a, (M, K)), ("b", b, (N, K)), ("da", da, (M, K)),
                            ("db", db, (N, K))):
-        if v is not None:
+        if v is not None and not _fits(v, shape, t, dev):
             _want(f"gemm_backward: {name}", v, shape, t, dev)
     with _on(stream, dev):
-        da = (torch.empty(M, K, dtype=t, device=dev) if da is None else da) if want_da else None
-        db = (torch.empty(N, K, dtype=t, device=dev) if db is None else db) if want_db else None
+        da = (dc.new_empty((M, K)) if da is None else da) if want_da else None
+        db = (dc.new_empty((N, K)) if db is None else db) if want_db else None
         if workspace is None:
             workspace = backward_workspace(dt, M, N, K, want_da, want_db, dev)
         _check(load_library().gemm_backward(dt, _ptr(dc), _ptr(a), _ptr(b), _ptr(da), _ptr(db), M, N, K,
@@ -670,20 +677,7 @@ def gemm_w4a16_preshuffle(q, scales, zeros=None, group=128, gated=False, out=Non
         _want(f"{where}: out", out, (n,), torch.uint8, q.device)
         _check(load_library().gemm_w4a16_preshuffle(dt, _ptr(q), _ptr(scales), _ptr(zeros), _ptr(out), N, K, group,
                                                     int(gated), _stream(stream)), where)
-    return W4Weights(out, scales.dtype, N // 2 if gated else N, K, group, zeros is not None, bool(gated))
-
-
-def _w4_check(where, x, weights, y, bias, gated):
-    """x, the output and the bias fit the weights."""
-    if weights.gated != gated:
-        raise ValueError(f"{where}: the weights were laid out {'' if weights.gated else 'not '}gated")
-    _want(f"{where}: x", x, (x.shape[0], weights.K), weights.dtype, weights.device)
-    if y is not None:
-        _want(f"{where}: output", y, (x.shape[0], weights.N), weights.dtype, weights.device)
-    if bias is not None:
-        import torch
-
-        _want(f"{where}: bias", bias, (weights.N,), torch.float32, weights.device)
+    return W4Weights(out, scales.dtype, N // 2 if gated else N, K, int(group), zeros is not None, bool(gated))
 
 
 def gemm_w4a16_workspace_size(M: int, N: int, K: int, group: int, gated=False) -> int:
@@ -701,37 +695,57 @@ def w4a16_workspace(M: int, weights: W4Weights):
     return torch.zeros(n, dtype=torch.uint8, device=weights.device) if n else None
 
 
-def _w4_run(where, x, weights, bias, act, y, workspace, stream):
-    M, N = x.shape[0], weights.N
-    with _on(stream, weights.device):
-        if y is None:
-            y = x.new_empty((M, N))
-        if workspace is None and M > 16 and weights.K > 8192:
-            # else a split saves no more than making and clearing a workspace costs (about 5 us)
+def _w4_run(where, gated, x, weights, bias, act, y, workspace, stream):
+    """One 4-bit product. A decode step's products take a few microseconds on the GPU, about what this
+    function and the launch take on the host, so it asks each thing once."""
+    device, dtype, N, K = weights.device, weights.dtype, weights.N, weights.K
+    shape = x.shape
+    M = shape[0]
+    if weights.gated is not gated:
+        raise ValueError(f"{where}: the weights were laid out {'not ' if gated else ''}gated")
+    if not (x.dtype is dtype and shape == (M, K) and x.is_contiguous() and x.device == device):
+        _want(f"{where}: x", x, (M, K), dtype, device)
+    if bias is not None:
+        import torch
+
+        _want(f"{where}: bias", bias, (N,), torch.float32, device)
+        bias = bias.data_ptr()
+    if stream is None:
+        handle = _stream(None)
+        out = x.new_empty((M, N)) if y is None else y
+    else:
+        handle = _stream(stream)
+        with _on(stream, device):
+            out = x.new_empty((M, N)) if y is None else y
+    if y is not None:
+        _want(f"{where}: output", y, (M, N), dtype, device)
+    if workspace is None and M > 16 and K > 8192:
+        # else a split saves no more than making and clearing a workspace costs (about 5 us)
+        with _on(stream, device):
             workspace = w4a16_workspace(M, weights)
-        if workspace is not None:
-            status = _lib.gemm_w4a16_ws(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros,
-                                        _ptr(bias), _act(act), y.data_ptr(), M, N, weights.K, weights.group,
-                                        weights.gated, workspace.data_ptr(), _nbytes(workspace), _stream(stream))
-        elif weights.gated:
-            status = _lib.gemm_w4a16_gated(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros,
-                                           _act(act), y.data_ptr(), M, N, weights.K, weights.group, _stream(stream))
-        else:
-            status = _lib.gemm_w4a16(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros,
-                                     _ptr(bias), _act(act), y.data_ptr(), M, N, weights.K, weights.group,
-                                     _stream(stream))
+    act = _act(act)
+    lib = load_library()
+    if workspace is not None:
+        status = lib.gemm_w4a16_ws(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros, bias,
+                                    act, out.data_ptr(), M, N, K, weights.group, gated, workspace.data_ptr(),
+                                    _nbytes(workspace), handle)
+    elif gated:
+        status = lib.gemm_w4a16_gated(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros,
+                                       act, out.data_ptr(), M, N, K, weights.group, handle)
+    else:
+        status = lib.gemm_w4a16(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros, bias,
+                                 act, out.data_ptr(), M, N, K, weights.group, handle)
+    if status:
         _check(status, where)
-    return y
+    return out
 
 
 def gemm_w4a16(x, weights: W4Weights, bias=None, act="none", y=None, workspace=None, stream=None):
     """y = act(x W^T + bias) on 4-bit weights: x [M, K] of the scales' type, bias fp32 [N] or None.
     workspace: from w4a16_workspace, kept by callers of few rows on a long K."""
-    _w4_check("gemm_w4a16", x, weights, y, bias, False)
-    return _w4_run("gemm_w4a16", x, weights, bias, act, y, workspace, stream)
+    return _w4_run("gemm_w4a16", False, x, weights, bias, act, y, workspace, stream)
 
 
 def gemm_w4a16_gated(x, weights: W4Weights, act="silu", h=None, workspace=None, stream=None):
     """h = act(x Wg^T) * (x Wu^T) on 4-bit weights laid out gated: x [M, K] of the scales' type."""
-    _w4_check("gemm_w4a16_gated", x, weights, h, None, True)
-    return _w4_run("gemm_w4a16_gated", x, weights, None, act, h, workspace, stream)
+    return _w4_run("gemm_w4a16_gated", True, x, weights, None, act, h, workspace, stream)

@@ -222,7 +222,7 @@ bool plan_pair(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t Nb, int64
 }
 
 // gated: dc itself is made by the call ([M][Np] in the workspace).
-int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, bool gated, BackwardPlan* p) {
+int make_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, bool gated, BackwardPlan* p) {
   if (M <= 0 || N <= 0 || K <= 0) return GP_EINVAL;
   if (!half_type(dtype)) return GP_EDTYPE;
   if (M >= kMaxBytes / 4 || N >= kMaxBytes || K >= kMaxBytes) return GP_ESHAPE;
@@ -261,6 +261,31 @@ int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool
   p->off_d = take(gated && (want_da || p->db_rows) ? M * p->Np * 2 : 0);
   p->bytes = std::max<int64_t>(at, 256);   // never none: one rule for every caller
   return GP_OK;
+}
+
+// A plan depends on these numbers alone and takes 3 to 6 us to make, as long as a
+// launch; a training loop asks for a few of them over and over. Kept per thread,
+// the latest of each slot.
+int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, bool gated, BackwardPlan* p) {
+  struct Slot {
+    int64_t key[4] = {-1, 0, 0, 0};
+    BackwardPlan plan;
+  };
+  static thread_local Slot slots[32];
+  const int64_t key[4] = {(int64_t)dtype * 8 + want_da * 4 + want_db * 2 + gated, M, N, K};
+  uint64_t h = 0;
+  for (int64_t k : key) h = (h ^ (uint64_t)k) * 0x9E3779B97F4A7C15ull;
+  Slot& s = slots[h >> 59];
+  if (key[0] >= 0 && std::equal(key, key + 4, s.key)) {
+    *p = s.plan;
+    return GP_OK;
+  }
+  const int r = make_backward_plan(dtype, M, N, K, want_da, want_db, gated, p);
+  if (r == GP_OK) {
+    std::copy(key, key + 4, s.key);
+    s.plan = *p;
+  }
+  return r;
 }
 
 uint32_t tiles64(int64_t R, int64_t C) { return (uint32_t)(((R + 63) / 64) * ((C + 63) / 64)); }
