@@ -38,20 +38,21 @@ __global__ __launch_bounds__(256) void preshuffle_gated_kernel(const char* __res
 // workgroup's reading it. Two workgroups on a CU take as long as one after the
 // other, so a started round counts whole. The constants come from timing every
 // tile with 1 to 16 ranges on one MI355X:
-//   row-major B: 36 shapes (M 32 to 4096, K 64 to 31744); the choice was the
-//     fastest or within 8% of it on 31. 2000 x 4096 x 14336 206 on 256 x 256 in two
-//     ranges, 232 on 128 x 256; 161 x 2656 x 10624 29.6 on 64 x 128 in four (39.7 in
-//     three, 35.8 in eight); transposed 4096 x 14336 x 128 42 on 128 x 128, 47 on
-//     256 x 256.
-//   gated: 14 shapes (M 70 to 7133, K 320 to 8192); within 5% on 13. 259 x 4384 x
-//     6592 37.0 on 128 x 256 in four ranges, 38.8 on 128 x 128 in two; 509 x 14336 x
-//     4096 57.8 on 128 x 256, 62.4 on 128 x 128, 63.1 on 256 x 256 in two; 1910 x
-//     10720 x 448 25.6 on 128 x 128, 34.3 on 256 x 256.
+//   row-major B: 40 shapes (M 32 to 5905, K 64 to 31744); the tile and ranges of
+//     least time by the model were the fastest or within 8% of it on 38 of them.
+//     M x N x K in us: 2000 x 4096 x 14336 150 on 256 x 256 in two ranges, 176 on
+//     128 x 128 in one; 161 x 2656 x 10624 25.9 on 64 x 128 in four (35.0 in three,
+//     40.9 in five), 28.8 on 128 x 128 in six; transposed 4096 x 14336 x 128 39.4
+//     on 128 x 128, 41.9 on 256 x 256.
+//   gated: 24 shapes (M 70 to 7133, K 320 to 8192); within 8% on 23. 259 x 4384 x
+//     6592 36.9 on 128 x 256 in four ranges, 38.7 on 128 x 128 in two; 509 x 14336 x
+//     4096 57.6 on 128 x 256, 62.4 on 128 x 128, 65.2 on 256 x 256 in two; 1536 x
+//     1984 x 512 7.4 on 128 x 128, 9.9 on 128 x 256.
 struct TileTime { int tm, tn; double step, ends, join; };
-constexpr TileTime kRowsTimes[] = {{256, 256, 1.45, 10, 4.3}, {128, 256, 1.05, 5, 2.1}, {128, 128, 0.52, 2, 1.1},
-                                   {64, 128, 0.40, 2, 0.55}};
-constexpr TileTime kGatedTimes[] = {{256, 256, 1.15, 9, 4.3}, {128, 256, 0.75, 4, 2.6}, {128, 128, 0.5, 1.5, 1.2},
-                                    {64, 128, 0.38, 1, 0.8}};
+constexpr TileTime kRowsTimes[] = {{256, 256, 1.21, 9.5, 3.2}, {128, 256, 0.99, 5.6, 2.1}, {128, 128, 0.60, 1.65, 1.25},
+                                   {64, 128, 0.32, 2.15, 0.7}};
+constexpr TileTime kGatedTimes[] = {{256, 256, 1.5, 6.1, 4.0}, {128, 256, 0.56, 6.0, 3.0}, {128, 128, 0.60, 1.25, 1.35},
+                                    {64, 128, 0.35, 0.73, 1.0}};
 double tile_us(const TileTime& t, int64_t M, int64_t N, int64_t Kb, int64_t ks, double speed = 1.0) {
   const double fill = (double)(((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn) * ks) / 256;
   const double rounds = fill <= 4 ? std::ceil(fill) : fill + 0.5;
@@ -189,10 +190,11 @@ bool plan_rows(int64_t M, int64_t N, int64_t Kb, const Plan* other, double copie
 // likewise. The workgroups share the CUs, so the time is that of all their work, or
 // of the longest:
 //   3.5 + max(sum of (K tiles * 0.4 + 0.6) / 256, longest) + joins   (us)
-// within 15% of 15 of 19 measured shapes; taken where it is 15% below the two
-// products' times (it also saves a launch). Products of M x F x H, one launch
-// against two: 130 x 2064 x 2048 16.8, 22.7; 1116 x 672 x 480 9.5, 17.4; 57 x 3392 x
-// 2080 18.2, 23.0; 606 x 4896 x 448 30.3, 33.6; 682 x 5808 x 608 40.2, 39.7.
+// taken where it is 15% below the two products' times (it also saves a launch); on
+// 25 measured shapes the choice was 7% above the best of both on average. Products
+// of M x F x H on their best ranges, one launch against two: 130 x 2064 x 2048 16.6,
+// 22.4; 1116 x 672 x 480 9.5, 17.3; 57 x 3392 x 2080 18.1, 23.2; 606 x 4896 x 448
+// 28.9, 33.2; 682 x 5808 x 608 40.5, 39.7.
 bool plan_pair(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t Nb, int64_t Kb, double apart, Plan* a, Plan* b) {
   const int64_t ta = ((Ma + 63) / 64) * ((Na + 127) / 128), tb = ((Mb + 63) / 64) * ((Nb + 127) / 128);
   if (ta + tb > 2048) return false;   // 71 x 6592 x 2784 (4576 tiles) 74 us, apart on larger tiles 66

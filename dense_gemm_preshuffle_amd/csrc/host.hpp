@@ -57,7 +57,7 @@ int require_gfx950();
 // K ranges of a small-M kernel whose waves run `steps` chunks of `step_us` each, on
 // `tiles` workgroups: the ranges (one workgroup per CU and 16 at most) for which
 // the chunks and the join, 0.8 us and 0.45 per range, take the least time. Measured
-// on 21 shapes with 1 to 16 ranges: gated 1 x 368 x 6784 11.1 us unsplit, 7.5 in
+// on 22 shapes with 1 to 16 ranges: gated 1 x 368 x 6784 11.1 us unsplit, 7.5 in
 // four, 11.5 in 16; 40 x 336 x 6720 21.2, 9.6 in six; 1 x 1024 x 2048 5.3, 6.1 in two.
 inline int64_t split_small(double steps, double step_us, int64_t tiles) {
   double best = steps * step_us;
