@@ -1062,7 +1062,10 @@ __device__ __forceinline__ void gemm_tile_body(const TileArgs& p, uint32_t w, ch
     const uint32_t ldc = T ? p.M : p.N, rskip = T ? nskip : mskip, cskip = T ? mskip : nskip;
     const uint32_t rend = T ? p.N : p.M;   // (the columns' end is ldc: whole 16-byte pieces, a row of 32)
     const size_t base = ((size_t)(T ? n0 : m0) * ldc + (T ? m0 : n0)) * C::OB;
-    const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.c + base, ((C::CROWS - 1) * ldc + C::CCOLS) * C::OB);
+    // up to the matrix's end: a tile that reaches past it may span 2^31 bytes, and
+    // the offset of what is skipped would lie inside
+    const uint32_t rows = min((uint32_t)C::CROWS, rend - (T ? n0 : m0)), cols = min((uint32_t)C::CCOLS, ldc - (T ? m0 : n0));
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.c + base, ((rows - 1) * ldc + cols) * C::OB);
 #pragma unroll
     for (int i = 0; i < TOTAL / C::THREADS; ++i) {
       const int q = i * C::THREADS + etid;
