@@ -52,8 +52,8 @@ __all__ = [
     "gemm_gated_preshuffle", "gemm_gated", "gemm_gated_workspace_size", "gated_workspace", "gemm_gated_backward",
     "gemm_gated_backward_workspace_size", "gated_backward_workspace", "gemm_backward", "gemm_backward_workspace_size",
     "backward_workspace", "W4Weights", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle", "gemm_w4a16",
-    "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "w4a16_workspace", "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE",
-    "KERNEL_SPLITK", "KERNEL_WIDE",
+    "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "w4a16_workspace", "gemm_status_string", "source_hash", "DTYPES",
+    "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE", "KERNEL_SPLITK", "KERNEL_WIDE",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -167,8 +167,9 @@ def load_library():
     lib.gemm_last_hip_call.argtypes = []
     lib.gemm_last_hip_call.restype = ctypes.c_char_p
     for f in ("gemm_preshuffle_b", "gemm_a8w8", "gemm_bf16", "gemm_mxfp4", "gemm_f16", "gemm_w4a8", "gemm_ex",
-              "gemm_plan", "gemm_plan_ws", "gemm_workspace_size", "gemm_ex_ws", "gemm_ex_noalloc", "gemm_gated_preshuffle", "gemm_gated",
-              "gemm_gated_workspace_size", "gemm_gated_backward", "gemm_gated_backward_workspace_size",
+              "gemm_plan", "gemm_plan_ws", "gemm_workspace_size", "gemm_ex_ws", "gemm_ex_noalloc",
+              "gemm_gated_preshuffle", "gemm_gated", "gemm_gated_workspace_size", "gemm_gated_backward",
+              "gemm_gated_backward_workspace_size",
               "gemm_backward", "gemm_backward_workspace_size", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle",
               "gemm_w4a16", "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "gemm_w4a16_ws"):
         getattr(lib, f).restype = ci
@@ -487,6 +488,16 @@ def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+def _workspace_bytes(where, t, device) -> int:
+    """Bytes of a workspace tensor, which the call's device has to hold in one piece."""
+    if t is None:
+        return 0
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{where}: expected a contiguous workspace on {device}, got one on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.numel() * t.element_size()
+
+
 def gemm_gated_preshuffle(w, dtype, out=None, stream=None):
     """w [2F, H] (F gate rows, then F up rows) -> layout of gemm_gated (uint8, flat)."""
     import torch
@@ -497,11 +508,11 @@ def gemm_gated_preshuffle(w, dtype, out=None, stream=None):
         raise ValueError("gemm_gated_preshuffle: w holds F gate rows and F up rows")
     _want("gemm_gated_preshuffle: w", w, (F2, H), t)
     n = 2 * F2 * (-(-H // 64) * 64)    # K is filled up to whole 128-byte tiles
-    if out is None:
-        out = torch.empty(n, dtype=torch.uint8, device=w.device)
-    _want("gemm_gated_preshuffle: out", out, (n,), torch.uint8, w.device)
-    _check(load_library().gemm_gated_preshuffle(_ptr(w), _ptr(out), F2 // 2, H, dt, _stream(stream)),
-           "gemm_gated_preshuffle")
+    with _on(stream, w.device):
+        out = torch.empty(n, dtype=torch.uint8, device=w.device) if out is None else out
+        _want("gemm_gated_preshuffle: out", out, (n,), torch.uint8, w.device)
+        _check(load_library().gemm_gated_preshuffle(_ptr(w), _ptr(out), F2 // 2, H, dt, _stream(stream)),
+               "gemm_gated_preshuffle")
     return out
 
 
@@ -544,9 +555,9 @@ def gemm_gated(dtype, x, w_shuf, act="silu", save=False, h=None, gate=None, up=N
             up = x.new_empty((M, F)) if up is None else up
         if workspace is None:
             workspace = gated_workspace(dt, M, F, H, device)
-    status = load_library().gemm_gated(dt, x.data_ptr(), w_shuf.data_ptr(), _act(act), h.data_ptr(), _ptr(gate), _ptr(up), M, F, H,
-                             _ptr(workspace), _nbytes(workspace), _stream(stream))
-    _check(status, "gemm_gated")
+    _check(load_library().gemm_gated(dt, x.data_ptr(), w_shuf.data_ptr(), _act(act), h.data_ptr(), _ptr(gate), _ptr(up),
+                                     M, F, H, _ptr(workspace), _workspace_bytes("gemm_gated", workspace, device),
+                                     _stream(stream)), "gemm_gated")
     return (h, gate, up) if save else h
 
 
@@ -588,7 +599,8 @@ def gemm_gated_backward(dtype, dh, gate, up, x, w, act="silu", want_dx=True, wan
         if workspace is None:
             workspace = gated_backward_workspace(dt, M, F, H, want_dx, want_dw, dev)
         _check(load_library().gemm_gated_backward(dt, _ptr(dh), _ptr(gate), _ptr(up), _ptr(x), _ptr(w), _act(act),
-                                                  _ptr(dx), _ptr(dw), M, F, H, _ptr(workspace), _nbytes(workspace),
+                                                  _ptr(dx), _ptr(dw), M, F, H, _ptr(workspace),
+                                                  _workspace_bytes("gemm_gated_backward", workspace, dev),
                                                   _stream(stream)), "gemm_gated_backward")
     return dx, dw
 
@@ -630,7 +642,8 @@ def gemm_backward(dtype, dc, a, b, want_da=True, want_db=True, da=None, db=None,
         if workspace is None:
             workspace = backward_workspace(dt, M, N, K, want_da, want_db, dev)
         _check(load_library().gemm_backward(dt, _ptr(dc), _ptr(a), _ptr(b), _ptr(da), _ptr(db), M, N, K,
-                                            _ptr(workspace), _nbytes(workspace), _stream(stream)), "gemm_backward")
+                                            _ptr(workspace), _workspace_bytes("gemm_backward", workspace, dev),
+                                            _stream(stream)), "gemm_backward")
     return da, db
 
 
@@ -728,7 +741,7 @@ def _w4_run(where, gated, x, weights, bias, act, y, workspace, stream):
     if workspace is not None:
         status = lib.gemm_w4a16_ws(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros, bias,
                                     act, out.data_ptr(), M, N, K, weights.group, gated, workspace.data_ptr(),
-                                    _nbytes(workspace), handle)
+                                    _workspace_bytes(where, workspace, device), handle)
     elif gated:
         status = lib.gemm_w4a16_gated(weights.gp_dtype, x.data_ptr(), weights.data.data_ptr(), weights.has_zeros,
                                        act, out.data_ptr(), M, N, K, weights.group, handle)

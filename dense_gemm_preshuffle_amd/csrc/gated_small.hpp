@@ -186,7 +186,7 @@ __global__ __launch_bounds__(WAVES * 64) void gated_small_kernel(GatedArgs p) {
     with_act(p.act, [&](auto act_c) GP_INLINE {
       constexpr int A = decltype(act_c)::value;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) h[r] = activate<A>(g[r]) * u[r];
+      for (int r = 0; r < 4; ++r) h[r] = activate_ffn<A>(g[r]) * u[r];
     });
     *(v2i*)(p.c + off) = pack_out4<DT>(h);
     if (p.gate) {

@@ -1020,7 +1020,7 @@ __device__ __forceinline__ void gemm_tile_body(const TileArgs& p, uint32_t w, ch
       store_half(p.c, [](Acc g, Acc u) GP_INLINE {
         v4f h;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) h[r] = activate<A>(g[r]) * u[r];
+        for (int r = 0; r < 4; ++r) h[r] = activate_ffn<A>(g[r]) * u[r];
         return h;
       });
     });

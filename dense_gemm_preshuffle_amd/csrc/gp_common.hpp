@@ -320,6 +320,13 @@ __device__ __forceinline__ float activate(float x) {
   else if constexpr (A == ACT_GELU) return 0.5f * x * (1.f + erf_as7126(x * 0.70710678118654752f));
   else return x;
 }
+// The same in the feed-forward and 4-bit products, whose ReLU keeps NaN (fmaxf
+// drops it: a product that failed would come out as 0).
+template <int A>
+__device__ __forceinline__ float activate_ffn(float x) {
+  if constexpr (A == ACT_RELU) return x < 0.f ? 0.f : x;
+  else return activate<A>(x);
+}
 template <class F>
 __device__ __forceinline__ void with_act(int act, F&& f) {
   switch (act) {

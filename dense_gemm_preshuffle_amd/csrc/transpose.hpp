@@ -94,8 +94,8 @@ __device__ __forceinline__ float widen16(uint32_t pair, int hi) {
 template <int A>
 __device__ __forceinline__ void activate_grad(float g, float& value, float& slope) {
   if constexpr (A == ACT_RELU) {
-    value = fmaxf(g, 0.f);
-    slope = g > 0.f ? 1.f : 0.f;
+    value = activate_ffn<A>(g);
+    slope = g <= 0.f ? 0.f : 1.f;
   } else if constexpr (A == ACT_SILU) {
     // e = e^-|g| by way of 2^64 e, since the hardware exponential returns 0
     // for results below 2^-126; s and 1 - s without cancellation on both sides

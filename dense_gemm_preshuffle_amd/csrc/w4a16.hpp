@@ -307,7 +307,7 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
       return t;
     };
     float o = total(b0) + (p.bias ? p.bias[n] : 0.f);
-    with_act(p.act, [&](auto act_c) GP_INLINE { o = activate<decltype(act_c)::value>(o); });
+    with_act(p.act, [&](auto act_c) GP_INLINE { o = activate_ffn<decltype(act_c)::value>(o); });
     if (p.gated) o *= total(b0 + 1);
     const uint32_t two = DT == DT_F16 ? pack_f16x2(o, 0.f) : pack_bf16x2(o, 0.f);
     *(uint16_t*)(p.y + ((size_t)(m0 + row) * p.N + n) * 2) = (uint16_t)two;

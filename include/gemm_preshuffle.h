@@ -393,7 +393,8 @@ int gemm_gated_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, size_t
  *   workspace   16-byte aligned, at least gemm_gated_backward_workspace_size
  *               bytes for the same outputs; its contents need not be set.
  * dg and du are rounded to the type before the two products, which accumulate
- * in fp32 and round once. relu'(0) is 0. The same call gives the same bits.
+ * in fp32 and round once. relu'(0) is 0; a NaN gate gives NaN with every act.
+ * The same call gives the same bits.
  */
 int gemm_gated_backward(int dtype, const void* dh, const void* gate, const void* up, const void* x, const void* w,
                         int act, void* dx, void* dw, int64_t M, int64_t F, int64_t H, void* workspace,
