@@ -35,7 +35,8 @@ __global__ __launch_bounds__(256) void preshuffle_gated_kernel(const char* __res
 //   start + rounds * (K tiles per range * step + ends) + ranges * join
 // of its workgroups on 256 CUs. step: a 128-byte K tile; ends: filling the
 // pipeline and storing the tile; join: writing a range's partial tile and the last
-// workgroup's reading it. Two workgroups on a CU take as long as one after the
+// workgroup's reading it (0: the tile is not split; a smaller one takes less
+// time wherever CUs would idle). Two workgroups on a CU take as long as one after the
 // other, so a started round counts whole. The constants come from timing every
 // tile with 1 to 16 ranges on one MI355X:
 //   row-major B: 40 shapes (M 32 to 5905, K 64 to 31744); the tile and ranges of
@@ -51,7 +52,7 @@ __global__ __launch_bounds__(256) void preshuffle_gated_kernel(const char* __res
 struct TileTime { int tm, tn; double step, ends, join; };
 constexpr TileTime kRowsTimes[] = {{256, 256, 1.21, 9.5, 3.2}, {128, 256, 0.99, 5.6, 2.1}, {128, 128, 0.60, 1.65, 1.25},
                                    {64, 128, 0.32, 2.15, 0.7}};
-constexpr TileTime kGatedTimes[] = {{256, 256, 1.5, 6.1, 4.0}, {128, 256, 0.56, 6.0, 3.0}, {128, 128, 0.60, 1.25, 1.35},
+constexpr TileTime kGatedTimes[] = {{256, 256, 1.5, 6.1, 0}, {128, 256, 0.56, 6.0, 3.0}, {128, 128, 0.60, 1.25, 1.35},
                                     {64, 128, 0.35, 0.73, 1.0}};
 double tile_us(const TileTime& t, int64_t M, int64_t N, int64_t Kb, int64_t ks, double speed = 1.0) {
   const double fill = (double)(((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn) * ks) / 256;
@@ -66,7 +67,7 @@ double choose_tile_us(const TileTime (&times)[4], int64_t M, int64_t N, int64_t 
     if (inside && (t.tm > M || t.tn > N)) continue;
     const int64_t n = ((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn), kt = Kb / 128;
     for (int64_t ks = 1; ks <= 16; ++ks) {
-      if (ks > 1 && (kt / ks < 4 || n * ks > 1024)) break;
+      if (ks > 1 && (t.join == 0 || kt / ks < 4 || n * ks > 1024)) break;
       const double us = tile_us(t, M, N, Kb, ks);
       if (best >= 0 && us >= best) continue;
       best = us;

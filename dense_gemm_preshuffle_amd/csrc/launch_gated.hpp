@@ -20,13 +20,12 @@ hipError_t launch_gated_small_f16(const GatedSmall& v, const GatedArgs& a, hipSt
 
 }  // namespace gp
 
-#define GP_GATED_CASE_IMPL(DT, TM, TN, KSV)                                                                    \
+#define GP_GATED_CASE(DT, TM, TN, KSV)                                                                         \
   if (tm == TM && tn == TN && (a.ksplit > 1) == KSV) {                                                         \
     hipLaunchKernelGGL((gemm_tile_kernel<DT, 16, TM, TN, 128, EPI_GATED, 3, false, 1, true, KSV>),             \
                        dim3(a.tiles_m * a.tiles_n * a.ksplit), dim3(64 * tile_waves(TM, TN)), 0, s, a);        \
     return hipGetLastError();                                                                                  \
   }
-#define GP_GATED_CASE(DT, TM, TN) GP_GATED_CASE_IMPL(DT, TM, TN, false) GP_GATED_CASE_IMPL(DT, TM, TN, true)
 #define GP_GATED_SMALL_CASE(DT, XL, P, W, S)                                                                   \
   if (v.xl == XL && v.pairs == P && v.waves == W && v.s == S) {                                                \
     constexpr uint32_t rows = XL == 0 ? 1 : 8 * XL;                                                            \

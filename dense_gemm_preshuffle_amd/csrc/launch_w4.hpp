@@ -40,7 +40,6 @@ hipError_t launch_w4_f16_z(const W4Plan& p, int sg, const W4Args& a, hipStream_t
     GP_W4_CASE(DT, ZV, 0, 2, 4, 2)                                                                             \
     GP_W4_CASE(DT, ZV, 1, 1, 16, 1)                                                                            \
     GP_W4_CASE(DT, ZV, 1, 2, 16, 1)                                                                            \
-    GP_W4_CASE(DT, ZV, 1, 2, 8, 1)                                                                             \
     GP_W4_CASE(DT, ZV, 1, 4, 4, 1)                                                                             \
     GP_W4_CASE(DT, ZV, 4, 1, 8, 1)                                                                             \
     GP_W4_CASE(DT, ZV, 4, 2, 8, 1)                                                                             \

@@ -141,8 +141,10 @@
 #define GP_WIDE_ALL(W) GP_WIDE_I8(W) GP_WIDE_FP8(W) GP_WIDE_BF16(W) GP_WIDE_FP4(W) GP_WIDE_F16(W)
 
 // Gated epilogue (BF16 / FP16, 16 x 16 blocks, 128-byte K tiles, 3 stages): X(dtype,
-// tile_m, tile_n), each with and without a K split across workgroups.
-#define GP_TILE_GATED(X, DT) X(DT, 256, 256) X(DT, 128, 256) X(DT, 128, 128) X(DT, 64, 128)
+// tile_m, tile_n, split of K across workgroups).
+#define GP_TILE_GATED(X, DT) \
+  X(DT, 256, 256, false) X(DT, 128, 256, false) X(DT, 128, 128, false) X(DT, 64, 128, false) \
+  X(DT, 128, 256, true) X(DT, 128, 128, true) X(DT, 64, 128, true)
 
 // Row-major B (BF16 / FP16, 16 x 16 blocks, 128-byte K tiles): X(dtype,
 // epilogue, tile_m, tile_n, stages, able to split K across workgroups). Three
