@@ -45,19 +45,23 @@ __global__ __launch_bounds__(256) void preshuffle_gated_kernel(const char* __res
 //     128 x 128 in one; 161 x 2656 x 10624 25.9 on 64 x 128 in four (35.0 in three,
 //     40.9 in five), 28.8 on 128 x 128 in six; transposed 4096 x 14336 x 128 39.4
 //     on 128 x 128, 41.9 on 256 x 256.
-//   gated: 24 shapes (M 70 to 7133, K 320 to 8192); within 8% on 23. 259 x 4384 x
+//   gated: 27 shapes (M 70 to 8192, K 320 to 8192); within 8% on 26. 259 x 4384 x
 //     6592 36.9 on 128 x 256 in four ranges, 38.7 on 128 x 128 in two; 509 x 14336 x
 //     4096 57.6 on 128 x 256, 62.4 on 128 x 128, 65.2 on 256 x 256 in two; 1536 x
-//     1984 x 512 7.4 on 128 x 128, 9.9 on 128 x 256.
-struct TileTime { int tm, tn; double step, ends, join; };
+//     1984 x 512 7.4 on 128 x 128, 9.9 on 128 x 256. Large ones run at the rate
+//     (PFLOP/s) that the power limit leaves a tile, the least time whatever the
+//     rounds: 8192 x 28672 x 4096 1378 on 256 x 256, 1412 on 128 x 256, 1647 on
+//     128 x 128.
+struct TileTime { int tm, tn; double step, ends, join, rate = 0; };
 constexpr TileTime kRowsTimes[] = {{256, 256, 1.21, 9.5, 3.2}, {128, 256, 0.99, 5.6, 2.1}, {128, 128, 0.60, 1.65, 1.25},
                                    {64, 128, 0.32, 2.15, 0.7}};
-constexpr TileTime kGatedTimes[] = {{256, 256, 1.5, 6.1, 0}, {128, 256, 0.56, 6.0, 3.0}, {128, 128, 0.60, 1.25, 1.35},
-                                    {64, 128, 0.35, 0.73, 1.0}};
+constexpr TileTime kGatedTimes[] = {{256, 256, 1.39, 6.1, 0, 1.42}, {128, 256, 0.56, 6.0, 3.0, 1.385},
+                                    {128, 128, 0.60, 1.25, 1.35, 1.19}, {64, 128, 0.35, 0.73, 1.0, 0.9}};
 double tile_us(const TileTime& t, int64_t M, int64_t N, int64_t Kb, int64_t ks, double speed = 1.0) {
   const double fill = (double)(((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn) * ks) / 256;
   const double rounds = fill <= 4 ? std::ceil(fill) : fill + 0.5;
-  return 3.5 + rounds * ((double)Kb / 128 / ks * t.step * speed + t.ends) + (ks > 1 ? ks * t.join : 0);
+  const double us = 3.5 + rounds * ((double)Kb / 128 / ks * t.step * speed + t.ends) + (ks > 1 ? ks * t.join : 0);
+  return t.rate > 0 ? std::max(us, (double)M * N * Kb * 1e-9 / t.rate) : us;   // Kb: two bytes, two operations
 }
 // The tile and K ranges of least time, and that time; below 0 if no tile fits.
 // inside: tiles no larger than the matrix.
