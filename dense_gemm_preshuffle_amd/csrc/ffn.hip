@@ -192,24 +192,24 @@ bool plan_rows(int64_t M, int64_t N, int64_t Kb, const Plan* other, double copie
 }
 
 // Both products in one launch, on 64 x 128 tiles: a [Ma][Na] over Ka K tiles, b
-// likewise. The workgroups share the CUs, so the time is that of all their work, or
-// of the longest:
-//   3.5 + max(sum of (K tiles * 0.4 + 0.6) / 256, longest) + joins   (us)
-// taken where it is 15% below the two products' times (it also saves a launch); on
-// 25 measured shapes the choice was 7% above the best of both on average. Products
-// of M x F x H on their best ranges, one launch against two: 130 x 2064 x 2048 16.6,
-// 22.4; 1116 x 672 x 480 9.5, 17.3; 57 x 3392 x 2080 18.1, 23.2; 606 x 4896 x 448
-// 28.9, 33.2; 682 x 5808 x 608 40.5, 39.7.
+// likewise. The workgroups share the CUs, two on each, so the time is that of all
+// their work, or of the longest, slowed by what runs beside it:
+//   3.5 + max(sum of (K tiles * 0.27 + 0.3) / 256, 1.4 * longest + 0.5) + joins (us)
+// taken where it is 5% below the two products' times (it also saves a launch). On
+// 25 shapes timed with every pair of ranges the choice was 3% above the best of
+// both on average, 17% at worst. Products of M x F x H on their best ranges, one
+// launch against two: 130 x 2064 x 2048 16.6, 22.4; 1116 x 672 x 480 9.5, 17.3; 57 x
+// 3392 x 2080 18.1, 23.2; 606 x 4896 x 448 28.9, 33.2; 682 x 5808 x 608 40.5, 39.7.
 bool plan_pair(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t Nb, int64_t Kb, double apart, Plan* a, Plan* b) {
   const int64_t ta = ((Ma + 63) / 64) * ((Na + 127) / 128), tb = ((Mb + 63) / 64) * ((Nb + 127) / 128);
-  if (ta + tb > 2048) return false;   // 71 x 6592 x 2784 (4576 tiles) 74 us, apart on larger tiles 66
-  double best = 0.85 * apart;
+  if (ta + tb > 2304) return false;   // 512 x 4096 x 4096 (4352 tiles) 89 us, apart on larger tiles 80
+  double best = 0.95 * apart;
   bool found = false;
   for (int64_t x = 1; x <= 16 && (x == 1 || (Ka / x >= 4 && ta * x <= 1024)); ++x)
     for (int64_t y = 1; y <= 16 && (y == 1 || (Kb / y >= 4 && tb * y <= 1024)); ++y) {
-      const double wa = 0.4 * (double)Ka / x + 0.6, wb = 0.4 * (double)Kb / y + 0.6;
-      const double us = 3.5 + std::max({(ta * x * wa + tb * y * wb) / 256, wa, wb}) + (x > 1 ? 0.55 * x : 0) +
-                        (y > 1 ? 0.55 * y : 0);
+      const double wa = 0.27 * (double)Ka / x + 0.3, wb = 0.27 * (double)Kb / y + 0.3;
+      const double us = 3.5 + std::max((ta * x * wa + tb * y * wb) / 256, 1.4 * std::max(wa, wb) + 0.5) +
+                        (double)(x > 1 ? x : 0) + (double)(y > 1 ? y : 0);
       if (us >= best) continue;
       best = us;
       found = true;
