@@ -18,8 +18,10 @@
 // constant operand whose result serves every column block; a zero point adds
 // z/8 of the same sum. What cancels there is at most 23 |x| per element
 // (16 |x| + |z| |x| with zero points) in fp32, far below the output's rounding.
-// Where x holds infinities, or the sums overflow, no finite number comes out;
-// such outputs are computed again, one by one, from the formula.
+// Where x or a scale is not finite, or the sums overflow, no finite number comes
+// out of that; a wave that holds such a sum goes over its share of K again, with
+// q - z itself as the operand (a whole number of at most 135, exact in both
+// types), and replaces the sums that were not finite alone.
 //
 // Layout: 16 output columns x 128 K per block of 1 KiB. Lane l of a wave reads
 // its 16 bytes at 16 l: column l % 16, K piece l / 16; dword j holds the eight
@@ -85,23 +87,19 @@ __device__ __forceinline__ float half_to_float(uint32_t bits) {
   else return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
 }
 
-// One output from the formula, for the sums that the split of q - z into u and
-// 8 + z cannot give (see above).
-template <int DT, int SG>
-__device__ __forceinline__ float w4_direct(const W4Args& p, uint32_t m, uint32_t nb, uint32_t col) {
-  const uint32_t kblk = (p.K + 127) / 128, sblk = (kblk + (1u << p.sshift) - 1) >> p.sshift;
-  const uint16_t* xr = (const uint16_t*)(p.x + (size_t)m * p.K * 2);
-  float sum = 0.f;
-  for (uint32_t k = 0; k < p.K; ++k) {
-    const uint32_t b = k / 128, j = k / 32 % 4, hi = k / 8 % 4, i = k % 8;
-    const uint32_t byte = (uint8_t)p.w[((size_t)nb * kblk + b) * 1024 + (hi * 16 + col) * 16 + j * 4 + (i & 3)];
-    const int u = (int)(i < 4 ? byte & 15u : byte >> 4);
-    const size_t g = (((size_t)nb * sblk + (b >> p.sshift)) * 16 + col) * SG + (SG > 1 ? j * SG / 4 : 0);
-    const int z = p.z ? (int)(int8_t)p.z[g] : 0;
-    const float s = half_to_float<DT>(((const uint16_t*)p.s)[g]);
-    sum = fmaf(half_to_float<DT>(xr[k]), s * (float)(u - 8 - z), sum);
+// Eight nibbles u = q + 8 -> eight 16-bit operands (u - 8 - z) f, without the
+// conversion's split: for the sums that it cannot give (see above).
+template <int DT>
+__device__ __forceinline__ v4i unpack_w4_less(int d, int z, float f) {
+  v4i o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t at = i < 2 ? 16 * i : 16 * (i - 2) + 4;   // elements 2 i, 2 i + 1
+    const float lo = f * (float)((int)((uint32_t)d >> at & 15u) - 8 - z),
+                hi = f * (float)((int)((uint32_t)d >> (at + 8) & 15u) - 8 - z);
+    o[i] = (int)(DT == DT_F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi));
   }
-  return sum;
+  return o;
 }
 
 // XL: 16-byte loads of x per lane and block: 1, 4, 8 or 16 serve 4, 16, 32 or
@@ -114,6 +112,7 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
   constexpr int NQ = MB * NB;
   constexpr int R = ONE ? 1 : 4;        // result registers that hold rows
   constexpr int STEPS = 4 / SG;         // K steps of 32 per scale inside a block
+  constexpr float kMaxFloat = 3.402823466e38f;
   static_assert(WAVES * (ROWS * 256 + NQ * 64 * R * 4) <= 160 * 1024, "LDS budget");
   __shared__ __attribute__((aligned(16))) char xs[WAVES * ROWS * 256];
   __shared__ __attribute__((aligned(16))) float red[WAVES * NQ * 64 * R];
@@ -267,12 +266,66 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
     if (ch < chunks) compute(P0{});
   }
 
+  uint32_t lost = 0;   // column blocks with a sum that is not finite
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb)
+  for (int nb = 0; nb < NB; ++nb) {
+    bool l = false;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-      for (int r = 0; r < R; ++r) red[((wave * NQ + mb * NB + nb) * R + r) * 64 + lane] = acc[mb][nb][r];
+      for (int r = 0; r < R; ++r) {
+        const float t = acc[mb][nb][r];
+        red[((wave * NQ + mb * NB + nb) * R + r) * 64 + lane] = t;
+        l |= !(fabsf(t) <= kMaxFloat);
+      }
+    lost |= __any(l) ? 1u << nb : 0u;
+  }
+  // Sums that are not finite, again with q - z as the operand: an infinity of x
+  // or of a scale meets the weight that the formula has there, 0 included. In BF16
+  // the operands carry 2^-16, which keeps the products of finite x finite (FP16's
+  // cannot overflow); a scale that is not finite goes into the operand, since a
+  // product x (q - z) of 0 would hide it. One column block at a time and
+  // straight from memory, whatever the number of such sums: 64 x 8192 x 28672 in
+  // BF16 76 us clean, 219 with a NaN in one row, 366 with nothing but NaN; one row
+  // 23, 34, 77 (output by output each would take K dependent steps).
+  while (lost) {
+    const uint32_t blk = __builtin_ctz(lost);
+    lost &= lost - 1;
+    constexpr int kDown = DT == DT_BF16 ? 16 : 0;
+    v4f sum[MB];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) sum[mb] = v4f{0.f, 0.f, 0.f, 0.f};
+    // steps of 32 K; few rows: not unrolled, for the registers of two workgroups per CU
+#pragma unroll(XL <= 1 ? 1 : XL <= 8 ? 4 : 2)
+    for (uint32_t step = 4 * kb0; step < 4 * kb1; ++step) {
+      const uint32_t b = step / 4, j = step % 4, go = (blk * sblk * 16 + lane_lo) * SG + (SG > 1 ? j * SG / 4 : 0),
+                     gs = (b >> p.sshift) * 16 * SG, col = 64 * j + 16 * lane_hi;
+      const int wd = buf_load4(rw, blk * kblk * 1024 + lane * 16 + 4 * j, b * 1024);
+      float sc = half_to_float<DT>(__builtin_amdgcn_raw_buffer_load_b16(rs, go * 2, gs * 2, 0));
+      const int z = ZERO ? (int)(int8_t)__builtin_amdgcn_raw_buffer_load_b8(rz, go, gs, 0) : 0;
+      float f = DT == DT_BF16 ? 0x1p-16f : 1.f;
+      if (!(fabsf(sc) <= kMaxFloat)) {
+        f = sc;
+        sc = 1.f;
+      }
+      const v4i wv = unpack_w4_less<DT>(wd, z, f);
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        const uint32_t m = ONE ? 0 : (mb * 16 + lane_lo) % ROWS;
+        const v4i xv = buf_load16(rx, 256 * b + col < Kb ? m * Kb + col : kOOB, 256 * b);
+        const v4f part = mfma<DT>(&xv, &wv, v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int r = 0; r < R; ++r) sum[mb][r] = fmaf(sc, part[r], sum[mb][r]);
+      }
+    }
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float& t = red[((wave * NQ + mb * NB + blk) * R + r) * 64 + lane];
+        if (!(fabsf(t) <= kMaxFloat)) t = ldexpf(sum[mb][r], kDown);
+      }
+  }
   __syncthreads();
 
   constexpr uint32_t PB = NQ * R * 256;   // bytes of one workgroup's sums
@@ -298,12 +351,9 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
     if (nb >= p.nblk || n >= p.N || row >= mrows) continue;
     auto total = [&](int blk) GP_INLINE {
       const int qr = (mb * NB + blk) * R + r;
+      if (p.ksplit <= 1) return sum_waves(qr);
       float t = 0.f;
-      if (p.ksplit > 1)
-        for (uint32_t z = 0; z < p.ksplit; ++z) t += buf_load4_coh(rp, z * PB + qr * 256 + lane * 4);
-      else
-        t = sum_waves(qr);
-      if (!(fabsf(t) <= 3.402823466e38f)) t = w4_direct<DT, SG>(p, m0 + row, nb0 + blk, lane_lo);
+      for (uint32_t z = 0; z < p.ksplit; ++z) t += buf_load4_coh(rp, z * PB + qr * 256 + lane * 4);
       return t;
     };
     float o = total(b0) + (p.bias ? p.bias[n] : 0.f);

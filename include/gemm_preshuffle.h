@@ -449,7 +449,8 @@ int gemm_w4a16_preshuffle(int dtype, const void* q, const void* scales, const in
  *   bias                      device fp32 [N], or NULL.
  * All device pointers 16-byte aligned (GP_EINVAL). The same call gives the
  * same bits. Any M is served, more than 64 rows in blocks that read the
- * weights again.
+ * weights again. Infinities and NaN in x or the scales give what the formula
+ * gives, in their own rows and columns; such a call takes up to 5 times as long.
  */
 int gemm_w4a16(int dtype, const void* x, const void* w_shuf, int has_zeros, const float* bias, int act, void* y,
                int64_t M, int64_t N, int64_t K, int group, void* stream);
