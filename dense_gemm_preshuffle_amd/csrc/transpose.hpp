@@ -105,9 +105,10 @@ __device__ __forceinline__ void activate_grad(float g, float& value, float& slop
     value = g * s;
     slope = s * (1.f + g * t);
   } else if constexpr (A == ACT_GELU) {
-    const float P = 0.5f * (1.f + erf_as7126(g * 0.70710678118654752f));
+    float e;
+    const float P = normal_cdf(g, e);
     value = g * P;
-    slope = P + g * (0.39894228040143268f * __expf(-0.5f * g * g));
+    slope = P + g * (0.39894228040143268f * e);
   } else {
     value = g;
     slope = 1.f;
