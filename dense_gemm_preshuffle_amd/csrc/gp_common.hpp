@@ -343,9 +343,19 @@ __device__ __forceinline__ float normal_cdf(float g, float& e) {
   return g < 0.f ? tail : 1.f - tail;
 }
 
+// s = 1 / (1 + e^-g) and t = 1 - s, without cancellation on either side and, by way
+// of 2^64 e^-|g| (the hardware exponential returns 0 for results below 2^-126), down
+// to the smallest numbers: 1 / (1 + e^88) is below the reciprocal's range.
+__device__ __forceinline__ void sigmoid_pair(float g, float& s, float& t) {
+  const float e = ldexpf(__builtin_amdgcn_exp2f(64.f - 1.44269504088896341f * fabsf(g)), -64);
+  const float r = __builtin_amdgcn_rcpf(1.f + e);
+  s = g >= 0.f ? r : e * r;
+  t = g >= 0.f ? e * r : r;
+}
+
 // The same in the feed-forward and 4-bit products, whose ReLU keeps NaN (fmaxf
-// drops it: a product that failed would come out as 0) and whose GELU keeps its
-// relative precision for negative x.
+// drops it: a product that failed would come out as 0) and whose GELU and SiLU keep
+// their relative precision for negative x.
 template <int A>
 __device__ __forceinline__ float activate_ffn(float x) {
   if constexpr (A == ACT_RELU) {
@@ -353,6 +363,10 @@ __device__ __forceinline__ float activate_ffn(float x) {
   } else if constexpr (A == ACT_GELU) {
     float e;
     return x * normal_cdf(x, e);
+  } else if constexpr (A == ACT_SILU) {
+    float s, t;
+    sigmoid_pair(x, s, t);
+    return x * s;
   } else {
     return activate<A>(x);
   }

@@ -45,7 +45,7 @@ LOW = {"gelu": -13.0, "silu": -96.0}
 
 @pytest.mark.parametrize("dtype", F64.TYPES)
 @pytest.mark.parametrize("M", [1, 24, 64, 65, 320])     # one row, few, the small kernel's last, tiles
-@pytest.mark.parametrize("act", ["gelu"])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
 def test_gated(act, M, dtype):
     """Row m: gate p[m, f], up 1, by weights that copy: h is the activation of p."""
     import torch
@@ -64,7 +64,7 @@ def test_gated(act, M, dtype):
 
 
 @pytest.mark.parametrize("dtype", F64.TYPES)
-@pytest.mark.parametrize("act", ["gelu"])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
 def test_gated_backward(act, dtype):
     """dh = up = 1 and weights that copy dg or du to dx: the derivative and the activation."""
     import torch
@@ -87,7 +87,7 @@ def test_gated_backward(act, dtype):
 
 @pytest.mark.parametrize("dtype", F64.TYPES)
 @pytest.mark.parametrize("M", [1, 3, 16, 40])
-@pytest.mark.parametrize("act", ["gelu"])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
 def test_w4(act, M, dtype):
     """Integers 1 at one K per column, scale 1: y is the activation of x's element."""
     import torch
