@@ -30,6 +30,7 @@ points have the names of the C ABI (include/gemm_preshuffle.h):
     gemm_w4a16(x, weights, bias, act)                -> act(x W^T + bias) (BF16 / FP16 activations)
     gemm_w4a16_gated(x, weights, act)                -> act(x Wg^T) * (x Wu^T) on 4-bit weights
     w4a16_workspace(M, weights)                      -> a device workspace of these (None: none needed)
+    gemm_gated_plan, gemm_w4a16_plan                 -> dict, the kernel they run (host-only)
 
 Tensors: A is [M, K] (INT8 / FP8 as any 1-byte dtype, BF16 / FP16 as
 bfloat16 / float16 or a 2-byte integer view, MXFP4 as uint8 [M, K/2]; W4A8:
@@ -52,8 +53,9 @@ __all__ = [
     "gemm_gated_preshuffle", "gemm_gated", "gemm_gated_workspace_size", "gated_workspace", "gemm_gated_backward",
     "gemm_gated_backward_workspace_size", "gated_backward_workspace", "gemm_backward", "gemm_backward_workspace_size",
     "backward_workspace", "W4Weights", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle", "gemm_w4a16",
-    "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "w4a16_workspace", "gemm_status_string", "source_hash", "DTYPES",
-    "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE", "KERNEL_SPLITK", "KERNEL_WIDE",
+    "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "w4a16_workspace", "gemm_gated_plan", "gemm_w4a16_plan",
+    "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE", "KERNEL_SPLITK",
+    "KERNEL_WIDE",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -159,6 +161,8 @@ def load_library():
     lib.gemm_w4a16.argtypes = [ci, vp, vp, ci, vp, ci, vp, i64, i64, i64, ci, vp]
     lib.gemm_w4a16_gated.argtypes = [ci, vp, vp, ci, ci, vp, i64, i64, i64, ci, vp]
     lib.gemm_w4a16_workspace_size.argtypes = [i64, i64, i64, ci, ci, psz]
+    lib.gemm_gated_plan.argtypes = [ci, i64, i64, i64, ctypes.POINTER(GemmPlanInfo)]
+    lib.gemm_w4a16_plan.argtypes = [i64, i64, i64, ci, ci, ci, ctypes.POINTER(GemmPlanInfo)]
     lib.gemm_w4a16_ws.argtypes = [ci, vp, vp, ci, vp, ci, vp, i64, i64, i64, ci, ci, vp, sz, vp]
     lib.gemm_status_string.argtypes = [ci]
     lib.gemm_status_string.restype = ctypes.c_char_p
@@ -171,7 +175,8 @@ def load_library():
               "gemm_gated_preshuffle", "gemm_gated", "gemm_gated_workspace_size", "gemm_gated_backward",
               "gemm_gated_backward_workspace_size",
               "gemm_backward", "gemm_backward_workspace_size", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle",
-              "gemm_w4a16", "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "gemm_w4a16_ws"):
+              "gemm_w4a16", "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "gemm_w4a16_ws", "gemm_gated_plan",
+              "gemm_w4a16_plan"):
         getattr(lib, f).restype = ci
     _lib = lib
     return lib
@@ -521,6 +526,13 @@ def gemm_gated_workspace_size(dtype, M: int, F: int, H: int) -> int:
     return _size("gemm_gated_workspace_size", _dt(dtype), M, F, H)
 
 
+def gemm_gated_plan(dtype, M: int, F: int, H: int) -> dict:
+    """Host-only: the kernel that gemm_gated runs for these sizes."""
+    info = GemmPlanInfo()
+    _check(load_library().gemm_gated_plan(_dt(dtype), M, F, H, ctypes.byref(info)), "gemm_gated_plan")
+    return {name: getattr(info, name) for name, _ in GemmPlanInfo._fields_}
+
+
 def gated_workspace(dtype, M: int, F: int, H: int, device="cuda"):
     """A zero-filled device workspace for gemm_gated (None when none is needed). Zero once here;
     every call leaves its counters zero again. Calls that may overlap need one each."""
@@ -697,6 +709,14 @@ def gemm_w4a16_workspace_size(M: int, N: int, K: int, group: int, gated=False) -
     """Host-only: workspace bytes with which a 4-bit product of these sizes (gated: N is F) may split K
     across workgroups (0: it does not)."""
     return _size("gemm_w4a16_workspace_size", M, N, K, group, int(gated))
+
+
+def gemm_w4a16_plan(M: int, N: int, K: int, group: int, gated=False, with_workspace=False) -> dict:
+    """Host-only: the kernel variant of a 4-bit product of these sizes (gated: N is F)."""
+    info = GemmPlanInfo()
+    _check(load_library().gemm_w4a16_plan(M, N, K, group, int(gated), int(with_workspace), ctypes.byref(info)),
+           "gemm_w4a16_plan")
+    return {name: getattr(info, name) for name, _ in GemmPlanInfo._fields_}
 
 
 def w4a16_workspace(M: int, weights: W4Weights):

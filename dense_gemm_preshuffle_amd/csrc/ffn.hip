@@ -434,6 +434,26 @@ int gemm_gated_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, size_t
   return GP_OK;
 }
 
+int gemm_gated_plan(int dtype, int64_t M, int64_t F, int64_t H, gemm_plan_info* out) {
+  if (!out) return GP_EINVAL;
+  GatedPlan p;
+  const int r = plan_gated(dtype, M, F, H, &p);
+  if (r) return r;
+  *out = gemm_plan_info();
+  const int64_t rows = p.variant.xl == 0 ? 1 : 8 * p.variant.xl;
+  out->kernel = p.small ? GP_KERNEL_SPLITK : GP_KERNEL_TILE;
+  out->tile_m = p.small ? (int)rows : p.tile.tm;
+  out->tile_n = p.small ? 32 * p.variant.pairs : p.tile.tn;
+  out->tile_k = p.small ? 64 * p.variant.s : 64;
+  out->waves = p.small ? p.variant.waves : tile_waves(p.tile.tm, p.tile.tn);
+  out->threads = 64 * out->waves;
+  out->ksplit = p.small ? (int)p.ks : p.tile.ks;
+  out->grid = out->ksplit * (p.small ? p.tiles : (M + p.tile.tm - 1) / p.tile.tm * ((2 * F + p.tile.tn - 1) / p.tile.tn));
+  out->mfma = 16;
+  out->workspace_bytes = p.bytes;
+  return GP_OK;
+}
+
 int gemm_gated(int dtype, const void* x, const void* w_shuf, int act, void* h, void* gate, void* up, int64_t M,
                int64_t F, int64_t H, void* workspace, size_t workspace_bytes, void* stream) {
   if (!x || !w_shuf || !h || !is_aligned16(x) || !is_aligned16(w_shuf) || !is_aligned16(h)) return GP_EINVAL;

@@ -104,7 +104,7 @@ __global__ __launch_bounds__(256) void layout_w4_kernel(W4LayoutArgs p) {
 //     (pairs 9.5); 32 rows 14336 x 8192 19.0 on fours (25.9, 40.9), 4096 x 4096
 //     7.6 on single ones (8.7); 64 rows 14336 x 8192 33.9 on fours (46.5).
 // split: with a workspace, K is split where few column blocks leave CUs idle.
-struct W4Split { int64_t ks = 1, bytes = 0; };
+struct W4Split { int64_t tiles = 0, ks = 1, bytes = 0; };
 int plan_w4(int64_t M, const W4Layout& l, bool gated, bool split, W4Plan* p, W4Split* k) {
   p->xl = M == 1 ? 0 : M <= 4 ? 1 : M <= 16 ? 4 : M <= 32 ? 8 : 16;
   if (p->xl <= 1) {
@@ -125,6 +125,7 @@ int plan_w4(int64_t M, const W4Layout& l, bool gated, bool split, W4Plan* p, W4S
   const int64_t rows = p->xl == 0 ? 1 : 4 * p->xl;
   const int64_t wgs = ((l.nblk + p->nb - 1) / p->nb) * ((M + rows - 1) / rows);
   if (wgs * p->waves * 64 >= (int64_t)1 << 32) return GP_ESHAPE;
+  k->tiles = wgs;
   if (split) {
     const double step_us = p->xl <= 1 ? 0.45 : p->xl == 4 ? 0.55 : p->xl == 8 ? 1.0 : 1.9;
     k->ks = split_small((double)l.kblk / p->waves, step_us, wgs);
@@ -250,6 +251,29 @@ int gemm_w4a16_workspace_size(int64_t M, int64_t N, int64_t K, int group, int ga
   W4Split k;
   if ((r = plan_w4(M, l, gated != 0, true, &p, &k))) return r;
   *bytes = (size_t)k.bytes;
+  return GP_OK;
+}
+
+int gemm_w4a16_plan(int64_t M, int64_t N, int64_t K, int group, int gated, int with_workspace, gemm_plan_info* out) {
+  if (!out || M <= 0) return GP_EINVAL;
+  if (M >= kMaxBytes || N >= kMaxBytes / 2) return GP_ESHAPE;
+  W4Layout l;
+  int r = layout_w4(gated ? 2 * N : N, K, group, false, gated != 0, &l);
+  if (r) return r;
+  W4Plan p;
+  W4Split k;
+  if ((r = plan_w4(M, l, gated != 0, with_workspace != 0, &p, &k))) return r;
+  *out = gemm_plan_info();
+  out->kernel = GP_KERNEL_SPLITK;
+  out->tile_m = p.xl == 0 ? 1 : 4 * p.xl;
+  out->tile_n = 16 * p.nb;
+  out->tile_k = 128 * p.s;
+  out->waves = p.waves;
+  out->threads = 64 * p.waves;
+  out->ksplit = (int)k.ks;
+  out->grid = k.tiles * k.ks;
+  out->mfma = 16;
+  out->workspace_bytes = k.bytes;
   return GP_OK;
 }
 

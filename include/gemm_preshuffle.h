@@ -383,6 +383,15 @@ int gemm_gated(int dtype, const void* x, const void* w_shuf, int act, void* h, v
 int gemm_gated_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, size_t* bytes);
 
 /*
+ * gemm_gated_plan -- host-only: the kernel that gemm_gated runs for these sizes.
+ * kernel is GP_KERNEL_TILE or GP_KERNEL_SPLITK (few rows; waves split K); tile_m
+ * rows and tile_n weight rows (gate and up) per workgroup, tile_k elements of K
+ * per step of a workgroup (tile) or of a wave; waves, threads, grid, ksplit and
+ * workspace_bytes as in gemm_plan_info, whose other members are 0.
+ */
+int gemm_gated_plan(int dtype, int64_t M, int64_t F, int64_t H, gemm_plan_info* out);
+
+/*
  * gemm_gated_backward -- gradients of gemm_gated from dh = dL/dh and the kept
  * gate and up:
  *   dg = dh * up * act'(gate),  du = dh * act(gate)
@@ -474,6 +483,10 @@ int gemm_w4a16_ws(int dtype, const void* x, const void* w_shuf, int has_zeros, c
 
 /* Host-only: the workspace bytes of gemm_w4a16_ws for these sizes (0: none). */
 int gemm_w4a16_workspace_size(int64_t M, int64_t N, int64_t K, int group, int gated, size_t* bytes);
+
+/* gemm_w4a16_plan -- host-only: the kernel variant of a 4-bit product, as
+ * gemm_gated_plan gives it (GP_KERNEL_SPLITK); with_workspace: of gemm_w4a16_ws. */
+int gemm_w4a16_plan(int64_t M, int64_t N, int64_t K, int group, int gated, int with_workspace, gemm_plan_info* out);
 
 /* Static, human-readable description of a gp_status value. */
 const char* gemm_status_string(int status);
