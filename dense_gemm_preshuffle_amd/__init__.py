@@ -533,13 +533,23 @@ def gemm_gated_plan(dtype, M: int, F: int, H: int) -> dict:
     return {name: getattr(info, name) for name, _ in GemmPlanInfo._fields_}
 
 
-def gated_workspace(dtype, M: int, F: int, H: int, device="cuda"):
-    """A zero-filled device workspace for gemm_gated (None when none is needed). Zero once here;
-    every call leaves its counters zero again. Calls that may overlap need one each."""
+def _split_workspace(n: int, device):
+    """n bytes with zero arrival counters (the first 64 KiB). The partial sums after them are written before
+    they are read; clearing them too made gemm_gated without a workspace of the caller's 46.0 us instead of
+    36.4 at 259 x 2192 x 6560 (28 MB)."""
     import torch
 
-    n = gemm_gated_workspace_size(dtype, M, F, H)
-    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+    if not n:
+        return None
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:65536].zero_()
+    return ws
+
+
+def gated_workspace(dtype, M: int, F: int, H: int, device="cuda"):
+    """A device workspace for gemm_gated, its counters zero (None when none is needed). Zero once here;
+    every call leaves its counters zero again. Calls that may overlap need one each."""
+    return _split_workspace(gemm_gated_workspace_size(dtype, M, F, H), device)
 
 
 def gemm_gated(dtype, x, w_shuf, act="silu", save=False, h=None, gate=None, up=None, workspace=None, stream=None):
@@ -720,12 +730,10 @@ def gemm_w4a16_plan(M: int, N: int, K: int, group: int, gated=False, with_worksp
 
 
 def w4a16_workspace(M: int, weights: W4Weights):
-    """A zero-filled device workspace for products of M rows on these weights (None when none is needed).
+    """A device workspace for products of M rows on these weights, its counters zero (None when none is needed).
     Zero once here; every call leaves its counters zero again. Calls that may overlap need one each."""
-    import torch
-
-    n = gemm_w4a16_workspace_size(M, weights.N, weights.K, weights.group, weights.gated)
-    return torch.zeros(n, dtype=torch.uint8, device=weights.device) if n else None
+    return _split_workspace(gemm_w4a16_workspace_size(M, weights.N, weights.K, weights.group, weights.gated),
+                            weights.device)
 
 
 def _w4_run(where, gated, x, weights, bias, act, y, workspace, stream):
