@@ -229,15 +229,19 @@ struct TileCfg {
 // Tile (tm, tn) and K split z of this workgroup. With a K split the ksplit
 // workgroups of one tile are consecutive in the logical order, so with the
 // XCD-aware order they run on the same XCD and meet in its L2.
+// ANY: that order for any number of workgroups (the XCDs' ranges may differ by
+// one); else only where 8 divides it. Gated, 6000 x 20000 x 2560 on 128 x 256 tiles
+// (3713 of them): 466 us, 700 row by row. The older epilogues keep their order.
+template <bool ANY = false>
 __device__ __forceinline__ void tile_coords(const TileArgs& p, uint32_t w, uint32_t& tm, uint32_t& tn, uint32_t& z) {
   const uint32_t T = p.tiles_m * p.tiles_n;
   const uint32_t S = p.ksplit;
   const uint32_t G = T * S;
-  if (p.xcd && (G % 8u) == 0) {
+  if (p.xcd && (ANY || (G % 8u) == 0)) {
     // Workgroups go round-robin to the 8 XCDs; give each XCD a contiguous
     // range of tiles, then walk it in groups of 8 M-tiles so that the tiles
     // resident together on one XCD share A rows and B columns in its L2.
-    const uint32_t logical = (w % 8u) * (G / 8u) + (w / 8u);
+    const uint32_t logical = (w % 8u) * (G / 8u) + (ANY ? min(w % 8u, G % 8u) : 0u) + (w / 8u);
     z = logical % S;
     const uint32_t t = logical / S;
     const uint32_t GROUP = 8u;
@@ -297,7 +301,7 @@ __device__ __forceinline__ void gemm_tile_body(const TileArgs& p, uint32_t w, ch
   const int lgrp = lane / MS;
 
   uint32_t tm, tn, kz;
-  tile_coords(p, w, tm, tn, kz);
+  tile_coords<C::ROWS || EPI == EPI_GATED>(p, w, tm, tn, kz);
   uint32_t m0 = tm * TM, n0 = tn * TN, mskip, nskip;
   if constexpr (C::ROWS) {
     // a matrix smaller than the tile: rows of A past it read zeros, what B
