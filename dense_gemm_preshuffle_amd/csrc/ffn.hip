@@ -48,20 +48,20 @@ __global__ __launch_bounds__(256) void preshuffle_gated_kernel(const char* __res
 //   gated: 27 shapes (M 70 to 8192, K 320 to 8192); within 8% on 26. 259 x 4384 x
 //     6592 36.9 on 128 x 256 in four ranges, 38.7 on 128 x 128 in two; 509 x 14336 x
 //     4096 57.6 on 128 x 256, 62.4 on 128 x 128, 65.2 on 256 x 256 in two; 1536 x
-//     1984 x 512 7.4 on 128 x 128, 9.9 on 128 x 256. Large ones run at the rate
-//     (PFLOP/s) that the power limit leaves a tile, the least time whatever the
-//     rounds: 8192 x 28672 x 4096 1378 on 256 x 256, 1412 on 128 x 256, 1647 on
-//     128 x 128.
-struct TileTime { int tm, tn; double step, ends, join, rate = 0; };
+//     1984 x 512 7.4 on 128 x 128, 9.9 on 128 x 256. The 256 x 256 tile's constants
+//     from 45 large ones (80 to 2100 GFLOP, M from 512) timed on the three largest
+//     tiles in turn, checked on 72 others: the choice is 0.7% above the best of the
+//     three on average there, 10% at worst. 557 x 15328 x 7488 158 on 256 x 256,
+//     180 on 128 x 256; 7292 x 21472 x 512 182, 149; 8192 x 28672 x 4096 1372, 1361.
+struct TileTime { int tm, tn; double step, ends, join; };
 constexpr TileTime kRowsTimes[] = {{256, 256, 1.21, 9.5, 3.2}, {128, 256, 0.99, 5.6, 2.1}, {128, 128, 0.60, 1.65, 1.25},
                                    {64, 128, 0.32, 2.15, 0.7}};
-constexpr TileTime kGatedTimes[] = {{256, 256, 1.39, 6.1, 0, 1.42}, {128, 256, 0.56, 6.0, 3.0, 1.385},
-                                    {128, 128, 0.60, 1.25, 1.35, 1.19}, {64, 128, 0.35, 0.73, 1.0, 0.9}};
+constexpr TileTime kGatedTimes[] = {{256, 256, 1.07, 14.4, 0}, {128, 256, 0.56, 6.0, 3.0}, {128, 128, 0.60, 1.25, 1.35},
+                                    {64, 128, 0.35, 0.73, 1.0}};
 double tile_us(const TileTime& t, int64_t M, int64_t N, int64_t Kb, int64_t ks, double speed = 1.0) {
   const double fill = (double)(((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn) * ks) / 256;
   const double rounds = fill <= 4 ? std::ceil(fill) : fill + 0.5;
-  const double us = 3.5 + rounds * ((double)Kb / 128 / ks * t.step * speed + t.ends) + (ks > 1 ? ks * t.join : 0);
-  return t.rate > 0 ? std::max(us, (double)M * N * Kb * 1e-9 / t.rate) : us;   // Kb: two bytes, two operations
+  return 3.5 + rounds * ((double)Kb / 128 / ks * t.step * speed + t.ends) + (ks > 1 ? ks * t.join : 0);
 }
 // The tile and K ranges of least time, and that time; below 0 if no tile fits.
 // inside: tiles no larger than the matrix.
