@@ -20,7 +20,7 @@
 namespace gp {
 
 struct GatedArgs {
-  const char* a;      // [M][Kb] activations
+  const char* a;      // [M][Ka] activations
   const char* b;      // preshuffled, gate and up blocks alternating
   char* c;            // [M][F]
   char* gate;         // [M][F] products to keep, or null
