@@ -600,7 +600,8 @@ def gemm_gated_backward(dtype, dh, gate, up, x, w, act="silu", want_dx=True, wan
                         workspace=None, stream=None):
     """(dx [M, H], dw [2F, H]) of gemm_gated from dh and the kept gate and up
     ([M, F]); w [2F, H] row-major. An output that is not wanted is None, and the
-    operand that it alone needs (w for dx, x for dw) may be None."""
+    operand that it alone needs (w for dx, x for dw) may be None. The gradients of
+    gate and up are rounded to the type on the way (fp16: infinite beyond 65504)."""
     dt, t = _half(dtype)
     M, F = dh.shape
     dev = dh.device

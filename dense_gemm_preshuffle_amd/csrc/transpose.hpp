@@ -116,7 +116,9 @@ __device__ __forceinline__ void activate_grad(float g, float& value, float& slop
 //   dg = dh * up * act'(gate), du = dh * act(gate)
 // in fp32, rounded once to the 16-bit type the matrix products read (the
 // products' own results are rounded to it as well, so this adds at most as
-// much error again). Written as d [M][Np] (dg, du, then zeros from 2F to Np in
+// much error again: normwise 0.00235 against float64 in bf16 where an fp32 form has
+// 0.00166, in fp16 0.000293 and 0.000207; operands in two 16-bit parts would
+// double the products, which are 85% of a large call). Written as d [M][Np] (dg, du, then zeros from 2F to Np in
 // each row; null if no product reads it) and dt = d^T [2F][Mp], zeros from M to
 // Mp (null likewise). F % 16 == 0.
 struct GateGradArgs {

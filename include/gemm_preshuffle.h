@@ -356,7 +356,8 @@ int gemm_plan_ws(int in_dtype, int64_t M, int64_t N, int64_t K, const gemm_opts*
  * x [M][H], h / g / u [M][F], both weights in one matrix w [2F][H]: the F gate
  * rows, then the F up rows. act is a GP_ACT_* (the activations above). M is
  * free, F % 16 == 0, H % 32 == 0 (else GP_ESHAPE), every matrix below 2^31
- * bytes; the buffers of one type (GP_BF16 or GP_F16, else GP_EDTYPE).
+ * bytes; the buffers of one type (GP_BF16 or GP_F16, else GP_EDTYPE). Outputs and
+ * workspaces overlap no other buffer of the call (not checked, but for the layouts).
  *
  * gemm_gated_preshuffle -- w [2F][H] -> w_shuf (4 F H' bytes, H' = H rounded up
  * to a multiple of 64; no overlap): the layout of gemm_preshuffle_b with 16-row
@@ -402,8 +403,11 @@ int gemm_gated_plan(int dtype, int64_t M, int64_t F, int64_t H, gemm_plan_info* 
  *   workspace   16-byte aligned, at least gemm_gated_backward_workspace_size
  *               bytes for the same outputs; its contents need not be set.
  * dg and du are rounded to the type before the two products, which accumulate
- * in fp32 and round once. relu'(0) is 0; a NaN gate gives NaN with every act.
- * The same call gives the same bits.
+ * in fp32 and round once: in FP16 a dg or du beyond 65504 is infinite, one below
+ * 2^-25 zero, as dh itself would be (a scaled loss keeps both inside). relu'(0)
+ * is 0; a NaN gate gives NaN with every act. The same call gives the same bits.
+ * For the limit of 2^31 bytes M and 2 F count rounded up, by a sixteenth at most
+ * (and to multiples of 64).
  */
 int gemm_gated_backward(int dtype, const void* dh, const void* gate, const void* up, const void* x, const void* w,
                         int act, void* dx, void* dw, int64_t M, int64_t F, int64_t H, void* workspace,
@@ -421,7 +425,8 @@ int gemm_gated_backward_workspace_size(int dtype, int64_t M, int64_t F, int64_t 
  *   da, db      outputs; either may be NULL, not both.
  *   workspace   16-byte aligned, at least gemm_backward_workspace_size bytes
  *               for the same outputs; its contents need not be set.
- * N % 32 == 0 and K % 32 == 0 (else GP_ESHAPE); M is free.
+ * N % 32 == 0 and K % 32 == 0 (else GP_ESHAPE); M is free. Every matrix is below
+ * 2^31 bytes with M rounded up, by a sixteenth at most (and to 64 rows).
  */
 int gemm_backward(int dtype, const void* dc, const void* a, const void* b, void* da, void* db, int64_t M, int64_t N,
                   int64_t K, void* workspace, size_t workspace_bytes, void* stream);
