@@ -31,6 +31,7 @@ points have the names of the C ABI (include/gemm_preshuffle.h):
     gemm_w4a16_gated(x, weights, act)                -> act(x Wg^T) * (x Wu^T) on 4-bit weights
     w4a16_workspace(M, weights)                      -> a device workspace of these (None: none needed)
     gemm_gated_plan, gemm_w4a16_plan                 -> dict, the kernel they run (host-only)
+    gemm_backward_plan                               -> two of them, or None (host-only)
 
 Tensors: A is [M, K] (INT8 / FP8 as any 1-byte dtype, BF16 / FP16 as
 bfloat16 / float16 or a 2-byte integer view, MXFP4 as uint8 [M, K/2]; W4A8:
@@ -54,8 +55,8 @@ __all__ = [
     "gemm_gated_backward_workspace_size", "gated_backward_workspace", "gemm_backward", "gemm_backward_workspace_size",
     "backward_workspace", "W4Weights", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle", "gemm_w4a16",
     "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "w4a16_workspace", "gemm_gated_plan", "gemm_w4a16_plan",
-    "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE", "KERNEL_SPLITK",
-    "KERNEL_WIDE",
+    "gemm_backward_plan", "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE",
+    "KERNEL_SPLITK", "KERNEL_WIDE", "KERNEL_ROWS", "KERNEL_PAIR",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -75,7 +76,7 @@ GP_EWORKSPACE = 6
 # gp_act values of the C ABI
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 EPI_AUTO, EPI_DIRECT, EPI_CSHUFFLE = 0, 1, 2
-KERNEL_AUTO, KERNEL_TILE, KERNEL_SPLITK, KERNEL_WIDE = 0, 1, 2, 3
+KERNEL_AUTO, KERNEL_TILE, KERNEL_SPLITK, KERNEL_WIDE, KERNEL_ROWS, KERNEL_PAIR = 0, 1, 2, 3, 4, 5
 
 
 class GemmError(RuntimeError):
@@ -161,6 +162,8 @@ def load_library():
     lib.gemm_w4a16.argtypes = [ci, vp, vp, ci, vp, ci, vp, i64, i64, i64, ci, vp]
     lib.gemm_w4a16_gated.argtypes = [ci, vp, vp, ci, ci, vp, i64, i64, i64, ci, vp]
     lib.gemm_w4a16_workspace_size.argtypes = [i64, i64, i64, ci, ci, psz]
+    lib.gemm_backward_plan.argtypes = [ci, i64, i64, i64, ci, ci, ci, ctypes.POINTER(GemmPlanInfo),
+                                       ctypes.POINTER(GemmPlanInfo)]
     lib.gemm_gated_plan.argtypes = [ci, i64, i64, i64, ctypes.POINTER(GemmPlanInfo)]
     lib.gemm_w4a16_plan.argtypes = [i64, i64, i64, ci, ci, ci, ctypes.POINTER(GemmPlanInfo)]
     lib.gemm_w4a16_ws.argtypes = [ci, vp, vp, ci, vp, ci, vp, i64, i64, i64, ci, ci, vp, sz, vp]
@@ -176,7 +179,7 @@ def load_library():
               "gemm_gated_backward_workspace_size",
               "gemm_backward", "gemm_backward_workspace_size", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle",
               "gemm_w4a16", "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "gemm_w4a16_ws", "gemm_gated_plan",
-              "gemm_w4a16_plan"):
+              "gemm_w4a16_plan", "gemm_backward_plan"):
         getattr(lib, f).restype = ci
     _lib = lib
     return lib
@@ -631,6 +634,16 @@ def gemm_gated_backward(dtype, dh, gate, up, x, w, act="silu", want_dx=True, wan
 def gemm_backward_workspace_size(dtype, M: int, N: int, K: int, want_da=True, want_db=True) -> int:
     """Host-only: workspace bytes of gemm_backward."""
     return _size("gemm_backward_workspace_size", _dt(dtype), M, N, K, int(want_da), int(want_db))
+
+
+def gemm_backward_plan(dtype, M: int, N: int, K: int, want_da=True, want_db=True, gated=False) -> tuple:
+    """Host-only: the kernels of the two products of gemm_backward (gated: of gemm_gated_backward, N is F
+    and K is H) for these sizes; None for an output that is not wanted."""
+    infos = GemmPlanInfo(), GemmPlanInfo()
+    _check(load_library().gemm_backward_plan(_dt(dtype), M, N, K, int(want_da), int(want_db), int(gated),
+                                             *(ctypes.byref(i) for i in infos)), "gemm_backward_plan")
+    return tuple({name: getattr(i, name) for name, _ in GemmPlanInfo._fields_} if want else None
+                 for i, want in zip(infos, (want_da, want_db)))
 
 
 def backward_workspace(dtype, M: int, N: int, K: int, want_da=True, want_db=True, device="cuda"):

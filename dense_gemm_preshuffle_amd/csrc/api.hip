@@ -1128,6 +1128,9 @@ int plan_gemm(int in_dtype, int64_t M, int64_t N, int64_t K, Plan* p) {
   return make_plan(in_dtype, M, N, K, nullptr, p, true);
 }
 int64_t plan_workspace(const Plan& p, int64_t M, int64_t N) { return workspace_bytes(p, M, N); }
+void report_plan(int in_dtype, int64_t M, int64_t N, int64_t K, const Plan& p, gemm_plan_info* out) {
+  fill_info(in_dtype, M, N, K, p, out);
+}
 int launch_gemm(int in_dtype, const Plan& p, const void* a, const void* b_shuf, void* c, int64_t M, int64_t N,
                 void* ws, hipStream_t s) {
   return launch(in_dtype, p, a, b_shuf, nullptr, nullptr, nullptr, GP_ACT_NONE, c, M, N, ws, s);

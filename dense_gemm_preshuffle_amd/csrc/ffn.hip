@@ -246,14 +246,14 @@ int make_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, bool want_da,
   // on 31 sizes against the tile that the model has for it alone (with the pair's
   // ranges) 24 took the same time within 2%, 4 up to 8% less, 3 more: da of 1500 x
   // 5984 x 800 40.5 us against 34.9, db of 1319 x 5280 x 704 21.1 against 19.1.
-  Plan copies;
+  Plan copies, copies_b;   // (one each: the planner sets what differs from a new Plan)
   double us_a = 0, us_b = 0;
   int r = plan_gemm(dtype, M, K, p->Np, &copies);
   p->da_rows = plan_rows(M, K, 2 * whole_k(p->Np), r ? nullptr : &copies, 4.0 * p->Np * K, &p->da, &us_a);
   if (!p->da_rows) p->da = copies;
-  r = plan_gemm(dtype, N, K, p->Mp, &copies);
-  p->db_rows = plan_rows(K, N, 2 * p->Mp, r ? nullptr : &copies, (gated ? 2.0 : 4.0) * p->Mp * N, &p->db, &us_b);
-  if (!p->db_rows) p->db = copies;
+  r = plan_gemm(dtype, N, K, p->Mp, &copies_b);
+  p->db_rows = plan_rows(K, N, 2 * p->Mp, r ? nullptr : &copies_b, (gated ? 2.0 : 4.0) * p->Mp * N, &p->db, &us_b);
+  if (!p->db_rows) p->db = copies_b;
   p->pair = p->da_rows && p->db_rows &&
             plan_pair(M, K, whole_k(p->Np) / 64, K, N, p->Mp / 64, us_a + us_b, &p->da, &p->db) && want_da && want_db;
   const int64_t part_a = want_da ? plan_workspace(p->da, M, K) : 0;
@@ -526,6 +526,35 @@ int gemm_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int
   const int r = plan_backward(dtype, M, N, K, want_da != 0, want_db != 0, false, &p);
   if (r) return r;
   *bytes = (size_t)p.bytes;
+  return GP_OK;
+}
+
+int gemm_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, int want_da, int want_db, int gated,
+                       gemm_plan_info* da, gemm_plan_info* db) {
+  if (!da || !db || (!want_da && !want_db)) return GP_EINVAL;
+  BackwardPlan p;
+  const int r = gated ? plan_gated_backward(dtype, M, N, K, want_da != 0, want_db != 0, &p)
+                      : plan_backward(dtype, M, N, K, want_da != 0, want_db != 0, false, &p);
+  if (r) return r;
+  *da = *db = gemm_plan_info();
+  auto fill = [&](const Plan& q, bool rows, int64_t m, int64_t n, int64_t k, gemm_plan_info* out) {
+    if (!rows) report_plan(dtype, m, n, k, q, out);
+    else {
+      out->kernel = p.pair ? GP_KERNEL_PAIR : GP_KERNEL_ROWS;
+      out->tile_m = q.tm;
+      out->tile_n = q.tn;
+      out->tile_k = 64;
+      out->waves = tile_waves(q.tm, q.tn);
+      out->threads = 64 * out->waves;
+      out->ksplit = q.ks;
+      out->grid = (m + q.tm - 1) / q.tm * ((n + q.tn - 1) / q.tn) * q.ks;
+      out->mfma = 16;
+    }
+    out->workspace_bytes = p.bytes;
+  };
+  const int64_t rows = gated ? 2 * N : N;
+  if (want_da) fill(p.da, p.da_rows, M, K, p.Np, da);
+  if (want_db) fill(p.db, p.db_rows, p.db_rows ? K : rows, p.db_rows ? rows : K, p.Mp, db);
   return GP_OK;
 }
 

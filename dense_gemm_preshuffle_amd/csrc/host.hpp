@@ -6,6 +6,7 @@
 
 #include <cstdint>
 
+#include "../../include/gemm_preshuffle.h"
 #include "gp_common.hpp"
 
 namespace gp {
@@ -44,6 +45,7 @@ constexpr int64_t kCounterBytes = kMaxSplitTiles * 4;
 // and the workspace bytes that plan needs (0: none).
 int plan_gemm(int in_dtype, int64_t M, int64_t N, int64_t K, Plan* p);
 int64_t plan_workspace(const Plan& p, int64_t M, int64_t N);
+void report_plan(int in_dtype, int64_t M, int64_t N, int64_t K, const Plan& p, gemm_plan_info* out);
 // Launch of a BF16 / FP16 plan, plain epilogue; pointers already validated.
 int launch_gemm(int in_dtype, const Plan& p, const void* a, const void* b_shuf, void* c, int64_t M, int64_t N,
                 void* ws, hipStream_t s);

@@ -99,8 +99,10 @@ enum {
   GP_KERNEL_SPLITK = 2,  /* small-M kernel: waves of a workgroup split K,
                             reduced through LDS (for the memory-bound small
                             batch of GEMM Opt. §1.3 / §8.3)                      */
-  GP_KERNEL_WIDE = 3     /* 256x256 tiles, 8 waves, A and B both through LDS
+  GP_KERNEL_WIDE = 3,    /* 256x256 tiles, 8 waves, A and B both through LDS
                             (INT8, FP8, BF16, FP16; M and N at least 256)        */
+  GP_KERNEL_ROWS = 4,    /* tile kernel on a row-major B (gemm_backward_plan only) */
+  GP_KERNEL_PAIR = 5     /* both products of a backward pass on it, in one launch */
 };
 
 /* Tuning options. Pass NULL, or a zero-filled struct, for all-automatic;
@@ -433,6 +435,17 @@ int gemm_backward(int dtype, const void* dc, const void* a, const void* b, void*
 
 /* Host-only: the workspace bytes of gemm_backward. */
 int gemm_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int want_da, int want_db, size_t* bytes);
+
+/*
+ * gemm_backward_plan -- host-only: the kernels of the two products of gemm_backward,
+ * or with gated = 1 of gemm_gated_backward (N is F, K is H). GP_KERNEL_ROWS and
+ * GP_KERNEL_PAIR: tile_m, tile_n, tile_k, waves, threads, grid, ksplit and mfma
+ * are set (db's tile is of its transpose, [K][N]); otherwise the plan of
+ * gemm_plan_ws on operands that the call lays out. workspace_bytes is the call's.
+ * An output that is not wanted: all 0.
+ */
+int gemm_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, int want_da, int want_db, int gated,
+                       gemm_plan_info* da, gemm_plan_info* db);
 
 /*
  * ---- Products with 4-bit weights and group scales (BF16 / FP16 activations) ----
