@@ -41,14 +41,14 @@ __global__ __launch_bounds__(256) void preshuffle_gated_kernel(const char* __res
 // tile with 1 to 16 ranges on one MI355X:
 //   row-major B: 40 shapes (M 32 to 5905, K 64 to 31744); the tile and ranges of
 //     least time by the model were the fastest or within 8% of it on 38 of them.
-//     M x N x K in us: 2000 x 4096 x 14336 150 on 256 x 256 in two ranges, 176 on
-//     128 x 128 in one; 161 x 2656 x 10624 25.9 on 64 x 128 in four (35.0 in three,
-//     40.9 in five), 28.8 on 128 x 128 in six; transposed 4096 x 14336 x 128 39.4
-//     on 128 x 128, 41.9 on 256 x 256.
+//     M x N x K in us (calls for one output, operands from HBM): 2000 x 4096 x 14336
+//     208 on 256 x 256 in two ranges, 247 on 128 x 128 in one; 161 x 2656 x 10624
+//     32.5 on 64 x 128 in four (37.0 in three, 42.3 in five), 33.3 on 128 x 128 in
+//     six; transposed 4096 x 14336 x 128 34.3 on 128 x 128, 42.4 on 256 x 256.
 //   gated: 27 shapes (M 70 to 8192, K 320 to 8192); within 8% on 26. 259 x 4384 x
-//     6592 36.9 on 128 x 256 in four ranges, 38.7 on 128 x 128 in two; 509 x 14336 x
-//     4096 57.6 on 128 x 256, 62.4 on 128 x 128, 65.2 on 256 x 256 in two; 1536 x
-//     1984 x 512 7.4 on 128 x 128, 9.9 on 128 x 256. The 256 x 256 tile's constants
+//     6592 38.9 on 128 x 256 in four ranges, 38.3 on 128 x 128 in two; 509 x 14336 x
+//     4096 59.0 on 128 x 256, 64.7 on 128 x 128; 1536 x 1984 x 512 7.6 on 128 x 128,
+//     10.3 on 128 x 256. The 256 x 256 tile's constants
 //     from 45 large ones (80 to 2100 GFLOP, M from 512) timed on the three largest
 //     tiles in turn, checked on 72 others: the choice is 0.7% above the best of the
 //     three on average there, 10% at worst. 557 x 15328 x 7488 158 on 256 x 256,
@@ -152,9 +152,9 @@ int plan_gated(int dtype, int64_t M, int64_t F, int64_t H, GatedPlan* p) {
 // from copies laid out for them: b^T for da, dc^T and a^T for db. The copies cost
 // bandwidth, the row-major products up to 14% of the matrix rate, so that the
 // copies pay off with many rows; which one, plan_rows estimates. Gated backward M
-// x F x H in us, row-major against copies: 130 x 2064 x 2048 30, 43; 512 x 4096 x
-// 4096 93, 121; 2000 x 7168 x 4096 440, 495; 4096 x 11008 x 4096 1260, 1225; 8192 x
-// 14336 x 4096 3118, 2999 (copies and the pointwise pass that also writes dc^T:
+// x F x H in us, row-major against copies: 130 x 2064 x 2048 22, 34; 512 x 4096 x
+// 4096 100, 112; 2000 x 7168 x 4096 452, 483; 4096 x 11008 x 4096 1322, 1245; 8192 x
+// 14336 x 4096 3229, 3039 (copies and the pointwise pass that also writes dc^T:
 // 458 of these; the matrix unit is busy 88% of the products' cycles at the 1.65
 // GHz that the power limit leaves).
 struct BackwardPlan {
@@ -201,9 +201,9 @@ bool plan_rows(int64_t M, int64_t N, int64_t Kb, const Plan* other, double copie
 //   3.5 + max(sum of (K tiles * 0.27 + 0.3) / 256, 1.4 * longest + 0.5) + joins (us)
 // taken where it is 5% below the two products' times (it also saves a launch). On
 // 25 shapes timed with every pair of ranges the choice was 3% above the best of
-// both on average, 17% at worst. Products of M x F x H on their best ranges, one
-// launch against two: 130 x 2064 x 2048 16.6, 22.4; 1116 x 672 x 480 9.5, 17.3; 57 x
-// 3392 x 2080 18.1, 23.2; 606 x 4896 x 448 28.9, 33.2; 682 x 5808 x 608 40.5, 39.7.
+// both on average, 17% at worst. Gated calls of M x F x H, one launch of the products
+// against two: 130 x 2064 x 2048 21.8, 27.7; 1116 x 672 x 480 17.7, 25.9; 57 x 3392 x
+// 2080 22.3, 27.2; 606 x 4896 x 448 33.5, 41.2; 682 x 5808 x 608 53.1, 57.0.
 bool plan_pair(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t Nb, int64_t Kb, double apart, Plan* a, Plan* b) {
   const int64_t ta = ((Ma + 63) / 64) * ((Na + 127) / 128), tb = ((Mb + 63) / 64) * ((Nb + 127) / 128);
   if (ta + tb > 2304) return false;   // 512 x 4096 x 4096 (4352 tiles) 89 us, apart on larger tiles 80
