@@ -48,15 +48,17 @@ __global__ __launch_bounds__(256) void preshuffle_gated_kernel(const char* __res
 //   gated: 27 shapes (M 70 to 8192, K 320 to 8192); within 8% on 26. 259 x 4384 x
 //     6592 38.9 on 128 x 256 in four ranges, 38.3 on 128 x 128 in two; 509 x 14336 x
 //     4096 59.0 on 128 x 256, 64.7 on 128 x 128; 1536 x 1984 x 512 7.6 on 128 x 128,
-//     10.3 on 128 x 256. The 256 x 256 tile's constants
-//     from 45 large ones (80 to 2100 GFLOP, M from 512) timed on the three largest
-//     tiles in turn, checked on 72 others: the choice is 0.7% above the best of the
-//     three on average there, 10% at worst. 557 x 15328 x 7488 158 on 256 x 256,
-//     180 on 128 x 256; 7292 x 21472 x 512 182, 149; 8192 x 28672 x 4096 1372, 1361.
+//     10.3 on 128 x 256. The 256 x 256 tile's constants from 156 large ones (80 to
+//     2100 GFLOP, M from 512, both types), every tile timed for 12 ms at a stretch,
+//     as a training step's products run: at the clock that the power limit leaves it,
+//     which is higher for the larger tile. The choice is 0.1% above the best of the
+//     three largest tiles on average there, 3.2% at worst, and 0.1% and 1.8% on 56
+//     others. 8192 x 28672 x 4096 1359 on 256 x 256, 1375 on 128 x 256, 1588 on 128 x
+//     128; 6385 x 12384 x 8000 973, 1040; 7292 x 21472 x 512 169, 148.
 struct TileTime { int tm, tn; double step, ends, join; };
 constexpr TileTime kRowsTimes[] = {{256, 256, 1.21, 9.5, 3.2}, {128, 256, 0.99, 5.6, 2.1}, {128, 128, 0.60, 1.65, 1.25},
                                    {64, 128, 0.32, 2.15, 0.7}};
-constexpr TileTime kGatedTimes[] = {{256, 256, 1.07, 14.4, 0}, {128, 256, 0.56, 6.0, 3.0}, {128, 128, 0.60, 1.25, 1.35},
+constexpr TileTime kGatedTimes[] = {{256, 256, 1.02, 15.4, 0}, {128, 256, 0.56, 6.0, 3.0}, {128, 128, 0.60, 1.25, 1.35},
                                     {64, 128, 0.35, 0.73, 1.0}};
 double tile_us(const TileTime& t, int64_t M, int64_t N, int64_t Kb, int64_t ks, double speed = 1.0) {
   const double fill = (double)(((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn) * ks) / 256;
