@@ -97,8 +97,11 @@ __device__ __forceinline__ void activate_grad(float g, float& value, float& slop
     value = activate_ffn<A>(g);
     slope = g <= 0.f ? 0.f : 1.f;
   } else if constexpr (A == ACT_SILU) {
-    float s, t;
-    sigmoid_pair(g, s, t);
+    // e = e^-|g| by way of 2^64 e, since the hardware exponential returns 0
+    // for results below 2^-126; s and 1 - s without cancellation on both sides
+    const float e = ldexpf(__builtin_amdgcn_exp2f(64.f - 1.44269504088896341f * fabsf(g)), -64);
+    const float r = __builtin_amdgcn_rcpf(1.f + e);
+    const float s = g >= 0.f ? r : e * r, t = g >= 0.f ? e * r : r;
     value = g * s;
     slope = s * (1.f + g * t);
   } else if constexpr (A == ACT_GELU) {
