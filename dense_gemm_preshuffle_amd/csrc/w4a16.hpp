@@ -266,20 +266,16 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
     if (ch < chunks) compute(P0{});
   }
 
-  uint32_t lost = 0;   // column blocks with a sum that is not finite
+  float probe = 0.f;   // 0 times every sum: NaN if one is not finite
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    bool l = false;
+  for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float t = acc[mb][nb][r];
-        red[((wave * NQ + mb * NB + nb) * R + r) * 64 + lane] = t;
-        l |= !(fabsf(t) <= kMaxFloat);
+        red[((wave * NQ + mb * NB + nb) * R + r) * 64 + lane] = acc[mb][nb][r];
+        probe = fmaf(acc[mb][nb][r], 0.f, probe);
       }
-    lost |= __any(l) ? 1u << nb : 0u;
-  }
   // Sums that are not finite, again with q - z as the operand: an infinity of x
   // or of a scale meets the weight that the formula has there, 0 included. In BF16
   // the operands carry 2^-16, which keeps the products of finite x finite (FP16's
@@ -288,9 +284,7 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(W4Args p) {
   // straight from memory, whatever the number of such sums: 64 x 8192 x 28672 in
   // BF16 76 us clean, 219 with a NaN in one row, 366 with nothing but NaN; one row
   // 23, 34, 77 (output by output each would take K dependent steps).
-  while (lost) {
-    const uint32_t blk = __builtin_ctz(lost);
-    lost &= lost - 1;
+  if (__builtin_expect(__any(!(probe == 0.f)), 0)) for (uint32_t blk = 0; blk < nreal; ++blk) {
     constexpr int kDown = DT == DT_BF16 ? 16 : 0;
     v4f sum[MB];
 #pragma unroll
