@@ -30,6 +30,10 @@ points have the names of the C ABI (include/gemm_preshuffle.h):
     gemm_w4a16(x, weights, bias, act)                -> act(x W^T + bias) (BF16 / FP16 activations)
     gemm_w4a16_gated(x, weights, act)                -> act(x Wg^T) * (x Wu^T) on 4-bit weights
     w4a16_workspace(M, weights)                      -> a device workspace of these (None: none needed)
+    gemm_norm(dtype, x, residual, norm_in, gate, norm_out)
+                                                     -> r = scale * residual + gate * norm_in(x), y = norm_out(r)
+    gemm_norm_backward(dtype, dy, dr, x, r, ...)     -> NormGrads
+    norm_backward_workspace                          -> a device workspace of it
     gemm_gated_plan, gemm_w4a16_plan                 -> dict, the kernel they run (host-only)
     gemm_backward_plan                               -> two of them, or None (host-only)
 
@@ -46,6 +50,7 @@ import ctypes
 import functools
 import os
 import re
+import typing
 
 __all__ = [
     "GemmError", "GemmLibraryMissing", "GemmOpts", "lib_path", "load_library",
@@ -55,7 +60,8 @@ __all__ = [
     "gemm_gated_backward_workspace_size", "gated_backward_workspace", "gemm_backward", "gemm_backward_workspace_size",
     "backward_workspace", "W4Weights", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle", "gemm_w4a16",
     "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "w4a16_workspace", "gemm_gated_plan", "gemm_w4a16_plan",
-    "gemm_backward_plan", "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE",
+    "gemm_backward_plan", "NORMS", "NormGrads", "gemm_norm", "gemm_norm_backward", "gemm_norm_backward_workspace_size",
+    "norm_backward_workspace", "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE",
     "KERNEL_SPLITK", "KERNEL_WIDE", "KERNEL_ROWS", "KERNEL_PAIR",
 ]
 
@@ -75,6 +81,8 @@ GP_EDTYPE = 3
 GP_EWORKSPACE = 6
 # gp_act values of the C ABI
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+# gp_norm values of the C ABI
+NORMS = {"none": 0, "rms": 1, "layer": 2}
 EPI_AUTO, EPI_DIRECT, EPI_CSHUFFLE = 0, 1, 2
 KERNEL_AUTO, KERNEL_TILE, KERNEL_SPLITK, KERNEL_WIDE, KERNEL_ROWS, KERNEL_PAIR = 0, 1, 2, 3, 4, 5
 
@@ -167,6 +175,11 @@ def load_library():
     lib.gemm_gated_plan.argtypes = [ci, i64, i64, i64, ctypes.POINTER(GemmPlanInfo)]
     lib.gemm_w4a16_plan.argtypes = [i64, i64, i64, ci, ci, ci, ctypes.POINTER(GemmPlanInfo)]
     lib.gemm_w4a16_ws.argtypes = [ci, vp, vp, ci, vp, ci, vp, i64, i64, i64, ci, ci, vp, sz, vp]
+    cf = ctypes.c_float
+    lib.gemm_norm.argtypes = [ci, vp, vp, cf, ci, vp, vp, vp, i64, ci, vp, vp, cf, vp, vp, i64, i64, vp]
+    lib.gemm_norm_backward.argtypes = [ci, vp, vp, vp, vp, cf, ci, vp, vp, vp, i64, ci, vp, cf, vp, vp, vp, vp, vp, vp,
+                                       vp, i64, i64, vp, sz, vp]
+    lib.gemm_norm_backward_workspace_size.argtypes = [ci, i64, i64, i64, psz]
     lib.gemm_status_string.argtypes = [ci]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_last_hip_error.argtypes = []
@@ -179,7 +192,8 @@ def load_library():
               "gemm_gated_backward_workspace_size",
               "gemm_backward", "gemm_backward_workspace_size", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle",
               "gemm_w4a16", "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "gemm_w4a16_ws", "gemm_gated_plan",
-              "gemm_w4a16_plan", "gemm_backward_plan"):
+              "gemm_w4a16_plan", "gemm_backward_plan", "gemm_norm", "gemm_norm_backward",
+              "gemm_norm_backward_workspace_size"):
         getattr(lib, f).restype = ci
     _lib = lib
     return lib
@@ -681,6 +695,133 @@ def gemm_backward(dtype, dc, a, b, want_da=True, want_db=True, da=None, db=None,
                                             _ptr(workspace), _workspace_bytes("gemm_backward", workspace, dev),
                                             _stream(stream)), "gemm_backward")
     return da, db
+
+
+def _device() -> int:
+    from torch import _C
+
+    return _C._cuda_getDevice()
+
+
+def _here(where, name, t, stream):
+    """A call's first tensor is on the current device, where its kernels are launched, and so is its stream."""
+    if not t.is_cuda:
+        raise ValueError(f"{where}: {name} is not a device tensor")
+    if t.device.index != _device():
+        raise ValueError(f"{where}: {name} is on {t.device}, the current device is cuda:{_device()}")
+    if stream is not None and not isinstance(stream, int) and stream.device != t.device:
+        raise ValueError(f"{where}: {name} is on {t.device}, the stream on {stream.device}")
+
+
+# ---- norms around a block, with its gate and the residual ----
+
+class NormGrads(typing.NamedTuple):
+    """Outputs of gemm_norm_backward; None where there is none or it is not wanted."""
+    dx: object = None
+    dresidual: object = None
+    dw_in: object = None
+    db_in: object = None
+    dgate: object = None
+    dw_out: object = None
+    db_out: object = None
+
+
+def _norm(kind) -> int:
+    return NORMS[kind] if isinstance(kind, str) else int(kind)
+
+
+def _norm_args(where, t, M, H, dev, rows, vectors, gate):
+    """Checks of the [M, H] tensors, the fp32 vectors over the columns and the gate; the gate's rows."""
+    import torch
+
+    for name, v in rows:
+        if v is not None and not _fits(v, (M, H), t, dev):
+            _want(f"{where}: {name}", v, (M, H), t, dev)
+    for name, v in vectors:
+        if v is not None and not _fits(v, (H,), torch.float32, dev):
+            _want(f"{where}: {name}", v, (H,), torch.float32, dev)
+    if gate is None:
+        return 0
+    if not _fits(gate, (gate.shape[0], H), torch.float32, dev):
+        _want(f"{where}: gate", gate, (gate.shape[0], H), torch.float32, dev)
+    return gate.shape[0]
+
+
+def gemm_norm(dtype, x, residual=None, scale=1.0, norm_in="none", w_in=None, b_in=None, gate=None, norm_out="rms",
+              w_out=None, b_out=None, eps=1e-6, want_r=True, r=None, y=None, stream=None):
+    """(r, y): r = scale * residual + gate * (norm_in(x) * w_in + b_in), y = norm_out(r) * w_out + b_out in one
+    pass. x, residual [M, H]; norm_in, norm_out "none", "rms" or "layer"; w_*, b_* fp32 [H] or None (ones, zeros);
+    gate fp32 [G, H], a row for each M / G rows of x, or None. y is None with norm_out "none"; with want_r=False r
+    is not stored and None. r may be the residual or x, y may be x."""
+    where = "gemm_norm"
+    dt, t = _half(dtype)
+    M, H = x.shape
+    dev = x.device
+    _here(where, "x", x, stream)
+    kin, kout = _norm(norm_in), _norm(norm_out)
+    if (r is not None and not want_r) or (y is not None and not kout):
+        raise ValueError(f"{where}: an output is given that is not computed")
+    gates = _norm_args(where, t, M, H, dev, (("x", x), ("residual", residual), ("r", r), ("y", y)),
+                       (("w_in", w_in), ("b_in", b_in), ("w_out", w_out), ("b_out", b_out)), gate)
+    with _on(stream, dev):
+        if want_r and r is None:
+            r = x.new_empty((M, H))
+        if kout and y is None:
+            y = x.new_empty((M, H))
+    _check(load_library().gemm_norm(dt, x.data_ptr(), _ptr(residual), scale, kin, _ptr(w_in), _ptr(b_in), _ptr(gate),
+                                    gates, kout, _ptr(w_out), _ptr(b_out), eps, _ptr(r), _ptr(y), M, H,
+                                    _stream(stream)), where)
+    return r, y
+
+
+def gemm_norm_backward_workspace_size(dtype, M: int, H: int, gates: int = 0) -> int:
+    """Host-only: workspace bytes of gemm_norm_backward (gates: rows of the gate, 0 without one)."""
+    return _size("gemm_norm_backward_workspace_size", _dt(dtype), M, H, gates)
+
+
+def norm_backward_workspace(dtype, M: int, H: int, gates: int = 0, device="cuda"):
+    """A device workspace for gemm_norm_backward (its contents need not be set)."""
+    import torch
+
+    return torch.empty(gemm_norm_backward_workspace_size(dtype, M, H, gates), dtype=torch.uint8, device=device)
+
+
+def gemm_norm_backward(dtype, dy, dr, x, r, scale=1.0, norm_in="none", w_in=None, b_in=None, gate=None,
+                       norm_out="rms", w_out=None, b_out=None, eps=1e-6, want_dx=True, want_dresidual=True,
+                       want_params=True, dx=None, dresidual=None, workspace=None, stream=None) -> NormGrads:
+    """Gradients of gemm_norm, called with the same arguments: dy is that of y (None with norm_out "none"), dr what
+    reaches r by other ways (None: nothing), r as gemm_norm returned it (None with norm_out "none"). x may be None
+    where neither the gate's gradient nor one through norm_in needs it. With want_params the gradients of the
+    parameters that are given are computed, in fp32."""
+    import torch
+
+    where = "gemm_norm_backward"
+    dt, t = _half(dtype)
+    lead = dy if dy is not None else dr
+    if lead is None:
+        raise ValueError(f"{where}: neither dy nor dr is given")
+    _here(where, "dr" if dy is None else "dy", lead, stream)
+    M, H = lead.shape
+    dev = lead.device
+    if (dx is not None and not want_dx) or (dresidual is not None and not want_dresidual):
+        raise ValueError(f"{where}: an output is given that is not computed")
+    gates = _norm_args(where, t, M, H, dev, (("dy", dy), ("dr", dr), ("x", x), ("r", r), ("dx", dx),
+                                             ("dresidual", dresidual)),
+                       (("w_in", w_in), ("b_in", b_in), ("w_out", w_out), ("b_out", b_out)), gate)
+    with _on(stream, dev):
+        if want_dx and dx is None:
+            dx = lead.new_empty((M, H))
+        if want_dresidual and dresidual is None:
+            dresidual = lead.new_empty((M, H))
+        grads = [torch.empty_like(v) if v is not None and want_params else None for v in (w_in, b_in, gate, w_out, b_out)]
+        if workspace is None and any(g is not None for g in grads):
+            workspace = norm_backward_workspace(dt, M, H, gates, dev)
+        _check(load_library().gemm_norm_backward(dt, _ptr(dy), _ptr(dr), _ptr(x), _ptr(r), scale, _norm(norm_in),
+                                                 _ptr(w_in), _ptr(b_in), _ptr(gate), gates, _norm(norm_out),
+                                                 _ptr(w_out), eps, _ptr(dx), _ptr(dresidual), *map(_ptr, grads), M, H,
+                                                 _ptr(workspace), _workspace_bytes(where, workspace, dev),
+                                                 _stream(stream)), where)
+    return NormGrads(dx, dresidual, *grads)
 
 
 # ---- 4-bit weights with group scales ----

@@ -87,6 +87,14 @@ typedef enum gp_act {
   GP_ACT_GELU = 3
 } gp_act;
 
+/* Norms of gemm_norm, over a row v of H values:
+ *   rms: v / sqrt(mean(v^2) + eps)   layer: (v - mean) / sqrt(mean((v - mean)^2) + eps) */
+typedef enum gp_norm {
+  GP_NORM_NONE = 0,
+  GP_NORM_RMS = 1,
+  GP_NORM_LAYER = 2
+} gp_norm;
+
 enum {
   GP_EPI_AUTO = 0,      /* planner's choice                                   */
   GP_EPI_DIRECT = 1,    /* each lane stores its accumulators (GEMM Opt. §7.1) */
@@ -505,6 +513,64 @@ int gemm_w4a16_workspace_size(int64_t M, int64_t N, int64_t K, int group, int ga
 /* gemm_w4a16_plan -- host-only: the kernel variant of a 4-bit product, as
  * gemm_gated_plan gives it (GP_KERNEL_SPLITK); with_workspace: of gemm_w4a16_ws. */
 int gemm_w4a16_plan(int64_t M, int64_t N, int64_t K, int group, int gated, int with_workspace, gemm_plan_info* out);
+
+/*
+ * ---- Norms around a block, with its gate and the residual (BF16, FP16) ----
+ *
+ *   u = norm_in(x) * w_in + b_in        (norm_in none: u = x)
+ *   r = scale * residual + gate * u     (the residual stream after the block)
+ *   y = norm_out(r) * w_out + b_out     (the next block's input)
+ *
+ * in one pass: x, the block's output, residual, r and y are [M][H] of one type;
+ * the norms' parameters and the gate are fp32, as a bias is. H % 8 == 0 and H <=
+ * 16384; M is below 2^31, the matrices of any size. All arithmetic is fp32; r and
+ * y are rounded once each, y from the r before its rounding. Infinities and NaN
+ * stay in their own rows.
+ *
+ * gemm_norm
+ *   residual   device [M][H], or NULL (r = gate * u).
+ *   norm_in, norm_out   GP_NORM_*.
+ *   w_*, b_*   device fp32 [H], or NULL (ones, zeros); NULL without that norm.
+ *   gate       device fp32 [gates][H], row m taking row m / (M / gates): 1 a learned
+ *              scale per channel, the batch a row per sequence; NULL with gates = 0:
+ *              no gate. gates divides M and is at most 256 (else GP_ESHAPE).
+ *   eps        at least 0.
+ *   r, y       outputs. y is given exactly if norm_out is a norm; r may then be NULL
+ *              (not stored). r may be the residual or x, y may be x: each element is
+ *              read before it is written; no other overlap.
+ * All device pointers 16-byte aligned (GP_EINVAL).
+ */
+int gemm_norm(int dtype, const void* x, const void* residual, float scale, int norm_in, const float* w_in,
+              const float* b_in, const float* gate, int64_t gates, int norm_out, const float* w_out,
+              const float* b_out, float eps, void* r, void* y, int64_t M, int64_t H, void* stream);
+
+/*
+ * gemm_norm_backward -- gradients of gemm_norm from dy = dL/dy and dr, the gradient
+ * that reaches r by other ways (the residual stream's; NULL: none). With n =
+ * norm_out(r), n1 = norm_in(x) or x, R the reciprocal root of each:
+ *   t = dr + R (d - n mean(d n) [- mean(d): layer]),   d = dy * w_out
+ *   dresidual = scale * t
+ *   dx = R1 (e - n1 mean(e n1) [- mean(e): layer]),    e = gate * t * w_in
+ *   dgate = sum of t * u over the rows of each gate row,
+ *   dw_in = sum of gate * t * n1, db_in = sum of gate * t,
+ *   dw_out = sum of dy * n, db_out = sum of dy          over all rows
+ *   r            as gemm_norm stored it (needed with norm_out); the norm's statistics
+ *                are taken again from it. dy is given exactly if norm_out is a norm.
+ *   x            needed for dgate, and for dx and dw_in where norm_in is a norm.
+ *   dx, dresidual   of the type; dw_*, db_* fp32 [H], dgate fp32 [gates][H]. Each
+ *                may be NULL (not computed), not all; no overlaps.
+ *   workspace    16-byte aligned, gemm_norm_backward_workspace_size bytes, contents not
+ *                set; needed for the fp32 outputs (else it may be NULL).
+ * Row sums are fp32, in a fixed order: the same call gives the same bits.
+ */
+int gemm_norm_backward(int dtype, const void* dy, const void* dr, const void* x, const void* r, float scale,
+                       int norm_in, const float* w_in, const float* b_in, const float* gate, int64_t gates,
+                       int norm_out, const float* w_out, float eps, void* dx, void* dresidual, float* dw_in,
+                       float* db_in, float* dgate, float* dw_out, float* db_out, int64_t M, int64_t H,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Host-only: the workspace bytes of gemm_norm_backward. */
+int gemm_norm_backward_workspace_size(int dtype, int64_t M, int64_t H, int64_t gates, size_t* bytes);
 
 /* Static, human-readable description of a gp_status value. */
 const char* gemm_status_string(int status);
