@@ -24,7 +24,11 @@ points have the names of the C ABI (include/gemm_preshuffle.h):
     gemm_gated(dtype, x, w_shuf, act, save)          -> h = act(x Wg^T) * (x Wu^T) (and gate, up to keep)
     gemm_gated_backward(dtype, dh, gate, up, x, w)   -> dx, dw
     gemm_backward(dtype, dc, a, b)                   -> da, db of C = A B^T
-    gated_workspace, gated_backward_workspace, backward_workspace
+    gemm_linear_preshuffle(w, dtype)                 -> weights [N, K] laid out for gemm_linear
+    gemm_linear(dtype, x, w_shuf, bias, act, residual, save)
+                                                     -> y = act(x W^T + bias) + residual (and z to keep)
+    gemm_linear_backward(dtype, dy, z, x, w, act)    -> dx, dw, dbias
+    gated_workspace, gated_backward_workspace, backward_workspace, linear_workspace, linear_backward_workspace
                                                      -> device workspaces of these
     gemm_w4a16_preshuffle(q, scales, zeros, group)   -> W4Weights, 4-bit weights laid out with their scales
     gemm_w4a16(x, weights, bias, act)                -> act(x W^T + bias) (BF16 / FP16 activations)
@@ -34,7 +38,13 @@ points have the names of the C ABI (include/gemm_preshuffle.h):
                                                      -> r = scale * residual + gate * norm_in(x), y = norm_out(r)
     gemm_norm_backward(dtype, dy, dr, x, r, ...)     -> NormGrads
     norm_backward_workspace                          -> a device workspace of it
-    gemm_gated_plan, gemm_w4a16_plan                 -> dict, the kernel they run (host-only)
+    gemm_moe_preshuffle(w13, w2, dtype)              -> MoeWeights, the experts' weights laid out
+    gemm_moe(dtype, x, router, weights, k, ...)      -> y, ids, gates of a mixture-of-experts layer (a few tokens)
+    gemm_moe_route(dtype, x, router, k, ...)         -> ids, gates (the router alone)
+    gemm_moe_experts(dtype, x, weights, ids, gates)  -> y (the experts alone)
+    moe_workspace(M, k, weights)                     -> a device workspace of these
+    gemm_gated_plan, gemm_linear_plan, gemm_w4a16_plan
+                                                     -> dict, the kernel they run (host-only)
     gemm_backward_plan                               -> two of them, or None (host-only)
 
 Tensors: A is [M, K] (INT8 / FP8 as any 1-byte dtype, BF16 / FP16 as
@@ -60,8 +70,10 @@ __all__ = [
     "gemm_gated_backward_workspace_size", "gated_backward_workspace", "gemm_backward", "gemm_backward_workspace_size",
     "backward_workspace", "W4Weights", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle", "gemm_w4a16",
     "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "w4a16_workspace", "gemm_gated_plan", "gemm_w4a16_plan",
-    "gemm_backward_plan", "NORMS", "NormGrads", "gemm_norm", "gemm_norm_backward", "gemm_norm_backward_workspace_size",
-    "norm_backward_workspace", "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE",
+    "gemm_backward_plan", "gemm_linear_preshuffle", "gemm_linear", "gemm_linear_workspace_size", "gemm_linear_plan",
+    "linear_workspace", "gemm_linear_backward", "gemm_linear_backward_workspace_size", "linear_backward_workspace", "NORMS", "NormGrads", "gemm_norm", "gemm_norm_backward", "gemm_norm_backward_workspace_size",
+    "norm_backward_workspace", "SCORES", "MoeWeights", "gemm_moe_weights_size", "gemm_moe_preshuffle", "gemm_moe_route",
+    "gemm_moe_experts", "gemm_moe", "gemm_moe_workspace_size", "moe_workspace", "gemm_status_string", "source_hash", "DTYPES", "EPI_DIRECT", "EPI_CSHUFFLE", "KERNEL_TILE",
     "KERNEL_SPLITK", "KERNEL_WIDE", "KERNEL_ROWS", "KERNEL_PAIR",
 ]
 
@@ -83,6 +95,8 @@ GP_EWORKSPACE = 6
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 # gp_norm values of the C ABI
 NORMS = {"none": 0, "rms": 1, "layer": 2}
+# gp_score values of the C ABI
+SCORES = {"softmax": 0, "sigmoid": 1}
 EPI_AUTO, EPI_DIRECT, EPI_CSHUFFLE = 0, 1, 2
 KERNEL_AUTO, KERNEL_TILE, KERNEL_SPLITK, KERNEL_WIDE, KERNEL_ROWS, KERNEL_PAIR = 0, 1, 2, 3, 4, 5
 
@@ -175,11 +189,23 @@ def load_library():
     lib.gemm_gated_plan.argtypes = [ci, i64, i64, i64, ctypes.POINTER(GemmPlanInfo)]
     lib.gemm_w4a16_plan.argtypes = [i64, i64, i64, ci, ci, ci, ctypes.POINTER(GemmPlanInfo)]
     lib.gemm_w4a16_ws.argtypes = [ci, vp, vp, ci, vp, ci, vp, i64, i64, i64, ci, ci, vp, sz, vp]
+    lib.gemm_linear_preshuffle.argtypes = [vp, vp, i64, i64, ci, vp]
+    lib.gemm_linear.argtypes = [ci, vp, vp, vp, ci, vp, vp, vp, i64, i64, i64, vp, sz, vp]
+    lib.gemm_linear_workspace_size.argtypes = [ci, i64, i64, i64, psz]
+    lib.gemm_linear_plan.argtypes = [ci, i64, i64, i64, ctypes.POINTER(GemmPlanInfo)]
+    lib.gemm_linear_backward.argtypes = [ci, vp, vp, vp, vp, ci, vp, vp, vp, i64, i64, i64, vp, sz, vp]
+    lib.gemm_linear_backward_workspace_size.argtypes = [ci, i64, i64, i64, ci, ci, ci, ci, psz]
     cf = ctypes.c_float
     lib.gemm_norm.argtypes = [ci, vp, vp, cf, ci, vp, vp, vp, i64, ci, vp, vp, cf, vp, vp, i64, i64, vp]
     lib.gemm_norm_backward.argtypes = [ci, vp, vp, vp, vp, cf, ci, vp, vp, vp, i64, ci, vp, cf, vp, vp, vp, vp, vp, vp,
                                        vp, i64, i64, vp, sz, vp]
     lib.gemm_norm_backward_workspace_size.argtypes = [ci, i64, i64, i64, psz]
+    lib.gemm_moe_weights_size.argtypes = [i64, i64, i64, psz]
+    lib.gemm_moe_preshuffle.argtypes = [ci, vp, vp, vp, i64, i64, i64, vp]
+    lib.gemm_moe_workspace_size.argtypes = [ci, i64, i64, i64, i64, i64, psz]
+    lib.gemm_moe_route.argtypes = [ci, vp, vp, vp, ci, ci, cf, vp, vp, i64, i64, i64, i64, vp, sz, vp]
+    lib.gemm_moe_experts.argtypes = [ci, vp, vp, vp, vp, ci, vp, vp, i64, i64, i64, i64, i64, vp, sz, vp]
+    lib.gemm_moe.argtypes = [ci, vp, vp, vp, ci, ci, cf, vp, ci, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, sz, vp]
     lib.gemm_status_string.argtypes = [ci]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_last_hip_error.argtypes = []
@@ -192,8 +218,11 @@ def load_library():
               "gemm_gated_backward_workspace_size",
               "gemm_backward", "gemm_backward_workspace_size", "gemm_w4a16_weights_size", "gemm_w4a16_preshuffle",
               "gemm_w4a16", "gemm_w4a16_gated", "gemm_w4a16_workspace_size", "gemm_w4a16_ws", "gemm_gated_plan",
-              "gemm_w4a16_plan", "gemm_backward_plan", "gemm_norm", "gemm_norm_backward",
-              "gemm_norm_backward_workspace_size"):
+              "gemm_w4a16_plan", "gemm_backward_plan", "gemm_linear_preshuffle", "gemm_linear",
+              "gemm_linear_workspace_size", "gemm_linear_plan", "gemm_linear_backward",
+              "gemm_linear_backward_workspace_size", "gemm_norm", "gemm_norm_backward",
+              "gemm_norm_backward_workspace_size", "gemm_moe_weights_size", "gemm_moe_preshuffle",
+              "gemm_moe_workspace_size", "gemm_moe_route", "gemm_moe_experts", "gemm_moe"):
         getattr(lib, f).restype = ci
     _lib = lib
     return lib
@@ -697,6 +726,13 @@ def gemm_backward(dtype, dc, a, b, want_da=True, want_db=True, da=None, db=None,
     return da, db
 
 
+@functools.lru_cache(maxsize=None)
+def _uint8():
+    import torch
+
+    return torch.uint8
+
+
 def _device() -> int:
     from torch import _C
 
@@ -711,6 +747,132 @@ def _here(where, name, t, stream):
         raise ValueError(f"{where}: {name} is on {t.device}, the current device is cuda:{_device()}")
     if stream is not None and not isinstance(stream, int) and stream.device != t.device:
         raise ValueError(f"{where}: {name} is on {t.device}, the stream on {stream.device}")
+
+
+# ---- linear layer with its epilogue ----
+
+def gemm_linear_preshuffle(w, dtype, out=None, stream=None):
+    """w [N, K] -> layout of gemm_linear (uint8, flat)."""
+    import torch
+
+    dt, t = _half(dtype)
+    _here("gemm_linear_preshuffle", "w", w, stream)
+    N, K = w.shape
+    _want("gemm_linear_preshuffle: w", w, (N, K), t)
+    n = 2 * N * (-(-K // 64) * 64)    # K is filled up to whole 128-byte tiles
+    with _on(stream, w.device):
+        out = torch.empty(n, dtype=torch.uint8, device=w.device) if out is None else out
+        _want("gemm_linear_preshuffle: out", out, (n,), torch.uint8, w.device)
+        _check(load_library().gemm_linear_preshuffle(_ptr(w), _ptr(out), N, K, dt, _stream(stream)),
+               "gemm_linear_preshuffle")
+    return out
+
+
+def gemm_linear_workspace_size(dtype, M: int, N: int, K: int) -> int:
+    """Host-only: workspace bytes of gemm_linear for these sizes (0: none)."""
+    return _size("gemm_linear_workspace_size", _dt(dtype), M, N, K)
+
+
+def gemm_linear_plan(dtype, M: int, N: int, K: int) -> dict:
+    """Host-only: the kernel that gemm_linear runs for these sizes."""
+    info = GemmPlanInfo()
+    _check(load_library().gemm_linear_plan(_dt(dtype), M, N, K, ctypes.byref(info)), "gemm_linear_plan")
+    return {name: getattr(info, name) for name, _ in GemmPlanInfo._fields_}
+
+
+def linear_workspace(dtype, M: int, N: int, K: int, device="cuda"):
+    """A device workspace for gemm_linear, its counters zero (None when none is needed). Zero once here;
+    every call leaves its counters zero again. Calls that may overlap need one each."""
+    return _split_workspace(gemm_linear_workspace_size(dtype, M, N, K), device)
+
+
+def gemm_linear(dtype, x, w_shuf, bias=None, act="none", residual=None, save=False, y=None, z=None, workspace=None,
+                stream=None):
+    """y = act(x W^T + bias) + residual: x [M, K], w_shuf from gemm_linear_preshuffle, bias fp32 [N], residual
+    [M, N], either of them None. Returns y, or (y, z) with save=True, z = x W^T + bias in x's type. y may be the
+    residual. Without a workspace one is made for the call where the plan needs it."""
+    dt, t = _half(dtype)
+    where = "gemm_linear"
+    _here(where, "x", x, stream)
+    M, K = x.shape
+    device = x.device
+    Kp = -(-K // 64) * 64
+    N = _nbytes(w_shuf) // (2 * Kp) if K else 0
+    _want("gemm_linear: x", x, (M, K), t)
+    _want("gemm_linear: w_shuf", w_shuf, (2 * N * Kp,), _uint8(), device)
+    if not save and z is not None:
+        raise ValueError("gemm_linear: z is written with save=True")
+    for name, v in (("residual", residual), ("y", y), ("z", z)):
+        if v is not None and not _fits(v, (M, N), t, device):
+            _want(f"gemm_linear: {name}", v, (M, N), t, device)
+    if bias is not None:
+        import torch
+
+        _want("gemm_linear: bias", bias, (N,), torch.float32, device)
+    with _on(stream, device):
+        y = x.new_empty((M, N)) if y is None else y
+        if save and z is None:
+            z = x.new_empty((M, N))
+        if workspace is None:
+            workspace = linear_workspace(dt, M, N, K, device)
+    _check(load_library().gemm_linear(dt, x.data_ptr(), w_shuf.data_ptr(), _ptr(bias), _act(act), _ptr(residual),
+                                      y.data_ptr(), _ptr(z), M, N, K, _ptr(workspace),
+                                      _workspace_bytes(where, workspace, device), _stream(stream)), where)
+    return (y, z) if save else y
+
+
+def gemm_linear_backward_workspace_size(dtype, M: int, N: int, K: int, act="silu", want_dx=True, want_dw=True,
+                                        want_dbias=True) -> int:
+    """Host-only: workspace bytes of gemm_linear_backward (any activation's serve act="none" too)."""
+    return _size("gemm_linear_backward_workspace_size", _dt(dtype), M, N, K, _act(act), int(want_dx), int(want_dw),
+                 int(want_dbias))
+
+
+def linear_backward_workspace(dtype, M: int, N: int, K: int, act="silu", want_dx=True, want_dw=True, want_dbias=True,
+                              device="cuda"):
+    """A device workspace for gemm_linear_backward (its contents need not be set)."""
+    import torch
+
+    return torch.empty(gemm_linear_backward_workspace_size(dtype, M, N, K, act, want_dx, want_dw, want_dbias),
+                       dtype=torch.uint8, device=device)
+
+
+def gemm_linear_backward(dtype, dy, z, x, w, act="none", want_dx=True, want_dw=True, want_dbias=True, dx=None, dw=None,
+                         dbias=None, workspace=None, stream=None):
+    """(dx [M, K], dw [N, K], dbias fp32 [N]) of gemm_linear from dy and the kept z ([M, N]; None without an
+    activation); w [N, K] row-major. An output that is not wanted is None, and the operand that it alone needs (w
+    for dx, x for dw) may be None. The residual's gradient is dy itself."""
+    import torch
+
+    where = "gemm_linear_backward"
+    dt, t = _half(dtype)
+    _here(where, "dy", dy, stream)
+    M, N = dy.shape
+    dev = dy.device
+    if not (want_dx or want_dw or want_dbias):
+        raise ValueError(f"{where}: no output wanted")
+    if (want_dx and w is None) or (want_dw and x is None) or (_act(act) and z is None):
+        raise ValueError(f"{where}: dx needs w, dw needs x, an activation needs z")
+    if (dx is not None and not want_dx) or (dw is not None and not want_dw) or (dbias is not None and not want_dbias):
+        raise ValueError(f"{where}: an output is given that is not wanted")
+    K = w.shape[1] if w is not None else x.shape[1] if x is not None else 32    # (dbias alone: of no consequence)
+    for name, v, shape in (("dy", dy, (M, N)), ("z", z, (M, N)), ("x", x, (M, K)), ("w", w, (N, K)), ("dx", dx, (M, K)),
+                           ("dw", dw, (N, K))):
+        if v is not None and not _fits(v, shape, t, dev):
+            _want(f"{where}: {name}", v, shape, t, dev)
+    if dbias is not None:
+        _want(f"{where}: dbias", dbias, (N,), torch.float32, dev)
+    with _on(stream, dev):
+        dx = (dy.new_empty((M, K)) if dx is None else dx) if want_dx else None
+        dw = (dy.new_empty((N, K)) if dw is None else dw) if want_dw else None
+        if want_dbias and dbias is None:
+            dbias = dy.new_empty((N,), dtype=torch.float32)
+        if workspace is None:
+            workspace = linear_backward_workspace(dt, M, N, K, act, want_dx, want_dw, want_dbias, dev)
+        _check(load_library().gemm_linear_backward(dt, _ptr(dy), _ptr(z), _ptr(x), _ptr(w), _act(act), _ptr(dx), _ptr(dw),
+                                                   _ptr(dbias), M, N, K, _ptr(workspace),
+                                                   _workspace_bytes(where, workspace, dev), _stream(stream)), where)
+    return dx, dw, dbias
 
 
 # ---- norms around a block, with its gate and the residual ----
@@ -822,6 +984,145 @@ def gemm_norm_backward(dtype, dy, dr, x, r, scale=1.0, norm_in="none", w_in=None
                                                  _ptr(workspace), _workspace_bytes(where, workspace, dev),
                                                  _stream(stream)), where)
     return NormGrads(dx, dresidual, *grads)
+
+
+# ---- mixture-of-experts layer for a few tokens ----
+
+class MoeWeights:
+    """Laid-out experts' weights (gemm_moe_preshuffle): the device buffer and what it holds."""
+
+    __slots__ = ("data", "dtype", "E", "F", "H", "device", "gp_dtype")
+
+    def __init__(self, data, dtype, gp_dtype, E, F, H):
+        self.data, self.dtype, self.gp_dtype = data, dtype, gp_dtype
+        self.E, self.F, self.H, self.device = E, F, H, data.device
+
+
+def gemm_moe_weights_size(E: int, F: int, H: int) -> int:
+    """Host-only: bytes of the laid-out weights of E experts."""
+    return _size("gemm_moe_weights_size", E, F, H)
+
+
+def gemm_moe_preshuffle(w13, w2, dtype, out=None, stream=None) -> MoeWeights:
+    """w13 [E, 2F, H] (an expert's F gate rows, then its F up rows) and w2 [E, H, F] -> MoeWeights."""
+    import torch
+
+    where = "gemm_moe_preshuffle"
+    dt, t = _half(dtype)
+    _here(where, "w13", w13, stream)
+    E, F2, H = w13.shape
+    F = F2 // 2
+    _want(f"{where}: w13", w13, (E, 2 * F, H), t)
+    _want(f"{where}: w2", w2, (E, H, F), t, w13.device)
+    n = gemm_moe_weights_size(E, F, H)
+    with _on(stream, w13.device):
+        out = torch.empty(n, dtype=torch.uint8, device=w13.device) if out is None else out
+        _want(f"{where}: out", out, (n,), torch.uint8, w13.device)
+        _check(load_library().gemm_moe_preshuffle(dt, _ptr(w13), _ptr(w2), _ptr(out), E, F, H, _stream(stream)), where)
+    return MoeWeights(out, t, dt, E, F, H)
+
+
+def gemm_moe_workspace_size(dtype, M: int, F: int, H: int, E: int, k: int) -> int:
+    """Host-only: workspace bytes of gemm_moe, gemm_moe_route (any F) and gemm_moe_experts."""
+    return _size("gemm_moe_workspace_size", _dt(dtype), M, F, H, E, k)
+
+
+def moe_workspace(M: int, k: int, weights: MoeWeights):
+    """A device workspace for M tokens with k experts each on these weights, its counters zero. Zero once here;
+    every call leaves its counters zero again. Calls that may overlap need one each."""
+    return _split_workspace(gemm_moe_workspace_size(weights.gp_dtype, M, weights.F, weights.H, weights.E, k), weights.device)
+
+
+def _moe_route_args(where, t, x, router, bias, M, H, E, k, ids, gates):
+    """Checks of a router's arguments; ids and gates, made where they are not given."""
+    import torch
+
+    dev = x.device
+    _want(f"{where}: x", x, (M, H), t, dev)
+    _want(f"{where}: router", router, (E, H), t, dev)
+    if bias is not None:
+        _want(f"{where}: bias", bias, (E,), torch.float32, dev)
+    ids = torch.empty(M, k, dtype=torch.int32, device=dev) if ids is None else ids
+    gates = torch.empty(M, k, dtype=torch.float32, device=dev) if gates is None else gates
+    _want(f"{where}: ids", ids, (M, k), torch.int32, dev)
+    _want(f"{where}: gates", gates, (M, k), torch.float32, dev)
+    return ids, gates
+
+
+def _score(score) -> int:
+    return SCORES[score] if isinstance(score, str) else int(score)
+
+
+def gemm_moe_route(dtype, x, router, k: int, bias=None, score="softmax", normalize=True, scale=1.0, ids=None, gates=None,
+                   workspace=None, stream=None):
+    """(ids int32 [M, k], gates fp32 [M, k]): the k experts of largest score (+ bias fp32 [E]) of x's rows, by falling
+    score, and their weights. x [M, H], router [E, H]; score "softmax" or "sigmoid"; normalize: the weights of a token
+    add up to scale. Without a workspace (gemm_moe_workspace_size) one is made for the call."""
+    where = "gemm_moe_route"
+    dt, t = _half(dtype)
+    _here(where, "x", x, stream)
+    (M, H), E = x.shape, router.shape[0]
+    with _on(stream, x.device):
+        ids, gates = _moe_route_args(where, t, x, router, bias, M, H, E, k, ids, gates)
+        if workspace is None:
+            workspace = _split_workspace(gemm_moe_workspace_size(dt, M, 16, H, E, k), x.device)
+        _check(load_library().gemm_moe_route(dt, _ptr(x), _ptr(router), _ptr(bias), _score(score), int(normalize), scale,
+                                             _ptr(ids), _ptr(gates), M, H, E, k, _ptr(workspace),
+                                             _workspace_bytes(where, workspace, x.device), _stream(stream)), where)
+    return ids, gates
+
+
+def _moe_experts_args(where, t, x, weights, residual, y, M):
+    if weights.dtype is not t:
+        raise ValueError(f"{where}: the weights are {weights.dtype}")
+    for name, v in (("x", x), ("residual", residual), ("y", y)):
+        if v is not None:
+            _want(f"{where}: {name}", v, (M, weights.H), t, weights.device)
+
+
+def gemm_moe_experts(dtype, x, weights: MoeWeights, ids, gates, act="silu", residual=None, y=None, workspace=None,
+                     stream=None):
+    """y = residual + sum over j of gates[m, j] * (act(x Wg^T) * (x Wu^T)) Wd^T with expert ids[m, j]'s weights: x and
+    residual [M, H], ids int32 [M, k] (outside [0, E): adds nothing), gates fp32 [M, k]. y may be the residual."""
+    import torch
+
+    where = "gemm_moe_experts"
+    dt, t = _half(dtype)
+    _here(where, "x", x, stream)
+    M, k = ids.shape
+    _moe_experts_args(where, t, x, weights, residual, y, M)
+    _want(f"{where}: ids", ids, (M, k), torch.int32, x.device)
+    _want(f"{where}: gates", gates, (M, k), torch.float32, x.device)
+    with _on(stream, x.device):
+        y = x.new_empty((M, weights.H)) if y is None else y
+        if workspace is None:
+            workspace = moe_workspace(M, k, weights)
+        _check(load_library().gemm_moe_experts(dt, _ptr(x), _ptr(weights.data), _ptr(ids), _ptr(gates), _act(act),
+                                               _ptr(residual), _ptr(y), M, weights.F, weights.H, weights.E, k,
+                                               _ptr(workspace), _workspace_bytes(where, workspace, x.device),
+                                               _stream(stream)), where)
+    return y
+
+
+def gemm_moe(dtype, x, router, weights: MoeWeights, k: int, bias=None, score="softmax", normalize=True, scale=1.0,
+             act="silu", residual=None, y=None, ids=None, gates=None, workspace=None, stream=None):
+    """(y, ids, gates): gemm_moe_route, then gemm_moe_experts on what it chose. Without a workspace (moe_workspace)
+    one is made for the call."""
+    where = "gemm_moe"
+    dt, t = _half(dtype)
+    _here(where, "x", x, stream)
+    M, E, F, H = x.shape[0], weights.E, weights.F, weights.H
+    _moe_experts_args(where, t, x, weights, residual, y, M)
+    with _on(stream, x.device):
+        ids, gates = _moe_route_args(where, t, x, router, bias, M, H, E, k, ids, gates)
+        y = x.new_empty((M, H)) if y is None else y
+        if workspace is None:
+            workspace = moe_workspace(M, k, weights)
+        _check(load_library().gemm_moe(dt, _ptr(x), _ptr(router), _ptr(bias), _score(score), int(normalize), scale,
+                                       _ptr(weights.data), _act(act), _ptr(residual), _ptr(y), _ptr(ids), _ptr(gates), M, F,
+                                       H, E, k, _ptr(workspace), _workspace_bytes(where, workspace, x.device),
+                                       _stream(stream)), where)
+    return y, ids, gates
 
 
 # ---- 4-bit weights with group scales ----

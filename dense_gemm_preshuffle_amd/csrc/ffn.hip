@@ -1,5 +1,5 @@
-// Host side of the gated feed-forward product, its backward pass and the
-// backward pass of a linear layer: validation, plans, workspaces, launches.
+// Host side of the gated feed-forward product, the linear layer with its epilogue
+// and their backward passes: validation, plans, workspaces, launches.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -9,6 +9,7 @@
 #include "../../include/gemm_preshuffle.h"
 #include "host.hpp"
 #include "launch_gated.hpp"
+#include "launch_linear.hpp"
 #include "launch_rows.hpp"
 #include "transpose.hpp"
 
@@ -17,16 +18,16 @@ namespace {
 
 bool half_type(int dtype) { return dtype == GP_BF16 || dtype == GP_F16; }
 
-// 16-byte pieces of the preshuffled gated layout: block 2p is gate block p of
-// the weights, block 2p + 1 up block p; K is filled up to kb64 64-byte blocks (a
-// multiple of two) with zeros.
-__global__ __launch_bounds__(256) void preshuffle_gated_kernel(const char* __restrict__ w, char* __restrict__ dst,
-                                                               uint32_t kb64, uint32_t Ka, uint32_t F, uint32_t chunks) {
+// 16-byte pieces of the preshuffled feed-forward layouts: K is filled up to kb64
+// 64-byte blocks (a multiple of two) with zeros; F > 0, gated: block 2p is gate block
+// p of the weights, block 2p + 1 up block p (F 0: the blocks in order).
+__global__ __launch_bounds__(256) void preshuffle_ffn_kernel(const char* __restrict__ w, char* __restrict__ dst,
+                                                             uint32_t kb64, uint32_t Ka, uint32_t F, uint32_t chunks) {
   const uint32_t x = blockIdx.x * 256u + threadIdx.x;
   if (x >= chunks) return;
   const uint32_t j = x & 15u, g = (x >> 4) & 3u, t = x >> 6;
   const uint32_t k0 = t % kb64, nb = t / kb64;
-  const uint32_t row = (nb & 1u) * F + (nb >> 1) * 16u + j, col = 64u * k0 + 16u * g;
+  const uint32_t row = (F ? (nb & 1u) * F + (nb >> 1) * 16u : nb * 16u) + j, col = 64u * k0 + 16u * g;
   *(v4i*)(dst + (size_t)x * 16u) = col < Ka ? *(const v4i*)(w + (size_t)row * Ka + col) : v4i{0, 0, 0, 0};
 }
 
@@ -91,7 +92,7 @@ double choose_tile_us(const TileTime (&times)[4], int64_t M, int64_t N, int64_t 
 
 // ---- gated product ----
 struct GatedPlan {
-  bool small = false;   // gated_small_kernel, else the tile kernel
+  bool small = false;   // ffn_small_kernel, else the tile kernel
   GatedSmall variant;
   int64_t ks = 1, tiles = 0, bytes = 0;   // small kernel: K ranges, workgroups of one, workspace
   Plan tile;
@@ -141,6 +142,48 @@ int plan_gated(int dtype, int64_t M, int64_t F, int64_t H, GatedPlan* p) {
     if (p->ks > 1) p->bytes = kCounterBytes + p->tiles * p->ks * ((rows + 15) / 16 * v.pairs * 2048);
   } else {
     p->bytes = plan_workspace(p->tile, M, 2 * F);
+  }
+  return GP_OK;
+}
+
+// ---- linear layer with its epilogue ----
+struct LinearPlan {
+  bool small = false;   // ffn_small_kernel, else the tile kernel
+  LinearSmall variant;
+  int64_t ks = 1, tiles = 0, bytes = 0;   // small kernel: K ranges, workgroups of one, workspace
+  Plan tile;
+};
+
+int check_linear(int dtype, int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return GP_EINVAL;
+  if (!half_type(dtype)) return GP_EDTYPE;
+  if (M >= kMaxBytes || N >= kMaxBytes || K >= kMaxBytes) return GP_ESHAPE;
+  if (N % 16 || K % 32) return GP_ESHAPE;
+  if (!fits(M, 2 * K) || !fits(N, 2 * whole_k(K)) || !fits(M, 2 * N)) return GP_ESHAPE;
+  return GP_OK;
+}
+
+// As the gated product (whose tile times hold: N columns here take as long as F of
+// them there take gate and up).
+int plan_linear(int dtype, int64_t M, int64_t N, int64_t K, LinearPlan* p) {
+  const int r = check_linear(dtype, M, N, K);
+  if (r) return r;
+  p->small = M <= 64;
+  if (!p->small) p->small = choose_tile_us(kGatedTimes, M, N, 2 * whole_k(K), true, &p->tile) < 0;
+  if (p->small) {
+    LinearSmall& v = p->variant;
+    const int64_t blocks = N / 16;
+    v.xl = M == 1 ? 0 : M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : M <= 48 ? 6 : 8;
+    v.s = v.xl <= 4 ? 2 : 1;
+    v.blocks = blocks >= 512 ? 2 : 1;
+    v.waves = 8;
+    const int64_t rows = v.xl == 0 ? 1 : 8 * v.xl;
+    p->tiles = ((blocks + v.blocks - 1) / v.blocks) * ((M + rows - 1) / rows);
+    if (p->tiles >= (int64_t)1 << 22) return GP_ESHAPE;   // threads of a grid
+    p->ks = split_small((double)whole_k(K) / 64 / v.waves, v.xl <= 2 ? 0.5 : v.xl == 4 ? 0.35 : 0.65, p->tiles);
+    if (p->ks > 1) p->bytes = kCounterBytes + p->tiles * p->ks * ((rows + 15) / 16 * v.blocks * 1024);
+  } else {
+    p->bytes = plan_workspace(p->tile, M, N);
   }
   return GP_OK;
 }
@@ -234,12 +277,12 @@ bool plan_pair(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t Nb, int64
   return found;
 }
 
-// gated: dc itself is made by the call ([M][Np] in the workspace).
+// gated: dc itself is made by the call ([M][Np] in the workspace; N % 16 is enough).
 int make_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, bool gated, BackwardPlan* p) {
   if (M <= 0 || N <= 0 || K <= 0) return GP_EINVAL;
   if (!half_type(dtype)) return GP_EDTYPE;
   if (M >= kMaxBytes / 4 || N >= kMaxBytes || K >= kMaxBytes) return GP_ESHAPE;
-  if (N % 32 || K % 32) return GP_ESHAPE;
+  if (N % (gated ? 16 : 32) || K % 32) return GP_ESHAPE;
   p->Mp = pad_k(M);
   p->Np = gated ? pad_k(N) : N;
   if (!fits(p->Mp, 2 * K) || !fits(p->Np, 2 * K) || !fits(p->Mp, 2 * p->Np)) return GP_ESHAPE;
@@ -335,10 +378,11 @@ TileArgs rows_args(const Plan& p, const void* a, int64_t lda, const void* b, voi
 
 // Launches, in order, what has to run once the pointers are valid. dc: the
 // output gradient, rows of ldc elements; gate: the pointwise backward that makes
-// it first (else null). Stops at the first launch that fails.
-int run_backward(int dtype, const BackwardPlan& p, const GateGradArgs* gate, const void* dc, const void* a,
-                 const void* b, void* da, void* db, int64_t M, int64_t N, int64_t K, char* ws, hipStream_t s) {
-  const int64_t ldc = gate ? p.Np : N;
+// it first (else null; linear: the linear layer's). Stops at the first launch that
+// fails.
+int run_backward(int dtype, const BackwardPlan& p, const GateGradArgs* gate, bool linear, const void* dc, int64_t ldc,
+                 const void* a, const void* b, void* da, void* db, int64_t M, int64_t N, int64_t K, char* ws,
+                 hipStream_t s) {
   PrepArgs t = {};
   uint64_t blocks = 0;
   if (gate) {
@@ -371,8 +415,9 @@ int run_backward(int dtype, const BackwardPlan& p, const GateGradArgs* gate, con
   int r;
   if (blocks > 0) {
     forget_hip_error();
-    if (dtype == GP_BF16) hipLaunchKernelGGL((prep_kernel<DT_BF16>), dim3((uint32_t)blocks), dim3(256), 0, s, t);
-    else hipLaunchKernelGGL((prep_kernel<DT_F16>), dim3((uint32_t)blocks), dim3(256), 0, s, t);
+    auto* prep = dtype == GP_BF16 ? (linear ? prep_kernel<DT_BF16, true> : prep_kernel<DT_BF16, false>)
+                                  : (linear ? prep_kernel<DT_F16, true> : prep_kernel<DT_F16, false>);
+    hipLaunchKernelGGL(prep, dim3((uint32_t)blocks), dim3(256), 0, s, t);
     if ((r = report_hip(hipGetLastError(), "kernel launch"))) return r;
   }
   const bool bf16 = dtype == GP_BF16;
@@ -412,6 +457,25 @@ int plan_gated_backward(int dtype, int64_t M, int64_t F, int64_t H, bool dx, boo
   return plan_backward(dtype, M, 2 * F, H, dx, dw, true, p);
 }
 
+// gemm_linear_backward: the products of gemm_backward, on a dz that the call makes where
+// there is an activation or N is no whole number of 64-byte blocks. Its workspace is
+// the products' (dz among it), then the row tiles' sums of the bias gradient.
+struct LinearBackwardPlan {
+  BackwardPlan products;
+  bool made = false;
+  int64_t off_sums = 0, bytes = 0;
+};
+int plan_linear_backward(int dtype, int64_t M, int64_t N, int64_t K, int act, bool dx, bool dw, bool db,
+                         LinearBackwardPlan* p) {
+  p->made = act != GP_ACT_NONE || N % 32;
+  // (the sizes are checked as for the products, also where only the sums are wanted)
+  const int r = plan_backward(dtype, M, N, K, dx || !dw, dw, p->made, &p->products);
+  if (r) return r;
+  p->off_sums = dx || dw ? align256(p->products.bytes) : 0;
+  p->bytes = std::max<int64_t>(p->off_sums + (db ? (p->products.Mp + 63) / 64 * N * 4 : 0), 256);
+  return GP_OK;
+}
+
 }  // namespace
 }  // namespace gp
 
@@ -429,7 +493,7 @@ int gemm_gated_preshuffle(const void* w, void* w_shuf, int64_t F, int64_t H, int
   if ((r = require_gfx950())) return r;
   const uint32_t chunks = (uint32_t)(bytes / 16);
   forget_hip_error();
-  hipLaunchKernelGGL(preshuffle_gated_kernel, dim3((chunks + 255) / 256), dim3(256), 0, (hipStream_t)stream, wb,
+  hipLaunchKernelGGL(preshuffle_ffn_kernel, dim3((chunks + 255) / 256), dim3(256), 0, (hipStream_t)stream, wb,
                      (char*)w_shuf, (uint32_t)(whole_k(H) / 32), (uint32_t)(2 * H), (uint32_t)F, chunks);
   return report_hip(hipGetLastError(), "kernel launch");
 }
@@ -486,6 +550,8 @@ int gemm_gated(int dtype, const void* x, const void* w_shuf, int act, void* h, v
     t.c = (char*)h;
     t.gate = (char*)gate;
     t.up = (char*)up;
+    t.bias = nullptr;
+    t.res = nullptr;
     t.M = (uint32_t)M;
     t.F = (uint32_t)F;
     t.Ka = (uint32_t)(2 * H);
@@ -520,6 +586,169 @@ int gemm_gated(int dtype, const void* x, const void* w_shuf, int act, void* h, v
                          : launch_gated_tile_f16(p.tile.tm, p.tile.tn, t, s);
   }
   return report_hip(e, "kernel launch");
+}
+
+int gemm_linear_preshuffle(const void* w, void* w_shuf, int64_t N, int64_t K, int dtype, void* stream) {
+  if (!w || !w_shuf || !is_aligned16(w) || !is_aligned16(w_shuf)) return GP_EINVAL;
+  int r = check_linear(dtype, 1, N, K);
+  if (r) return r;
+  const int64_t bytes = 2 * N * whole_k(K);
+  const char *wb = (const char*)w, *sb = (const char*)w_shuf;
+  if (sb < wb + 2 * N * K && wb < sb + bytes) return GP_EINVAL;   // overlap
+  if ((r = require_gfx950())) return r;
+  const uint32_t chunks = (uint32_t)(bytes / 16);
+  forget_hip_error();
+  hipLaunchKernelGGL(preshuffle_ffn_kernel, dim3((chunks + 255) / 256), dim3(256), 0, (hipStream_t)stream, wb,
+                     (char*)w_shuf, (uint32_t)(whole_k(K) / 32), (uint32_t)(2 * K), 0u, chunks);
+  return report_hip(hipGetLastError(), "kernel launch");
+}
+
+int gemm_linear_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes) return GP_EINVAL;
+  LinearPlan p;
+  const int r = plan_linear(dtype, M, N, K, &p);
+  if (r) return r;
+  *bytes = (size_t)p.bytes;
+  return GP_OK;
+}
+
+int gemm_linear_plan(int dtype, int64_t M, int64_t N, int64_t K, gemm_plan_info* out) {
+  if (!out) return GP_EINVAL;
+  LinearPlan p;
+  const int r = plan_linear(dtype, M, N, K, &p);
+  if (r) return r;
+  *out = gemm_plan_info();
+  out->kernel = p.small ? GP_KERNEL_SPLITK : GP_KERNEL_TILE;
+  out->tile_m = p.small ? (p.variant.xl == 0 ? 1 : 8 * p.variant.xl) : p.tile.tm;
+  out->tile_n = p.small ? 16 * p.variant.blocks : p.tile.tn;
+  out->tile_k = p.small ? 64 * p.variant.s : 64;
+  out->waves = p.small ? p.variant.waves : tile_waves(p.tile.tm, p.tile.tn);
+  out->threads = 64 * out->waves;
+  out->ksplit = p.small ? (int)p.ks : p.tile.ks;
+  out->grid = out->ksplit * (p.small ? p.tiles : (M + p.tile.tm - 1) / p.tile.tm * ((N + p.tile.tn - 1) / p.tile.tn));
+  out->mfma = 16;
+  out->workspace_bytes = p.bytes;
+  return GP_OK;
+}
+
+int gemm_linear(int dtype, const void* x, const void* w_shuf, const float* bias, int act, const void* residual, void* y,
+                void* z, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!x || !w_shuf || !y || !is_aligned16(x) || !is_aligned16(w_shuf) || !is_aligned16(y)) return GP_EINVAL;
+  if (!is_aligned16(bias) || !is_aligned16(residual) || !is_aligned16(z)) return GP_EINVAL;
+  if (act < GP_ACT_NONE || act > GP_ACT_GELU) return GP_EINVAL;
+  LinearPlan p;
+  int r = plan_linear(dtype, M, N, K, &p);
+  if (r) return r;
+  if (p.bytes > 0) {
+    if (!workspace || (int64_t)workspace_bytes < p.bytes) return GP_EWORKSPACE;
+    if (!is_aligned16(workspace)) return GP_EINVAL;
+  }
+  if ((r = require_gfx950())) return r;
+  const hipStream_t s = (hipStream_t)stream;
+  forget_hip_error();
+  hipError_t e;
+  if (p.small) {
+    GatedArgs t;
+    t.a = (const char*)x;
+    t.b = (const char*)w_shuf;
+    t.c = (char*)y;
+    t.gate = (char*)z;
+    t.up = nullptr;
+    t.bias = bias;
+    t.res = (const char*)residual;
+    t.M = (uint32_t)M;
+    t.F = (uint32_t)N;
+    t.Ka = (uint32_t)(2 * K);
+    t.Kb = (uint32_t)(2 * whole_k(K));
+    t.act = act;
+    t.ksplit = (uint32_t)p.ks;
+    t.cnt = p.ks > 1 ? (uint32_t*)workspace : nullptr;
+    t.part = p.ks > 1 ? (char*)workspace + kCounterBytes : nullptr;
+    e = dtype == GP_BF16 ? launch_linear_small_bf16(p.variant, t, s) : launch_linear_small_f16(p.variant, t, s);
+  } else {
+    TileArgs t = {};
+    t.a = (const char*)x;
+    t.b = (const char*)w_shuf;
+    t.bias = bias;
+    t.c = (char*)y;
+    t.z = (char*)z;
+    t.res = (const char*)residual;
+    t.M = (uint32_t)M;
+    t.N = (uint32_t)N;
+    t.Kb = (uint32_t)(2 * whole_k(K));
+    t.ka = (uint32_t)(2 * K);
+    t.tiles_m = (uint32_t)((M + p.tile.tm - 1) / p.tile.tm);
+    t.tiles_n = (uint32_t)((N + p.tile.tn - 1) / p.tile.tn);
+    t.xcd = 1;
+    t.act = act;
+    t.ksplit = (uint32_t)p.tile.ks;
+    t.cnt = p.tile.ks > 1 ? (uint32_t*)workspace : nullptr;
+    t.part = p.tile.ks > 1 ? (char*)workspace + kCounterBytes : nullptr;
+    e = dtype == GP_BF16 ? launch_linear_tile_bf16(p.tile.tm, p.tile.tn, t, s)
+                         : launch_linear_tile_f16(p.tile.tm, p.tile.tn, t, s);
+  }
+  return report_hip(e, "kernel launch");
+}
+
+int gemm_linear_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int act, int want_dx, int want_dw,
+                                        int want_dbias, size_t* bytes) {
+  if (!bytes || (!want_dx && !want_dw && !want_dbias) || act < GP_ACT_NONE || act > GP_ACT_GELU) return GP_EINVAL;
+  LinearBackwardPlan p;
+  const int r = plan_linear_backward(dtype, M, N, K, act, want_dx != 0, want_dw != 0, want_dbias != 0, &p);
+  if (r) return r;
+  *bytes = (size_t)p.bytes;
+  return GP_OK;
+}
+
+int gemm_linear_backward(int dtype, const void* dy, const void* z, const void* x, const void* w, int act, void* dx,
+                         void* dw, float* dbias, int64_t M, int64_t N, int64_t K, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  if (!dy || (!dx && !dw && !dbias) || act < GP_ACT_NONE || act > GP_ACT_GELU) return GP_EINVAL;
+  if ((act != GP_ACT_NONE && !z) || (dx && !w) || (dw && !x)) return GP_EINVAL;
+  if (!is_aligned16(dy) || !is_aligned16(z) || !is_aligned16(x) || !is_aligned16(w) || !is_aligned16(dx) ||
+      !is_aligned16(dw) || !is_aligned16(dbias))
+    return GP_EINVAL;
+  LinearBackwardPlan p;
+  int r = plan_linear_backward(dtype, M, N, K, act, dx != nullptr, dw != nullptr, dbias != nullptr, &p);
+  if (r) return r;
+  if (!workspace || (int64_t)workspace_bytes < p.bytes) return GP_EWORKSPACE;
+  if (!is_aligned16(workspace)) return GP_EINVAL;
+  if ((r = require_gfx950())) return r;
+  char* ws = (char*)workspace;
+  const hipStream_t s = (hipStream_t)stream;
+  const bool products = dx || dw;
+  const BackwardPlan& q = p.products;
+  GateGradArgs t = {};
+  t.dh = (const char*)dy;
+  t.gate = act == GP_ACT_NONE ? nullptr : (const char*)z;
+  t.d = p.made && (dx || (dw && q.db_rows)) ? ws + q.off_d : nullptr;
+  t.dt = dw && !q.db_rows ? ws + q.off_ct : nullptr;
+  t.sums = dbias ? (float*)(ws + p.off_sums) : nullptr;
+  t.M = (uint32_t)M;
+  t.F = (uint32_t)N;
+  t.Mp = (uint32_t)q.Mp;
+  t.Np = (uint32_t)q.Np;
+  t.tiles_c = (uint32_t)((N + 63) / 64);
+  t.act = act;
+  // the products last: where no product is wanted nothing but the sums runs
+  const bool pass = p.made || dbias;
+  if (products) {
+    r = run_backward(dtype, q, pass ? &t : nullptr, true, p.made ? (const void*)(ws + q.off_d) : dy, p.made ? q.Np : N, x, w,
+                     dx, dw, M, N, K, ws, s);
+  } else {
+    PrepArgs only = {};
+    only.gate = t;
+    only.gate.blocks = tiles64(q.Mp, N);
+    forget_hip_error();
+    auto* prep = dtype == GP_BF16 ? prep_kernel<DT_BF16, true> : prep_kernel<DT_F16, true>;
+    hipLaunchKernelGGL(prep, dim3(only.gate.blocks), dim3(256), 0, s, only);
+    r = report_hip(hipGetLastError(), "kernel launch");
+  }
+  if (r || !dbias) return r;
+  forget_hip_error();
+  hipLaunchKernelGGL(bias_sums_kernel, dim3((uint32_t)((N + 31) / 32)), dim3(1024), 0, s, (const float*)t.sums, dbias,
+                     (uint32_t)N, (uint32_t)((q.Mp + 63) / 64));
+  return report_hip(hipGetLastError(), "kernel launch");
 }
 
 int gemm_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int want_da, int want_db, size_t* bytes) {
@@ -571,7 +800,7 @@ int gemm_backward(int dtype, const void* dc, const void* a, const void* b, void*
   if (!workspace || (int64_t)workspace_bytes < p.bytes) return GP_EWORKSPACE;
   if (!is_aligned16(workspace)) return GP_EINVAL;
   if ((r = require_gfx950())) return r;
-  return run_backward(dtype, p, nullptr, dc, a, b, da, db, M, N, K, (char*)workspace, (hipStream_t)stream);
+  return run_backward(dtype, p, nullptr, false, dc, N, a, b, da, db, M, N, K, (char*)workspace, (hipStream_t)stream);
 }
 
 int gemm_gated_backward_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, int want_dx, int want_dw,
@@ -612,7 +841,7 @@ int gemm_gated_backward(int dtype, const void* dh, const void* gate, const void*
   t.Np = (uint32_t)p.Np;
   t.tiles_c = (uint32_t)((F + 63) / 64);
   t.act = act;
-  return run_backward(dtype, p, &t, ws + p.off_d, x, w, dx, dw, M, 2 * F, H, ws, (hipStream_t)stream);
+  return run_backward(dtype, p, &t, false, ws + p.off_d, p.Np, x, w, dx, dw, M, 2 * F, H, ws, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -52,7 +52,9 @@ struct TileArgs {
   int act;            // Act
   char* gate;         // EPI_GATED: [M][N/2] gate and up products to keep, or null
   char* up;
-  uint32_t ka;        // EPI_GATED, EPI_ROWS: bytes per row of A (at most Kb; K past them reads zeros)
+  char* z;            // EPI_LINEAR: [M][N] product + bias to keep, or null
+  const char* res;    // EPI_LINEAR: [M][N] residual, or null
+  uint32_t ka;        // EPI_GATED, EPI_LINEAR, EPI_ROWS: bytes per row of A (at most Kb; K past them reads zeros)
   uint32_t kb_rows, ldb;  // EPI_ROWS: rows of B (K, below 16-bit elements of Kb: the rest are zeros), bytes per row
   // K split across workgroups (tile kernel): ksplit workgroups share each
   // tile, each taking a contiguous range of its K tiles; their partial sums
@@ -126,6 +128,7 @@ struct TileCfg {
   static constexpr int OB = (DT == DT_I8) ? 4 : 2;        // output element bytes
   static constexpr bool FSC = DT == DT_FP8 || DT == DT_I4;  // fp32 row / column scales
   static constexpr bool ROWS = EPI == EPI_ROWS || EPI == EPI_ROWS_T;   // B row-major [K][N]
+  static constexpr bool FFN = EPI == EPI_GATED || EPI == EPI_LINEAR;   // K filled up to whole tiles in B alone
   static constexpr int CCOLS = (EPI == EPI_GATED) ? TN / 2 : (EPI == EPI_ROWS_T) ? TM : TN;   // stored columns
   static constexpr int CROWS = (EPI == EPI_ROWS_T) ? TN : TM;   // and rows
   static constexpr int CSTRIDE = CCOLS * OB + 16;         // padded C row in LDS
@@ -220,6 +223,8 @@ struct TileCfg {
   static_assert(KG == 1 || (KG == 2 && !NSC), "K groups: not with FP4's staged scales");
   static_assert(DT != DT_I4 || MS == 16, "W4A8: 16 x 16 blocks");
   static_assert(WAVES == 4 || KG == 1, "8-wave tiles: one K group");
+  static_assert(EPI != EPI_LINEAR || (MS == 16 && KG == 1 && FUSED && TM * CPR % 8 == 0 && (DT == DT_BF16 || DT == DT_F16)),
+                "linear epilogue");
   static_assert(EPI != EPI_GATED || (MS == 16 && NACC % 2 == 0 && KG == 1 && (DT == DT_BF16 || DT == DT_F16)),
                 "gated epilogue: whole gate / up pairs of 16-column blocks per wave");
   static_assert(!ROWS || (MS == 16 && (NACC == 2 || NACC == 4) && KG == 1 && PIPE != 0 && (DT == DT_BF16 || DT == DT_F16)),
@@ -301,7 +306,7 @@ __device__ __forceinline__ void gemm_tile_body(const TileArgs& p, uint32_t w, ch
   const int lgrp = lane / MS;
 
   uint32_t tm, tn, kz;
-  tile_coords<C::ROWS || EPI == EPI_GATED>(p, w, tm, tn, kz);
+  tile_coords<C::ROWS || C::FFN>(p, w, tm, tn, kz);
   uint32_t m0 = tm * TM, n0 = tn * TN, mskip, nskip;
   if constexpr (C::ROWS) {
     // a matrix smaller than the tile: rows of A past it read zeros, what B
@@ -317,12 +322,12 @@ __device__ __forceinline__ void gemm_tile_body(const TileArgs& p, uint32_t w, ch
   const uint32_t Kb = p.Kb;
   // bytes per row of A; AMASK: K is filled up to whole tiles beside A, whose
   // rows end earlier
-  constexpr bool AMASK = C::ROWS || EPI == EPI_GATED;
+  constexpr bool AMASK = C::ROWS || C::FFN;
   const uint32_t Ka = AMASK ? p.ka : Kb * C::AKB;
   // K tiles of this workgroup: split kz of ksplit equal ranges; of this group:
   // [kt0, kt0 + KT) (the planner makes ksplit * KG divide the K tiles). With a
-  // row-major B or the gated epilogue the ranges may differ by a tile.
-  constexpr bool UNEVEN = C::ROWS || EPI == EPI_GATED;
+  // row-major B, the gated or the linear epilogue the ranges may differ by a tile.
+  constexpr bool UNEVEN = C::ROWS || C::FFN;
   const int KALL = (int)(Kb / TKB);
   const int KTS = KALL / (KS ? (int)p.ksplit : 1);
   const int kr0 = KS && UNEVEN ? (int)kz * KALL / (int)p.ksplit : (int)kz * KTS;
@@ -1032,6 +1037,72 @@ __device__ __forceinline__ void gemm_tile_body(const TileArgs& p, uint32_t w, ch
       store_half(p.gate, [](Acc g, Acc) GP_INLINE -> v4f { return g; });
       store_half(p.up, [](Acc, Acc u) GP_INLINE -> v4f { return u; });
     }
+    return;
+  }
+
+  if constexpr (EPI == EPI_LINEAR) {
+    // Through LDS (the A buffers are dead) for whole rows: the residual's tile is
+    // put there first, every lane adds its own elements to it in fp32, rounds once
+    // and puts the sum in their place. Its loads are issued before anything else of
+    // the epilogue. An edge tile's rows and columns that belong to its neighbour are
+    // read (in place they may change meanwhile), added up and not stored.
+    constexpr int CH_ROW = TN * C::OB / 16, PASSES = TM * CH_ROW / C::THREADS;
+    static_assert(EPI != EPI_LINEAR || TM * CH_ROW % C::THREADS == 0, "whole passes");
+    const size_t base = ((size_t)m0 * p.N + n0) * C::OB;
+    const uint32_t bytes = ((TM - 1) * p.N + TN) * C::OB;
+    v4i held[PASSES];
+    auto piece = [&](int i) GP_INLINE -> char* {   // in LDS
+      const int q = i * C::THREADS + etid;
+      return lds + (q / CH_ROW) * C::CSTRIDE + (q % CH_ROW) * 16;
+    };
+    if (p.res) {
+      const __amdgpu_buffer_rsrc_t rr = make_rsrc(p.res + base, bytes);
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const uint32_t q = i * C::THREADS + etid;
+        held[i] = buf_load16(rr, (q / CH_ROW) * p.N * C::OB + (q % CH_ROW) * 16, 0);
+      }
+    }
+    auto own = [&](int mi, int ni) GP_INLINE -> v2i* {   // this lane's 4 columns of a block, in LDS
+      return (v2i*)(lds + (mi * MS + elrow) * C::CSTRIDE + (wave * C::NPW + ni * MS + 4 * elgrp) * C::OB);
+    };
+    auto store_rows = [&](char* dst) GP_INLINE {
+      __syncthreads();
+      const __amdgpu_buffer_rsrc_t ro = make_rsrc(dst + base, bytes);
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const uint32_t q = i * C::THREADS + etid;
+        buf_store16(*(const v4i*)piece(i), ro, c_off(q / CH_ROW, (q % CH_ROW) * 8));
+      }
+      __syncthreads();
+    };
+    __syncthreads();
+    if (p.z) {
+#pragma unroll
+      for (int mi = 0; mi < C::MREP; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < C::NACC; ++ni) *own(mi, ni) = pack_out4<DT>(acc[mi][ni] + bias4(ni, 0));
+      store_rows(p.z);
+    }
+    if (p.res) {
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) *(v4i*)piece(i) = held[i];
+      __syncthreads();
+    }
+    with_act(p.act, [&](auto act_c) GP_INLINE {
+      constexpr int A = decltype(act_c)::value;
+#pragma unroll
+      for (int mi = 0; mi < C::MREP; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < C::NACC; ++ni) {
+          v4f v = acc[mi][ni] + bias4(ni, 0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = activate_ffn<A>(v[r]);
+          if (p.res) v += widen4<DT>(*own(mi, ni));
+          *own(mi, ni) = pack_out4<DT>(v);
+        }
+    });
+    store_rows(p.c);
     return;
   }
 

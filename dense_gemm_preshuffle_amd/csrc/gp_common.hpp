@@ -46,8 +46,10 @@ enum DType : int { DT_I8 = 0, DT_FP8 = 1, DT_BF16 = 2, DT_FP4 = 3, DT_F16 = 4, D
 enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
 // Not options of the C ABI: EPI_GATED: pairs of column blocks are a gate and an
 // up product, and act(gate) * up is stored; EPI_ROWS: B is row-major [K][N] (see
-// the tile kernel); EPI_ROWS_T: so, and the output is stored transposed, [N][M].
-enum Epi : int { EPI_DIRECT = 1, EPI_CSHUFFLE = 2, EPI_GATED = 3, EPI_ROWS = 4, EPI_ROWS_T = 5 };
+// the tile kernel); EPI_ROWS_T: so, and the output is stored transposed, [N][M];
+// EPI_LINEAR: act(product + bias) + residual is stored, and the sum before the
+// activation where it is to be kept.
+enum Epi : int { EPI_DIRECT = 1, EPI_CSHUFFLE = 2, EPI_GATED = 3, EPI_ROWS = 4, EPI_ROWS_T = 5, EPI_LINEAR = 6 };
 
 // gfx9 buffer resource word 3 (32-bit raw buffer, bounds checked on num_records).
 constexpr int kRsrcWord3 = 0x00020000;
@@ -271,6 +273,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return (uint32_t)__builtin_bit_cast(uint16_t, a) | ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
 }
 
+// One of two packed 16-bit values in fp32.
+template <int DT>
+__device__ __forceinline__ float widen16(uint32_t pair, int hi) {
+  if constexpr (DT == DT_BF16) return __builtin_bit_cast(float, hi ? (pair & 0xFFFF0000u) : (pair << 16));
+  else return (float)__builtin_bit_cast(_Float16, (uint16_t)(hi ? pair >> 16 : pair));
+}
+
 // Four fp32 results -> 8 bytes of the output type.
 template <int DT>
 __device__ __forceinline__ v2i pack_out4(v4f v) {
@@ -283,6 +292,12 @@ __device__ __forceinline__ v2i pack_out4(v4f v) {
     o[1] = (int)pack_bf16x2(v[2], v[3]);
   }
   return o;
+}
+
+template <int DT>
+__device__ __forceinline__ v4f widen4(v2i v) {
+  return v4f{widen16<DT>((uint32_t)v[0], 0), widen16<DT>((uint32_t)v[0], 1), widen16<DT>((uint32_t)v[1], 0),
+             widen16<DT>((uint32_t)v[1], 1)};
 }
 
 // erf for the GELU epilogue: Abramowitz & Stegun, Handbook of Mathematical

@@ -1,12 +1,12 @@
 // Launch tables of the gated product (BF16 and FP16).
 #pragma once
 
-#include "gated_small.hpp"
+#include "ffn_small.hpp"
 #include "gemm_tile.hpp"
 
 namespace gp {
 
-// A variant of gated_small_kernel: x loads (0: one row, else rows / 8), column
+// A variant of ffn_small_kernel<GATED>: x loads (0: one row, else rows / 8), column
 // pairs, waves, 64-element K chunks per group.
 struct GatedSmall {
   int xl = 0, pairs = 1, waves = 8, s = 2;
@@ -30,7 +30,7 @@ hipError_t launch_gated_small_f16(const GatedSmall& v, const GatedArgs& a, hipSt
   if (v.xl == XL && v.pairs == P && v.waves == W && v.s == S) {                                                \
     constexpr uint32_t rows = XL == 0 ? 1 : 8 * XL;                                                            \
     const dim3 grid(((a.F / 16 + P - 1) / P) * ((a.M + rows - 1) / rows) * a.ksplit);                          \
-    hipLaunchKernelGGL((gated_small_kernel<DT, XL, P, W, S>), grid, dim3(W * 64), 0, s, a);                    \
+    hipLaunchKernelGGL((ffn_small_kernel<DT, XL, 2 * P, W, S, true>), grid, dim3(W * 64), 0, s, a);            \
     return hipGetLastError();                                                                                  \
   }
 #define GP_DEFINE_GATED(NAME, DT)                                                                              \

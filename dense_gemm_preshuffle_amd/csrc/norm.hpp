@@ -13,7 +13,6 @@
 #pragma once
 
 #include "gp_common.hpp"
-#include "transpose.hpp"   // widen16
 
 namespace gp {
 

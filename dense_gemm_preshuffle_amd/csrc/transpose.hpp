@@ -82,12 +82,6 @@ __device__ __forceinline__ void copy_tile(Tile64& t, const CopyJob& p, uint32_t 
   }
 }
 
-template <int DT>
-__device__ __forceinline__ float widen16(uint32_t pair, int hi) {
-  if constexpr (DT == DT_BF16) return __builtin_bit_cast(float, hi ? (pair & 0xFFFF0000u) : (pair << 16));
-  else return (float)__builtin_bit_cast(_Float16, (uint16_t)(hi ? pair >> 16 : pair));
-}
-
 // Derivative of the activation and its value, both from one evaluation.
 //   relu' = [g > 0]; silu' = s (1 + g (1 - s)), s = 1 / (1 + e^-g);
 //   gelu' = P(g) + g p(g), P and p the normal distribution and its density.
@@ -124,13 +118,20 @@ __device__ __forceinline__ void activate_grad(float g, float& value, float& slop
 // double the products, which are 85% of a large call). Written as d [M][Np] (dg, du, then zeros from 2F to Np in
 // each row; null if no product reads it) and dt = d^T [2F][Mp], zeros from M to
 // Mp (null likewise). F % 16 == 0.
+//
+// LINEAR: the same of a linear layer with an epilogue, from dy (dh) and the kept z
+// (gate; null without an activation):
+//   d = dy * act'(z)   [M][Np], zeros from F to Np,   dt = d^T [F][Mp]
+// and, where sums is not null, the sum of d over each tile's 64 rows in fp32, before
+// its rounding ([row tiles][F]; bias_sums_kernel adds them up).
 struct GateGradArgs {
   const char *dh, *gate, *up;
   char *d, *dt;
+  float* sums;                              // LINEAR alone
   uint32_t M, F, Mp, Np, tiles_c, blocks;   // 64 x 64 tiles per row of tiles, and in all
   int act;
 };
-template <int DT>
+template <int DT, bool LINEAR>
 __device__ __forceinline__ void gate_grad_tile(Tile64& tg, Tile64& tu, const GateGradArgs& p, uint32_t block) {
   const uint32_t c0 = block % p.tiles_c * 64u, r0 = block / p.tiles_c * 64u;
   const int q = threadIdx.x & 7, rp = threadIdx.x >> 3;
@@ -141,9 +142,10 @@ __device__ __forceinline__ void gate_grad_tile(Tile64& tg, Tile64& tu, const Gat
     const bool on = c < p.F && r + h < p.M;
     const size_t off = ((size_t)(r + h) * p.F + c) * 2;
     in[0][h] = on ? *(const v4i*)(p.dh + off) : v4i{0, 0, 0, 0};
-    in[1][h] = on ? *(const v4i*)(p.gate + off) : v4i{0, 0, 0, 0};
-    in[2][h] = on ? *(const v4i*)(p.up + off) : v4i{0, 0, 0, 0};
+    in[1][h] = on && (!LINEAR || p.gate) ? *(const v4i*)(p.gate + off) : v4i{0, 0, 0, 0};
+    if constexpr (!LINEAR) in[2][h] = on ? *(const v4i*)(p.up + off) : v4i{0, 0, 0, 0};
   }
+  float sum[8] = {};   // LINEAR: of the lane's two rows, per column
   with_act(p.act, [&](auto act_c) GP_INLINE {
     constexpr int A = decltype(act_c)::value;
 #pragma unroll
@@ -153,12 +155,18 @@ __device__ __forceinline__ void gate_grad_tile(Tile64& tg, Tile64& tu, const Gat
         float og[2], ou[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float dh = widen16<DT>((uint32_t)in[0][h][i], e), g = widen16<DT>((uint32_t)in[1][h][i], e),
-                      u = widen16<DT>((uint32_t)in[2][h][i], e);
+          const float dh = widen16<DT>((uint32_t)in[0][h][i], e), g = widen16<DT>((uint32_t)in[1][h][i], e);
           float value, slope;
           activate_grad<A>(g, value, slope);
-          og[e] = dh * u * slope;
-          ou[e] = dh * value;
+          if constexpr (LINEAR) {
+            og[e] = dh * slope;
+            sum[2 * i + e] += og[e];
+            ou[e] = 0.f;
+          } else {
+            const float u = widen16<DT>((uint32_t)in[2][h][i], e);
+            og[e] = dh * u * slope;
+            ou[e] = dh * value;
+          }
         }
         if constexpr (DT == DT_F16) {
           dg[h][i] = (int)pack_f16x2(og[0], og[1]);
@@ -175,20 +183,36 @@ __device__ __forceinline__ void gate_grad_tile(Tile64& tg, Tile64& tu, const Gat
       if (r + h < p.M) {
         char* o = p.d + ((size_t)(r + h) * p.Np + c) * 2;
         *(v4i*)o = dg[h];
-        *(v4i*)(o + (size_t)p.F * 2) = du[h];
+        if constexpr (!LINEAR) *(v4i*)(o + (size_t)p.F * 2) = du[h];
       }
+  constexpr uint32_t W = LINEAR ? 1 : 2;   // halves of a row of d
   if (p.d && c0 + 64 >= p.F) {
     // the last column tile fills the padding of its rows, 8 columns at a time
-    const uint32_t pad = (p.Np - 2 * p.F) / 8, rows = r0 < p.M ? min(64u, p.M - r0) : 0u;
+    const uint32_t pad = (p.Np - W * p.F) / 8, rows = r0 < p.M ? min(64u, p.M - r0) : 0u;
     for (uint32_t x = threadIdx.x; x < rows * pad; x += 256)
-      *(v4i*)(p.d + ((size_t)(r0 + x / pad) * p.Np + 2 * p.F + x % pad * 8) * 2) = v4i{0, 0, 0, 0};
+      *(v4i*)(p.d + ((size_t)(r0 + x / pad) * p.Np + W * p.F + x % pad * 8) * 2) = v4i{0, 0, 0, 0};
+  }
+  if constexpr (LINEAR) {
+    if (p.sums) {
+      // the wave's 16 rows through its lanes (q is lane % 8), the four waves' through LDS, in order
+      float* red = (float*)tu.d;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        for (int o = 8; o < 64; o <<= 1) sum[i] += __shfl_xor(sum[i], o, 64);
+        if ((threadIdx.x & 63) < 8) red[(threadIdx.x >> 6) * 64 + 8 * q + i] = sum[i];
+      }
+      __syncthreads();
+      const uint32_t k = threadIdx.x;
+      if (k < 64 && c0 + k < p.F)
+        p.sums[(size_t)(block / p.tiles_c) * p.F + c0 + k] = ((red[k] + red[64 + k]) + red[128 + k]) + red[192 + k];
+    }
   }
   if (!p.dt) return;
   tg.put(q, rp, dg[0], dg[1]);
-  tu.put(q, rp, du[0], du[1]);
+  if constexpr (!LINEAR) tu.put(q, rp, du[0], du[1]);
   __syncthreads();
   store_transposed(tg, p.dt, c0, r0, p.F, p.Mp);
-  store_transposed(tu, p.dt + (size_t)p.F * p.Mp * 2, c0, r0, p.F, p.Mp);
+  if constexpr (!LINEAR) store_transposed(tu, p.dt + (size_t)p.F * p.Mp * 2, c0, r0, p.F, p.Mp);
 }
 
 // Everything the backward products need beforehand, in one launch (a launch costs
@@ -200,14 +224,14 @@ struct PrepArgs {
   uint32_t* cnt;       // null: none
   uint32_t ncnt;
 };
-template <int DT>
+template <int DT, bool LINEAR>
 __global__ __launch_bounds__(256) void prep_kernel(PrepArgs p) {
   __shared__ __attribute__((aligned(16))) Tile64 t0, t1;
   if (p.cnt)
     for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < p.ncnt; i += gridDim.x * 256u) p.cnt[i] = 0u;
   uint32_t b = blockIdx.x;
   if (b < p.gate.blocks) {
-    gate_grad_tile<DT>(t0, t1, p.gate, b);
+    gate_grad_tile<DT, LINEAR>(t0, t1, p.gate, b);
     return;
   }
   b -= p.gate.blocks;
@@ -219,6 +243,24 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepArgs p) {
     }
     b -= p.copy[i].blocks;
   }
+}
+
+// A bias gradient from the row tiles' sums: 32 columns a workgroup, 32 tiles at a
+// time, then those in order.
+__global__ __launch_bounds__(1024) inline void bias_sums_kernel(const float* sums, float* db, uint32_t N, uint32_t tiles) {
+  __shared__ float red[32][33];
+  const uint32_t lane = threadIdx.x & 31, row = threadIdx.x >> 5, c = blockIdx.x * 32u + lane;
+  float s = 0.f;
+  if (c < N) {
+#pragma unroll 4
+    for (uint32_t q = row; q < tiles; q += 32) s += sums[(size_t)q * N + c];
+  }
+  red[row][lane] = s;
+  __syncthreads();
+  if (row != 0 || c >= N) return;
+#pragma unroll
+  for (int q = 1; q < 32; ++q) s += red[q][lane];
+  db[c] = s;
 }
 
 }  // namespace gp

@@ -146,6 +146,16 @@
   X(DT, 256, 256, false) X(DT, 128, 256, false) X(DT, 128, 128, false) X(DT, 64, 128, false) \
   X(DT, 128, 256, true) X(DT, 128, 128, true) X(DT, 64, 128, true)
 
+// Linear layer with its epilogue (BF16 / FP16, 16 x 16 blocks, 128-byte K tiles, 3
+// stages): X(dtype, tile_m, tile_n, able to split K across workgroups); and its
+// small-M kernel: X(dtype, x loads, column blocks, waves, K chunks per group).
+#define GP_TILE_LINEAR(X, DT) \
+  X(DT, 256, 256, false) X(DT, 128, 256, false) X(DT, 128, 128, false) X(DT, 64, 128, false) \
+  X(DT, 128, 256, true) X(DT, 128, 128, true) X(DT, 64, 128, true)
+#define GP_SMALL_LINEAR(X, DT) \
+  X(DT, 0, 1, 8, 2) X(DT, 0, 2, 8, 2) X(DT, 1, 1, 8, 2) X(DT, 1, 2, 8, 2) X(DT, 2, 1, 8, 2) X(DT, 2, 2, 8, 2) \
+  X(DT, 4, 1, 8, 2) X(DT, 4, 2, 8, 2) X(DT, 6, 1, 8, 1) X(DT, 6, 2, 8, 1) X(DT, 8, 1, 8, 1) X(DT, 8, 2, 8, 1)
+
 // Row-major B (BF16 / FP16, 16 x 16 blocks, 128-byte K tiles): X(dtype,
 // epilogue, tile_m, tile_n, stages, able to split K across workgroups). Three
 // stages of B do not fit the registers of the 128 x 256 tile, nor of the 256 x 256

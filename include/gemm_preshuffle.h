@@ -95,6 +95,12 @@ typedef enum gp_norm {
   GP_NORM_LAYER = 2
 } gp_norm;
 
+/* Scores of the router of gemm_moe over a token's logits l. */
+typedef enum gp_score {
+  GP_SCORE_SOFTMAX = 0,   /* exp(l) / sum of exp(l) over all experts */
+  GP_SCORE_SIGMOID = 1    /* 1 / (1 + exp(-l))                       */
+} gp_score;
+
 enum {
   GP_EPI_AUTO = 0,      /* planner's choice                                   */
   GP_EPI_DIRECT = 1,    /* each lane stores its accumulators (GEMM Opt. §7.1) */
@@ -456,6 +462,65 @@ int gemm_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, int want_da, 
                        gemm_plan_info* da, gemm_plan_info* db);
 
 /*
+ * ---- Linear layer with its epilogue and its backward pass (BF16, FP16) ----
+ *
+ *   z = x W^T + bias,  y = act(z) + residual
+ *
+ * x [M][K], W [N][K], z / y / residual [M][N] of one type (GP_BF16 or GP_F16, else
+ * GP_EDTYPE), bias fp32 [N]. M is free, N % 16 == 0, K % 32 == 0 (else GP_ESHAPE),
+ * every matrix below 2^31 bytes.
+ *
+ * gemm_linear_preshuffle -- w [N][K] -> w_shuf (2 N K' bytes, K' = K rounded up to
+ * a multiple of 64; no overlap): the layout of gemm_preshuffle_b, with zeros from K
+ * to K' (the same bytes as gemm_preshuffle_b's where K % 64 == 0).
+ */
+int gemm_linear_preshuffle(const void* w, void* w_shuf, int64_t N, int64_t K, int dtype, void* stream);
+
+/*
+ * gemm_linear -- one kernel: the product is accumulated in fp32, bias, activation
+ * and residual are taken in fp32 and y is rounded once.
+ *   w_shuf      from gemm_linear_preshuffle.
+ *   bias, residual   NULL: none. y may be the residual itself (in place); no
+ *               other overlap.
+ *   z           device [M][N], or NULL: z rounded to the type, which the backward
+ *               pass of an activation reads.
+ *   workspace   as for gemm_ex_ws (its first 64 KiB zero before the first call and
+ *               left zero by each), at least gemm_linear_workspace_size bytes; may
+ *               be NULL where that is 0.
+ * The activations keep NaN and are those of gemm_gated. All device pointers 16-byte
+ * aligned (GP_EINVAL). The same call gives the same bits.
+ */
+int gemm_linear(int dtype, const void* x, const void* w_shuf, const float* bias, int act, const void* residual, void* y,
+                void* z, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Host-only: the workspace bytes of gemm_linear for these sizes (0: none), and the
+ * kernel that it runs (as gemm_gated_plan). */
+int gemm_linear_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, size_t* bytes);
+int gemm_linear_plan(int dtype, int64_t M, int64_t N, int64_t K, gemm_plan_info* out);
+
+/*
+ * gemm_linear_backward -- gradients of gemm_linear from dy = dL/dy (the residual's
+ * gradient is dy itself):
+ *   dz = dy * act'(z),  dx [M][K] = dz W,  dw [N][K] = dz^T x,  dbias [N] = sum over m of dz
+ *   z           as kept; may be NULL without an activation (dz = dy).
+ *   w           row-major (needed for dx); x (needed for dw).
+ *   dx, dw, dbias   outputs of the type, dbias fp32; each may be NULL, not all.
+ *   workspace   16-byte aligned, at least gemm_linear_backward_workspace_size bytes
+ *               for the same act and outputs; its contents need not be set.
+ * With an activation dz is rounded to the type before the two products (in FP16 one
+ * beyond 65504 is infinite, one below 2^-25 zero); dbias is summed in fp32 before
+ * that rounding, in a fixed order. Sizes as gemm_linear's; for the limit of 2^31 bytes
+ * M and N count rounded up, by a sixteenth at most (and to multiples of 64).
+ */
+int gemm_linear_backward(int dtype, const void* dy, const void* z, const void* x, const void* w, int act, void* dx,
+                         void* dw, float* dbias, int64_t M, int64_t N, int64_t K, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Host-only: the workspace bytes of gemm_linear_backward. */
+int gemm_linear_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int act, int want_dx, int want_dw,
+                                        int want_dbias, size_t* bytes);
+
+/*
  * ---- Products with 4-bit weights and group scales (BF16 / FP16 activations) ----
  *
  *   y = act(x W^T + bias),  W[n][k] = scale[n][k / G] (q[n][k] - zero[n][k / G])
@@ -571,6 +636,66 @@ int gemm_norm_backward(int dtype, const void* dy, const void* dr, const void* x,
 
 /* Host-only: the workspace bytes of gemm_norm_backward. */
 int gemm_norm_backward_workspace_size(int dtype, int64_t M, int64_t H, int64_t gates, size_t* bytes);
+
+/*
+ * ---- Mixture-of-experts layer for a few tokens (BF16, FP16) ----
+ *
+ *   l = x Wr^T, p = softmax(l) or sigmoid(l); the k experts of largest p + bias of
+ *   each token, by falling p + bias, ties to the lowest expert; their weights
+ *   g_j = scale * p_j, or (normalize) scale * p_j / (sum of the chosen p)
+ *   y = residual + sum over j of g_j (act(x Wg^T) * (x Wu^T)) Wd^T,  the weights of
+ *   the j-th chosen expert
+ *
+ * for generated tokens: bound by reading the chosen experts' weights, once each. x, y
+ * and residual are [M][H], the router Wr [E][H], of one type (GP_BF16 or GP_F16,
+ * else GP_EDTYPE). F % 16 == 0, H % 32 == 0, M <= 256, k <= 32 and <= E, E <= 512, an
+ * expert's matrix below 2^31 bytes (else GP_ESHAPE); the experts' weights together of
+ * any size.
+ *
+ * gemm_moe_weights_size -- host-only: bytes of the laid-out weights.
+ * gemm_moe_preshuffle -- w13 [E][2F][H] (an expert's F gate rows, then its F up
+ * rows) and w2 [E][H][F] -> w_shuf (gemm_moe_weights_size bytes, no overlap), once
+ * per layer.
+ */
+int gemm_moe_weights_size(int64_t E, int64_t F, int64_t H, size_t* bytes);
+int gemm_moe_preshuffle(int dtype, const void* w13, const void* w2, void* w_shuf, int64_t E, int64_t F, int64_t H,
+                        void* stream);
+
+/*
+ * gemm_moe_route -- the router: ids int32 [M][k] and gates fp32 [M][k]. Logits and
+ * scores are taken in 64 bits, so that the choice depends on the inputs alone. NaN
+ * counts as less than any number in the choice (ids are distinct experts always) and
+ * stays NaN in the weights.
+ *   bias        device fp32 [E], added to the scores for the choice alone, or NULL.
+ *   score       GP_SCORE_*.
+ *   workspace   as for gemm_ex_ws (its first 64 KiB zero before the first call and
+ *               left zero by each; calls that may overlap need one each),
+ *               gemm_moe_workspace_size bytes of any F.
+ */
+int gemm_moe_route(int dtype, const void* x, const void* router, const float* bias, int score, int normalize, float scale,
+                   int32_t* ids, float* gates, int64_t M, int64_t H, int64_t E, int64_t k, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * gemm_moe_experts -- the experts' products for choices and weights that the caller
+ * has. An id outside [0, E) (an expert that is elsewhere, or none) adds nothing; an
+ * expert may stand twice for a token. h = act(gate) * up is rounded to the type
+ * between the two products (as gemm_gated stores it), all else stays fp32; y is
+ * rounded once.
+ *   residual    device [M][H], or NULL. y may be the residual; it is not x.
+ * The same call gives the same bits.
+ */
+int gemm_moe_experts(int dtype, const void* x, const void* w_shuf, const int32_t* ids, const float* gates, int act,
+                     const void* residual, void* y, int64_t M, int64_t F, int64_t H, int64_t E, int64_t k,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* gemm_moe -- both, one after the other; ids and gates are outputs. */
+int gemm_moe(int dtype, const void* x, const void* router, const float* bias, int score, int normalize, float scale,
+             const void* w_shuf, int act, const void* residual, void* y, int32_t* ids, float* gates, int64_t M, int64_t F,
+             int64_t H, int64_t E, int64_t k, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Host-only: the workspace bytes of gemm_moe and its two parts. */
+int gemm_moe_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, int64_t E, int64_t k, size_t* bytes);
 
 /* Static, human-readable description of a gp_status value. */
 const char* gemm_status_string(int status);
