@@ -163,25 +163,57 @@ int check_linear(int dtype, int64_t M, int64_t N, int64_t K) {
   return GP_OK;
 }
 
-// As the gated product (whose tile times hold: N columns here take as long as F of
-// them there take gate and up).
+// Column blocks and K ranges of the small kernel for M rows, of least time by the model
+//   2.8 + rounds * (K / ranges) (32 blocks / 55 + 2 M / 100) + join   (us, K in 1000s)
+// of a workgroup's bytes of weights (55 a ns for a CU) and of x, which every workgroup
+// reads again from L2 (100 a ns): wide workgroups read x less often, and then K ranges
+// give every CU one; join: 0.7 and 0.4 per range. Fitted to 450 sizes (M 1 to 64, N and K
+// 256 to 16384), each timed on every variant with up to 16 ranges: 2% above the best
+// on average, 16% at worst (56 x 10512 x 1280 14.0 us, 11.8 on four blocks). us, N x K:
+//   37 rows, 4096 x 14336: one block, no split 31.7; two, two ranges 27.2; four, four 26.2
+//   64 rows, same: 39.9, 30.6, 29.3;   1 row: 19.5, 22 (two), and 21.2 one in two ranges
+//   64 rows, 512 x 8192: one block 21.0, in eight ranges 9.5
+// Waves and chunks of each are the best of three for it (16 rows on one block: 4 waves
+// of two chunks 8.7 at 4096 x 4096, 8 waves 9.1; 64 rows on two: 8 waves 31.4, 4 33.6 at 14336
+// x 4096).
+void plan_small_linear(int64_t M, int64_t N, int64_t K, LinearPlan* p) {
+  const int xl = M == 1 ? 0 : M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : M <= 48 ? 6 : 8;
+  const int64_t rows = xl == 0 ? 1 : 8 * xl, blocks = N / 16, chunks = whole_k(K) / 64;
+  double best = -1;
+  for (int nb = 1; nb <= (xl <= 2 ? 2 : 4); nb *= 2) {
+    LinearSmall v;
+    v.xl = xl;
+    v.blocks = nb;
+    v.waves = nb == 1 && (xl == 2 || xl == 4 || xl == 8) ? 4 : 8;
+    v.s = nb == 1 && xl <= 4 ? 2 : 1;
+    const int64_t tiles = (blocks + nb - 1) / nb * ((M + rows - 1) / rows);
+    const double byte_us = 32.0 * nb / 55e3 + 2.0 * (double)std::min(M, rows) / 100e3;
+    for (int64_t ks = 1; ks <= 16; ++ks) {
+      if (ks > 1 && (tiles * ks > 1024 || chunks < v.waves * ks)) break;
+      const int64_t steps = (chunks + v.waves * ks - 1) / (v.waves * ks) * v.waves * 64;
+      const double fill = (double)(tiles * ks) / 256, rounds = fill <= 3 ? std::ceil(fill) : fill + 0.5;
+      const double us = 2.8 + rounds * (double)steps * byte_us + (ks > 1 ? 0.7 + 0.4 * (double)ks : 0);
+      if (best >= 0 && us >= best) continue;
+      best = us;
+      p->variant = v;
+      p->ks = ks;
+      p->tiles = tiles;
+    }
+  }
+  if (p->ks > 1) p->bytes = kCounterBytes + p->tiles * p->ks * ((rows + 15) / 16 * p->variant.blocks * 1024);
+}
+
+// Up to 64 rows, and above where no tile fits into [M][N], the small kernel; otherwise a
+// tile by the gated product's times (N columns here take as long as its F gate and F up
+// ones, 2 F = N).
 int plan_linear(int dtype, int64_t M, int64_t N, int64_t K, LinearPlan* p) {
   const int r = check_linear(dtype, M, N, K);
   if (r) return r;
   p->small = M <= 64;
   if (!p->small) p->small = choose_tile_us(kGatedTimes, M, N, 2 * whole_k(K), true, &p->tile) < 0;
   if (p->small) {
-    LinearSmall& v = p->variant;
-    const int64_t blocks = N / 16;
-    v.xl = M == 1 ? 0 : M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : M <= 48 ? 6 : 8;
-    v.s = v.xl <= 4 ? 2 : 1;
-    v.blocks = blocks >= 512 ? 2 : 1;
-    v.waves = 8;
-    const int64_t rows = v.xl == 0 ? 1 : 8 * v.xl;
-    p->tiles = ((blocks + v.blocks - 1) / v.blocks) * ((M + rows - 1) / rows);
-    if (p->tiles >= (int64_t)1 << 22) return GP_ESHAPE;   // threads of a grid
-    p->ks = split_small((double)whole_k(K) / 64 / v.waves, v.xl <= 2 ? 0.5 : v.xl == 4 ? 0.35 : 0.65, p->tiles);
-    if (p->ks > 1) p->bytes = kCounterBytes + p->tiles * p->ks * ((rows + 15) / 16 * v.blocks * 1024);
+    plan_small_linear(M, N, K, p);
+    if (p->tiles * p->ks >= (int64_t)1 << 22) return GP_ESHAPE;   // threads of a grid
   } else {
     p->bytes = plan_workspace(p->tile, M, N);
   }

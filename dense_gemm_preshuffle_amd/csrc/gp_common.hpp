@@ -314,6 +314,44 @@ __device__ __forceinline__ float erf_as7126(float x) {
   return copysignf(1.f - poly * __expf(-ax * ax), x);
 }
 
+// Sums over a wave, in the same order on every run and the same in every lane: within
+// rows of 16 lanes by data-parallel moves (pairs, quads, halves, the row), the four rows'
+// through scalar registers. A move takes 8 cycles or so, an exchange through LDS
+// (__shfl_xor) over 60.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+constexpr int kDppSwapPairs = 0xB1, kDppSwapQuadHalves = 0x4E, kDppHalfRowMirror = 0x141, kDppRowMirror = 0x140;
+__device__ __forceinline__ float wave_sum(float v) {
+  auto add = [&](auto c) GP_INLINE {
+    v += __builtin_bit_cast(float, dpp<decltype(c)::value>(__builtin_bit_cast(uint32_t, v)));
+  };
+  add(std::integral_constant<int, kDppSwapPairs>{});
+  add(std::integral_constant<int, kDppSwapQuadHalves>{});
+  add(std::integral_constant<int, kDppHalfRowMirror>{});
+  add(std::integral_constant<int, kDppRowMirror>{});
+  auto row = [&](int r) GP_INLINE {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 16 * r));
+  };
+  return (row(0) + row(1)) + (row(2) + row(3));
+}
+__device__ __forceinline__ double wave_sum64(double v) {
+  auto both = [](double x, auto&& f) GP_INLINE -> double {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, (uint64_t)f((uint32_t)(u >> 32)) << 32 | f((uint32_t)u));
+  };
+  auto add = [&](auto c) GP_INLINE { v += both(v, [](uint32_t u) GP_INLINE { return dpp<decltype(c)::value>(u); }); };
+  add(std::integral_constant<int, kDppSwapPairs>{});
+  add(std::integral_constant<int, kDppSwapQuadHalves>{});
+  add(std::integral_constant<int, kDppHalfRowMirror>{});
+  add(std::integral_constant<int, kDppRowMirror>{});
+  auto row = [&](int r) GP_INLINE {
+    return both(v, [r](uint32_t u) GP_INLINE { return (uint32_t)__builtin_amdgcn_readlane((int)u, 16 * r); });
+  };
+  return (row(0) + row(1)) + (row(2) + row(3));
+}
+
 // The value of x, hidden from the optimizer: every quantity derived from the
 // result is computed where this call stands. Used at the start of epilogues
 // so that their per-lane addresses are not hoisted above the K loop, where

@@ -35,11 +35,6 @@ __device__ __forceinline__ double shfl_xor64(double v, int o) {
   const uint32_t lo = __shfl_xor((uint32_t)u, o, 64), hi = __shfl_xor((uint32_t)(u >> 32), o, 64);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += shfl_xor64(v, o);
-  return v;
-}
 
 constexpr uint32_t kMaxExperts = 512;
 

@@ -15,10 +15,10 @@ namespace {
 
 constexpr int64_t kMaxGates = 256, kMaxRow = 16384;
 
-// Waves of a row and 8-column pieces of a lane, the workgroups, and the rows of each.
+// Waves of a row and 8-column pieces of a lane, and the workgroups.
 struct NormPlan {
   int wpr = 1, c = 1;
-  int64_t wg_rows = 1, wgs = 1, per_gate = 1;
+  int64_t wgs = 1, per_gate = 1;   // per_gate: backward, of one gate row
 };
 
 bool norm_kind(int k) { return k >= GP_NORM_NONE && k <= GP_NORM_LAYER; }
@@ -30,40 +30,49 @@ int check_norm(int dtype, int64_t M, int64_t H, int64_t gates) {
   return GP_OK;
 }
 
-void row_shape(int64_t H, NormPlan* p) {
-  p->wpr = H <= 1024 ? 1 : H <= 2048 ? 4 : H <= 4096 ? 8 : 16;
-  p->c = H <= 512 ? 1 : H <= 1024 ? 2 : H <= 8192 ? 1 : 2;
+// One wave a row as long as it holds the row in 16 columns a lane (and there are rows
+// for all waves), then the fewest waves that hold it in 8, and 16 from 4096 on. Measured us
+// (residual add and RMS norm, graph of calls): 1 x 4096 on 8 waves of one piece 3.2, 4 of two
+// 4.5, 16 of one 3.7; 1500 x 1024 on one wave of two 5.6, four of one 5.4, 16384 x 1024 26.1
+// and 28.2; 3000 x 5120 on 8 of two 27.8, 16 of one 26.8, but with layer norms on both sides 37.8
+// and 39.5; 4096 x 16384 on 16 of two 111, 8 of four 116.
+void row_shape(int64_t M, int64_t H, NormPlan* p) {
+  if (H <= 512) p->wpr = 1, p->c = 1;
+  else if (H <= 1024 && M >= 1024) p->wpr = 1, p->c = 2;
+  else if (H <= 2048) p->wpr = 4, p->c = 1;
+  else if (H <= 4096) p->wpr = 8, p->c = 1;
+  else if (H <= 8192) p->wpr = 8, p->c = 2;
+  else p->wpr = 16, p->c = 2;
 }
+
+// The workgroups that the CUs hold at once (by their registers), or one per row (four
+// rows of one wave each).
+int64_t resident(const NormPlan& p) { return 256 * (p.wpr * p.c >= 16 ? 1 : p.wpr == 8 || p.c == 2 ? 2 : 4); }
 
 NormPlan plan_norm(int64_t M, int64_t H) {
   NormPlan p;
-  row_shape(H, &p);
-  const int64_t rpw = norm_threads(p.wpr) / (64 * p.wpr), most = 256 * (2048 / norm_threads(p.wpr));
-  const int64_t rows = (M + most - 1) / most;
-  p.wg_rows = (rows + rpw - 1) / rpw * rpw;
-  p.wgs = (M + p.wg_rows - 1) / p.wg_rows;
+  row_shape(M, H, &p);
+  const int64_t rpw = norm_threads(p.wpr) / (64 * p.wpr);
+  p.wgs = std::min(resident(p), (M + rpw - 1) / rpw);
   return p;
 }
 
 NormPlan plan_norm_grad(int64_t M, int64_t H, int64_t gates) {
   NormPlan p;
-  row_shape(H, &p);
-  const int64_t rpw = norm_grad_threads(p.wpr) / (64 * p.wpr), most = 256 * (1024 / norm_grad_threads(p.wpr));
-  const int64_t G = std::max<int64_t>(gates, 1), of_gate = M / G, want = std::max<int64_t>(most / G, 1);
-  const int64_t rows = (of_gate + want - 1) / want;
-  p.wg_rows = (rows + rpw - 1) / rpw * rpw;
-  p.per_gate = (of_gate + p.wg_rows - 1) / p.wg_rows;
+  row_shape(M, H, &p);
+  const int64_t rpw = norm_threads(p.wpr) / (64 * p.wpr), G = std::max<int64_t>(gates, 1), of_gate = M / G;
+  p.per_gate = std::min(std::max<int64_t>(resident(p) / G, 1), (of_gate + rpw - 1) / rpw);
   p.wgs = G * p.per_gate;
   return p;
 }
 
-#define GP_NORM_SHAPES(X) X(1, 1) X(1, 2) X(4, 1) X(8, 1) X(16, 1) X(16, 2)
+#define GP_NORM_SHAPES(X) X(1, 1) X(1, 2) X(4, 1) X(8, 1) X(8, 2) X(16, 2)
 
 template <int DT>
 hipError_t launch_norm(const NormPlan& p, const NormArgs& a, hipStream_t s) {
 #define GP_NORM_CASE(W, C)                                                                              \
   if (p.wpr == W && p.c == C) {                                                                         \
-    hipLaunchKernelGGL((norm_kernel<DT, W, C>), dim3((uint32_t)p.wgs), dim3(norm_threads(W)), 0, s, a); \
+    hipLaunchKernelGGL((norm_kernel<DT, W, C, (W * C < 32)>), dim3((uint32_t)p.wgs), dim3(norm_threads(W)), 0, s, a); \
     return hipGetLastError();                                                                           \
   }
   GP_NORM_SHAPES(GP_NORM_CASE)
@@ -71,12 +80,12 @@ hipError_t launch_norm(const NormPlan& p, const NormArgs& a, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-template <int DT>
+template <int DT, bool IN>
 hipError_t launch_norm_grad(const NormPlan& p, const NormGradArgs& a, hipStream_t s) {
-#define GP_NORM_CASE(W, C)                                                                                        \
-  if (p.wpr == W && p.c == C) {                                                                                   \
-    hipLaunchKernelGGL((norm_grad_kernel<DT, W, C>), dim3((uint32_t)p.wgs), dim3(norm_grad_threads(W)), 0, s, a); \
-    return hipGetLastError();                                                                                     \
+#define GP_NORM_CASE(W, C)                                                                                       \
+  if (p.wpr == W && p.c == C) {                                                                                  \
+    hipLaunchKernelGGL((norm_grad_kernel<DT, W, C, IN>), dim3((uint32_t)p.wgs), dim3(norm_threads(W)), 0, s, a); \
+    return hipGetLastError();                                                                                    \
   }
   GP_NORM_SHAPES(GP_NORM_CASE)
 #undef GP_NORM_CASE
@@ -118,7 +127,6 @@ int gemm_norm(int dtype, const void* x, const void* residual, float scale, int n
   a.eps = eps;
   a.H = (uint32_t)H;
   a.gate_rows = (uint32_t)(gates ? M / gates : M);
-  a.wg_rows = (uint32_t)p.wg_rows;
   a.M = (uint64_t)M;
   a.kin = norm_in;
   a.kout = norm_out;
@@ -173,14 +181,15 @@ int gemm_norm_backward(int dtype, const void* dy, const void* dr, const void* x,
   a.eps = eps;
   a.H = (uint32_t)H;
   a.gate_rows = (uint32_t)(gates ? M / gates : M);
-  a.wg_rows = (uint32_t)p.wg_rows;
   a.wgs_per_gate = (uint32_t)p.per_gate;
   a.sums = (dw_out ? 1u : 0u) | (db_out ? 2u : 0u) | (dw_in || dgate ? 4u : 0u) | (db_in || (dgate && b_in) ? 8u : 0u);
   a.kin = norm_in;
   a.kout = norm_out;
   forget_hip_error();
   const hipStream_t s = (hipStream_t)stream;
-  e = report_hip(dtype == GP_BF16 ? launch_norm_grad<DT_BF16>(p, a, s) : launch_norm_grad<DT_F16>(p, a, s), "kernel launch");
+  auto* launch = in || gate ? (dtype == GP_BF16 ? launch_norm_grad<DT_BF16, true> : launch_norm_grad<DT_F16, true>)
+                            : (dtype == GP_BF16 ? launch_norm_grad<DT_BF16, false> : launch_norm_grad<DT_F16, false>);
+  e = report_hip(launch(p, a, s), "kernel launch");
   if (e || !sums) return e;
   NormSumsArgs t;
   t.part = (const float*)workspace;
@@ -196,7 +205,7 @@ int gemm_norm_backward(int dtype, const void* dy, const void* dr, const void* x,
   t.parts = (uint32_t)p.wgs;
   t.wgs_per_gate = (uint32_t)p.per_gate;
   forget_hip_error();
-  hipLaunchKernelGGL(norm_sums_kernel, dim3((uint32_t)((H + 31) / 32), (uint32_t)(4 + gates)), dim3(1024), 0, s, t);
+  hipLaunchKernelGGL(norm_sums_kernel, dim3((uint32_t)((H + 63) / 64), (uint32_t)(4 + gates)), dim3(1024), 0, s, t);
   return report_hip(hipGetLastError(), "kernel launch");
 }
 

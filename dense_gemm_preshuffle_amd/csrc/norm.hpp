@@ -23,7 +23,7 @@ struct NormArgs {
   const float *w_in, *b_in, *gate, *w_out, *b_out;   // null: ones, zeros; gate [G][H]
   char *r, *y;                              // [M][H]; either null: not stored
   float scale, eps;
-  uint32_t H, gate_rows, wg_rows;           // rows per gate row, rows per workgroup
+  uint32_t H, gate_rows;                    // gate_rows: rows per gate row
   uint64_t M;
   int kin, kout;                            // Norm
 };
@@ -51,33 +51,30 @@ __device__ __forceinline__ void load8(const float* p, uint32_t col, bool on, flo
   }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-
 // Sums of N values over the WPR waves of a row, in the same order on every run. Of two
-// halves of `red` consecutive sums take turns, so that one barrier each is enough:
-// a half is written again only after the barrier of the sum between.
-template <int WPR, int N>
+// halves of `red` consecutive sums take turns, so that one barrier each is enough: a half
+// is written again only after the barrier of the sum between.
+template <int WPR>
 struct RowSum {
-  float* red;   // LDS [2][16][N]
+  float (*red)[2][16];   // LDS [2][2][16]
   int wave, turn;
+  template <int N>
   __device__ __forceinline__ void operator()(float (&v)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
     if constexpr (WPR > 1) {
-      float* half = red + turn * (16 * N);
+      float(*half)[16] = red[turn];
       turn ^= 1;
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if ((threadIdx.x & 63) == 0) half[wave * N + i] = v[i];
+        if ((threadIdx.x & 63) == 0) half[i][wave] = v[i];
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        v[i] = half[i];
-        for (int w = 1; w < WPR; ++w) v[i] += half[w * N + i];
+        v4f t = *(const v4f*)&half[i][0];
+#pragma unroll
+        for (int w = 4; w < WPR; w += 4) t += *(const v4f*)&half[i][w];
+        v[i] = (t[0] + t[1]) + (t[2] + t[3]);
       }
     }
   }
@@ -85,30 +82,42 @@ struct RowSum {
 
 constexpr int norm_threads(int wpr) { return wpr < 4 ? 256 : 64 * wpr; }
 
-// Normalises the row v in place; the reciprocal root.
+// Normalises the row v in place; the reciprocal root. What lanes past the row hold is
+// kept out of the sums (a piece at a time: a select per element is a tenth of the
+// arithmetic). The root is the hardware's, 1 ulp, of a value that is scaled up where it
+// would take it for zero; the mean is the quotient rounded once, so that a row of one
+// value leaves zeros.
 template <int WPR, int C>
-__device__ __forceinline__ float normalize_row(int kind, float (&v)[C][8], const bool (&on)[C], float h, float eps,
-                                               RowSum<WPR, 1>& sum) {
+__device__ __forceinline__ float normalize_row(int kind, float (&v)[C][8], const bool (&on)[C], uint32_t H, float inv_h,
+                                               float eps, RowSum<WPR>& sum) {
   float s[1] = {0.f};
   if (kind == NORM_LAYER) {
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+      float t = v[c][0];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += v[c][i];
+      for (int i = 1; i < 8; ++i) t += v[c][i];
+      s[0] += on[c] ? t : 0.f;
+    }
     sum(s);
-    const float mean = s[0] / h;   // exact for a row of one value, which then leaves zeros
+    float mean = s[0] * inv_h;
+    mean = fmaf(fmaf(-mean, (float)H, s[0]), inv_h, mean);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = on[c] ? v[c][i] - mean : 0.f;
+      for (int i = 0; i < 8; ++i) v[c][i] -= mean;
     s[0] = 0.f;
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    float t = v[c][0] * v[c][0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[0] = fmaf(v[c][i], v[c][i], s[0]);
+    for (int i = 1; i < 8; ++i) t = fmaf(v[c][i], v[c][i], t);
+    s[0] += on[c] ? t : 0.f;
+  }
   sum(s);
-  const float rs = 1.f / sqrtf(s[0] / h + eps);
+  const float mean2 = fmaf(s[0], inv_h, eps);
+  const float rs = mean2 < 0x1p-100f ? 0x1p32f * __builtin_amdgcn_rsqf(0x1p64f * mean2) : __builtin_amdgcn_rsqf(mean2);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -116,15 +125,14 @@ __device__ __forceinline__ float normalize_row(int kind, float (&v)[C][8], const
   return rs;
 }
 
-template <int DT, int WPR, int C>
+template <int DT, int WPR, int C, bool KEEP>
 __global__ __launch_bounds__(norm_threads(WPR)) void norm_kernel(NormArgs p) {
   constexpr int T = 64 * WPR, RPW = norm_threads(WPR) / T;   // threads of a row, rows at a time
-  constexpr bool KEEP = WPR * C < 32;   // parameters in registers (16 waves have 128 a lane)
-  __shared__ float red[2 * 16];
+  __shared__ __attribute__((aligned(16))) float red[2][2][16];
   const int t = threadIdx.x % T;
   const uint32_t H = p.H;
-  const float h = (float)H;
-  RowSum<WPR, 1> sum{red, (int)threadIdx.x >> 6, 0};
+  const float inv_h = 1.f / (float)H;
+  RowSum<WPR> sum{red, (int)threadIdx.x >> 6, 0};
   uint32_t col[C];
   bool on[C];
   float a[KEEP ? C : 1][8], b[KEEP ? C : 1][8], wo[KEEP ? C : 1][8], bo[KEEP ? C : 1][8];
@@ -147,20 +155,19 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_kernel(NormArgs p) {
     on[c] = col[c] < H;
     if constexpr (KEEP) load_out(c, wo[c], bo[c]);
   }
-  const uint64_t m0 = (uint64_t)blockIdx.x * p.wg_rows, m1 = min(m0 + p.wg_rows, p.M);
+  const uint64_t m0 = (uint64_t)blockIdx.x * RPW, m1 = p.M, step = (uint64_t)gridDim.x * RPW;
+  const float scale = p.res ? p.scale : 0.f;   // (without a residual r holds zeros)
   uint64_t gate = 0, gate_end = 0;   // the gate row, and the row at which it changes
   v4i xv[C], rv[C];
-  auto load = [&](uint64_t m) GP_INLINE {
+  auto load = [&](const char* from, uint64_t m, v4i (&v)[C]) GP_INLINE {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const size_t off = (m * H + col[c]) * 2;
-      xv[c] = on[c] && m < m1 ? *(const v4i*)(p.x + off) : v4i{0, 0, 0, 0};
-      rv[c] = p.res && on[c] && m < m1 ? *(const v4i*)(p.res + off) : v4i{0, 0, 0, 0};
-    }
+    for (int c = 0; c < C; ++c)
+      v[c] = from && on[c] && m < m1 ? *(const v4i*)(from + (m * H + col[c]) * 2) : v4i{0, 0, 0, 0};
   };
   uint64_t m = m0 + threadIdx.x / T;
-  load(m);
-  for (; m < m1; m += RPW) {
+  load(p.x, m, xv);
+  if constexpr (KEEP) load(p.res, m, rv);
+  for (; m < m1; m += step) {
     if (m >= gate_end) {
       gate = m / p.gate_rows;
       gate_end = (gate + 1) * p.gate_rows;
@@ -169,27 +176,32 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_kernel(NormArgs p) {
         for (int c = 0; c < C; ++c) load_in(gate, c, a[c], b[c]);
     }
     float v[C][8], r[C][8];
+    if constexpr (!KEEP) load(p.res, m, rv);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       widen8<DT>(xv[c], v[c]);
-      widen8<DT>(rv[c], r[c]);
+      if constexpr (KEEP) widen8<DT>(rv[c], r[c]);
     }
-    load(m + RPW);   // the next row's, while this one is reduced
-    if (p.kin != NORM_NONE) normalize_row<WPR, C>(p.kin, v, on, h, p.eps, sum);
+    load(p.x, m + step, xv);   // the next row's, while this one is reduced
+    if constexpr (KEEP) load(p.res, m + step, rv);
+    if (p.kin != NORM_NONE) normalize_row<WPR, C>(p.kin, v, on, H, inv_h, p.eps, sum);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       constexpr auto at = [](int k) GP_INLINE { return KEEP ? k : 0; };
-      if constexpr (!KEEP) load_in(gate, c, a[0], b[0]);
+      if constexpr (!KEEP) {
+        widen8<DT>(rv[c], r[c]);
+        load_in(gate, c, a[0], b[0]);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        r[c][i] = on[c] ? fmaf(v[c][i], a[at(c)][i], b[at(c)][i]) + (p.res ? p.scale * r[c][i] : 0.f) : 0.f;
+        r[c][i] = fmaf(scale, r[c][i], fmaf(v[c][i], a[at(c)][i], b[at(c)][i]));
     }
     if (p.r)
 #pragma unroll
       for (int c = 0; c < C; ++c)
         if (on[c]) *(v4i*)(p.r + (m * H + col[c]) * 2) = narrow8<DT>(r[c]);
     if (p.y) {
-      normalize_row<WPR, C>(p.kout, r, on, h, p.eps, sum);
+      normalize_row<WPR, C>(p.kout, r, on, H, inv_h, p.eps, sum);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         constexpr auto at = [](int k) GP_INLINE { return KEEP ? k : 0; };
@@ -220,125 +232,150 @@ struct NormGradArgs {
   char *dx, *dres;                          // either null: not stored
   float* part;                              // [workgroups][4][H]: dy n, dy, t n1, t
   float scale, eps;
-  uint32_t H, gate_rows, wg_rows, wgs_per_gate;
+  uint32_t H, gate_rows, wgs_per_gate;
   uint32_t sums;                            // bit i: sum i is wanted
   int kin, kout;
 };
 
 template <int WPR, int C>
 __device__ __forceinline__ void normalize_grad(int kind, float (&d)[C][8], const float (&n)[C][8], const bool (&on)[C],
-                                               float rs, float inv_h, RowSum<WPR, 2>& sum) {
+                                               float rs, float inv_h, RowSum<WPR>& sum) {
   float s[2] = {0.f, 0.f};
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    float t = 0.f, u = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      s[0] = fmaf(d[c][i], n[c][i], s[0]);
-      s[1] += d[c][i];
+      t = fmaf(d[c][i], n[c][i], t);
+      u += d[c][i];
     }
+    s[0] += on[c] ? t : 0.f;
+    s[1] += on[c] ? u : 0.f;
+  }
   sum(s);
-  const float along = s[0] * inv_h, mean = kind == NORM_LAYER ? s[1] * inv_h : 0.f;
+  const float along = -rs * (s[0] * inv_h), shift = kind == NORM_LAYER ? -rs * (s[1] * inv_h) : 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d[c][i] = on[c] ? rs * (d[c][i] - mean - n[c][i] * along) : 0.f;
+    for (int i = 0; i < 8; ++i) d[c][i] = fmaf(n[c][i], along, fmaf(d[c][i], rs, shift));
 }
 
-constexpr int norm_grad_threads(int wpr) { return wpr < 4 ? 256 : 64 * wpr; }
-// sums 2 and 3 in LDS: 16 waves have 128 registers a lane
+// sums 2 and 3 in LDS, parameters read again for each row: 16 waves have 128 registers a lane
 constexpr bool norm_grad_lds(int wpr, int c) { return wpr * c >= 32; }
 
-template <int DT, int WPR, int C>
-__global__ __launch_bounds__(norm_grad_threads(WPR)) void norm_grad_kernel(NormGradArgs p) {
-  constexpr int TH = norm_grad_threads(WPR), T = 64 * WPR, RPW = TH / T;
-  constexpr bool LDS = norm_grad_lds(WPR, C);
-  constexpr int NREG = LDS ? 2 : 4;
-  __shared__ float red1[2 * 16], red2[2 * 16 * 2];
-  __shared__ __attribute__((aligned(16))) v4f far[LDS ? 2 * C * T * 2 : 1];
+template <int DT, int WPR, int C, bool IN>
+__global__ __launch_bounds__(norm_threads(WPR)) void norm_grad_kernel(NormGradArgs p) {
+  constexpr int TH = norm_threads(WPR), T = 64 * WPR, RPW = TH / T;
+  constexpr bool LDS = norm_grad_lds(WPR, C), KEEP = !LDS;
+  constexpr int NSUM = IN ? 4 : 2, NREG = LDS && IN ? 2 : NSUM, K = KEEP ? C : 1;
+  __shared__ __attribute__((aligned(16))) float red[2][2][16];
+  __shared__ __attribute__((aligned(16))) v4f far[NREG < NSUM ? 2 * C * T * 2 : 1];
   __shared__ float fold[RPW > 1 ? T * 8 : 1];
   const int t = threadIdx.x % T, grp = threadIdx.x / T;
   const uint32_t H = p.H;
-  const float h = (float)H, inv_h = 1.f / h;
-  RowSum<WPR, 1> sum1{red1, (int)threadIdx.x >> 6, 0};
-  RowSum<WPR, 2> sum2{red2, (int)threadIdx.x >> 6, 0};
+  const float inv_h = 1.f / (float)H;
+  RowSum<WPR> sum{red, (int)threadIdx.x >> 6, 0};
   const uint64_t g = blockIdx.x / p.wgs_per_gate;
-  const uint64_t m0 = g * p.gate_rows + (uint64_t)(blockIdx.x % p.wgs_per_gate) * p.wg_rows;
-  const uint64_t m1 = min(m0 + p.wg_rows, (g + 1) * (uint64_t)p.gate_rows);
+  const uint64_t m1 = (g + 1) * (uint64_t)p.gate_rows, step = (uint64_t)p.wgs_per_gate * RPW;
   uint32_t col[C];
   bool on[C];
-  float acc[NREG][C][8];
+  float acc[NREG][C][8], wo[K][8], wi[K][8];
+  auto load_in = [&](int c, float (&w)[8]) GP_INLINE {   // gate * w_in
+    float gv[8];
+    load8(p.w_in, col[c], on[c], 1.f, w);
+    load8(p.gate ? p.gate + g * H : nullptr, col[c], on[c], 1.f, gv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] *= gv[i];
+  };
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     col[c] = (c * T + t) * 8u;
     on[c] = col[c] < H;
+    if constexpr (KEEP) {
+      load8(p.w_out, col[c], on[c], 1.f, wo[c]);
+      if constexpr (IN) load_in(c, wi[c]);
+    }
 #pragma unroll
     for (int k = 0; k < NREG; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[k][c][i] = 0.f;
   }
   auto far_at = [&](int k, int c, int h) GP_INLINE -> v4f& { return far[(((k - 2) * C + c) * 2 + h) * T + t]; };
-  if constexpr (LDS)
+  if constexpr (NREG < NSUM)
 #pragma unroll
     for (int k = 2; k < 4; ++k)
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int h = 0; h < 2; ++h) far_at(k, c, h) = v4f{0.f, 0.f, 0.f, 0.f};
-  auto add = [&](auto k_c, int c, const float (&v)[8]) GP_INLINE {
+  // adds a v (or a v w)
+  auto add = [&](auto k_c, int c, const float (&v)[8], const float (&w)[8], bool one) GP_INLINE {
     constexpr int k = decltype(k_c)::value;
     if constexpr (k < NREG) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[k][c][i] += v[i];
+      for (int i = 0; i < 8; ++i) acc[k][c][i] = one ? acc[k][c][i] + v[i] : fmaf(v[i], w[i], acc[k][c][i]);
     } else {
-      far_at(k, c, 0) += v4f{v[0], v[1], v[2], v[3]};
-      far_at(k, c, 1) += v4f{v[4], v[5], v[6], v[7]};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v4f f = far_at(k, c, h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = one ? f[i] + v[4 * h + i] : fmaf(v[4 * h + i], w[4 * h + i], f[i]);
+        far_at(k, c, h) = f;
+      }
     }
   };
-  for (uint64_t m = m0 + grp; m < m1; m += RPW) {
+  v4i xv[C], rv[C], dv[C], sv[C];
+  auto load = [&](const char* from, uint64_t m, v4i (&v)[C]) GP_INLINE {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      v[c] = from && on[c] && m < m1 ? *(const v4i*)(from + (m * H + col[c]) * 2) : v4i{0, 0, 0, 0};
+  };
+  auto load_row = [&](uint64_t m) GP_INLINE {
+    load(p.r, m, rv);
+    load(p.dy, m, dv);
+    if constexpr (KEEP) {
+      load(p.dr, m, sv);
+      if constexpr (IN) load(p.x, m, xv);
+    }
+  };
+  uint64_t m = g * p.gate_rows + (uint64_t)(blockIdx.x % p.wgs_per_gate) * RPW + grp;
+  if constexpr (KEEP) load_row(m);
+  for (; m < m1; m += step) {
     float d[C][8], n[C][8];
-    v4i xv[C], rv[C], dv[C];
+    v4i s[C], x[C];   // of dr and x, as they were loaded
+    if constexpr (!KEEP) load_row(m);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const size_t off = (m * H + col[c]) * 2;
-      const v4i z = v4i{0, 0, 0, 0};
-      rv[c] = p.dy && on[c] ? *(const v4i*)(p.r + off) : z;
-      dv[c] = p.dy && on[c] ? *(const v4i*)(p.dy + off) : z;
-      if constexpr (!LDS) xv[c] = p.x && on[c] ? *(const v4i*)(p.x + off) : z;
+      widen8<DT>(rv[c], n[c]);
+      widen8<DT>(dv[c], d[c]);
+      if constexpr (KEEP) {
+        s[c] = sv[c];
+        if constexpr (IN) x[c] = xv[c];
+      }
     }
-    float rs = 0.f;
+    if constexpr (KEEP) load_row(m + step);   // the next row's, while this one is reduced
     if (p.dy) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) widen8<DT>(rv[c], n[c]);
-      rs = normalize_row<WPR, C>(p.kout, n, on, h, p.eps, sum1);
+      const float rs = normalize_row<WPR, C>(p.kout, n, on, H, inv_h, p.eps, sum);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        float w[8], v[8];
-        widen8<DT>(dv[c], d[c]);
-        if (p.sums & 2u) add(std::integral_constant<int, 1>{}, c, d[c]);
-        if (p.sums & 1u) {
+        if (p.sums & 2u) add(std::integral_constant<int, 1>{}, c, d[c], d[c], true);
+        if (p.sums & 1u) add(std::integral_constant<int, 0>{}, c, d[c], n[c], false);
+        if constexpr (!KEEP) load8(p.w_out, col[c], on[c], 1.f, wo[0]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = d[c][i] * n[c][i];
-          add(std::integral_constant<int, 0>{}, c, v);
-        }
-        load8(p.w_out, col[c], on[c], 1.f, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[c][i] *= w[i];
+        for (int i = 0; i < 8; ++i) d[c][i] *= wo[KEEP ? c : 0][i];
       }
-      normalize_grad<WPR, C>(p.kout, d, n, on, rs, inv_h, sum2);
-    } else {
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[c][i] = 0.f;
+      normalize_grad<WPR, C>(p.kout, d, n, on, rs, inv_h, sum);
     }
-    if (p.dr)
+    if (p.dr) {
+      if constexpr (!KEEP) load(p.dr, m, s);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         float v[8];
-        widen8<DT>(on[c] ? *(const v4i*)(p.dr + (m * H + col[c]) * 2) : v4i{0, 0, 0, 0}, v);
+        widen8<DT>(s[c], v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[c][i] += v[i];
       }
+    }
     if (p.dres)
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -347,42 +384,36 @@ __global__ __launch_bounds__(norm_grad_threads(WPR)) void norm_grad_kernel(NormG
         for (int i = 0; i < 8; ++i) v[i] = p.scale * d[c][i];
         if (on[c]) *(v4i*)(p.dres + (m * H + col[c]) * 2) = narrow8<DT>(v);
       }
-    if (!p.dx && !(p.sums & 12u)) continue;
-    float rs1 = 0.f;
-    if (p.x) {
+    if constexpr (IN) {
+      float rs1 = 0.f;
+      if (p.x) {
+        if constexpr (!KEEP) load(p.x, m, x);
+#pragma unroll
+        for (int c = 0; c < C; ++c) widen8<DT>(x[c], n[c]);
+        if (p.kin != NORM_NONE) rs1 = normalize_row<WPR, C>(p.kin, n, on, H, inv_h, p.eps, sum);
+      }
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if constexpr (LDS) xv[c] = on[c] ? *(const v4i*)(p.x + (m * H + col[c]) * 2) : v4i{0, 0, 0, 0};
-        widen8<DT>(xv[c], n[c]);
+        if (p.sums & 8u) add(std::integral_constant<int, 3>{}, c, d[c], d[c], true);
+        if (p.sums & 4u) add(std::integral_constant<int, 2>{}, c, d[c], n[c], false);
       }
-      if (p.kin != NORM_NONE) rs1 = normalize_row<WPR, C>(p.kin, n, on, h, p.eps, sum1);
-    }
+      if (p.dx) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if (p.sums & 8u) add(std::integral_constant<int, 3>{}, c, d[c]);
-      if (p.sums & 4u) {
-        float v[8];
+        for (int c = 0; c < C; ++c) {
+          if constexpr (!KEEP) load_in(c, wi[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = d[c][i] * n[c][i];
-        add(std::integral_constant<int, 2>{}, c, v);
+          for (int i = 0; i < 8; ++i) d[c][i] *= wi[KEEP ? c : 0][i];
+        }
+        if (p.kin != NORM_NONE) normalize_grad<WPR, C>(p.kin, d, n, on, rs1, inv_h, sum);
       }
     }
-    if (!p.dx) continue;
+    if (p.dx)
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      float w[8], gv[8];
-      load8(p.w_in, col[c], on[c], 1.f, w);
-      load8(p.gate ? p.gate + g * H : nullptr, col[c], on[c], 1.f, gv);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[c][i] *= gv[i] * w[i];
-    }
-    if (p.kin != NORM_NONE) normalize_grad<WPR, C>(p.kin, d, n, on, rs1, inv_h, sum2);
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (on[c]) *(v4i*)(p.dx + (m * H + col[c]) * 2) = narrow8<DT>(d[c]);
+      for (int c = 0; c < C; ++c)
+        if (on[c]) *(v4i*)(p.dx + (m * H + col[c]) * 2) = narrow8<DT>(d[c]);
   }
   // the workgroup's sums; where it ran several rows at a time, theirs in order
-  static_for<0, 4>([&](auto k_c) GP_INLINE {
+  static_for<0, NSUM>([&](auto k_c) GP_INLINE {
     constexpr int k = decltype(k_c)::value;
     if (!(p.sums >> k & 1u)) return;
 #pragma unroll
@@ -418,43 +449,47 @@ __global__ __launch_bounds__(norm_grad_threads(WPR)) void norm_grad_kernel(NormG
   });
 }
 
-// Sums of the workgroups' parts: 32 columns a workgroup (blockIdx.x), 32 of the
-// parts at a time, then those in order. blockIdx.y: 0 dw_out, 1 db_out, 2 dw_in, 3
+// Sums of the workgroups' parts: 64 columns a workgroup (blockIdx.x), four a lane, 64 of
+// the parts at a time, then those in order. blockIdx.y: 0 dw_out, 1 db_out, 2 dw_in, 3
 // db_in, 4 + g the gradient of gate row g.
 struct NormSumsArgs {
   const float *part, *gate, *w_in, *b_in;
   float *dw_out, *db_out, *dw_in, *db_in, *dgate;   // null: not wanted
   uint32_t H, parts, wgs_per_gate;
 };
-__global__ __launch_bounds__(1024) inline void norm_sums_kernel(NormSumsArgs p) {
-  __shared__ float red[2][32][33];
-  const uint32_t kind = blockIdx.y, lane = threadIdx.x & 31, row = threadIdx.x >> 5, H = p.H;
-  const uint32_t c = blockIdx.x * 32u + lane;
+static __global__ __launch_bounds__(1024) void norm_sums_kernel(NormSumsArgs p) {
+  __shared__ __attribute__((aligned(16))) v4f red[2][64][16];
+  const uint32_t kind = blockIdx.y, lane = threadIdx.x & 15, row = threadIdx.x >> 4, H = p.H;
+  const uint32_t c = blockIdx.x * 64u + 4 * lane;
   float* const out = kind == 0 ? p.dw_out : kind == 1 ? p.db_out : kind == 2 ? p.dw_in : kind == 3 ? p.db_in : p.dgate;
   if (!out) return;
-  float s = 0.f, s0 = 0.f;
+  const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
+  v4f s = zero, s0 = zero;
+  const bool of_gate = kind >= 4;
   if (c < H) {
-    const bool of_gate = kind >= 4;
     const uint32_t first = of_gate ? (kind - 4) * p.wgs_per_gate : 0u, last = of_gate ? first + p.wgs_per_gate : p.parts;
     const uint32_t k = of_gate ? 2u : kind;
-    for (uint32_t q = first + row; q < last; q += 32) {
-      const float v = p.part[((size_t)q * 4 + k) * H + c];
-      if (kind == 2 || kind == 3) s = fmaf(p.gate ? p.gate[(size_t)(q / p.wgs_per_gate) * H + c] : 1.f, v, s);
-      else s += v;
-      if (of_gate && p.b_in) s0 += p.part[((size_t)q * 4 + 3) * H + c];
+#pragma unroll 4
+    for (uint32_t q = first + row; q < last; q += 64) {
+      v4f v = *(const v4f*)(p.part + ((size_t)q * 4 + k) * H + c);
+      if ((kind == 2 || kind == 3) && p.gate) v *= *(const v4f*)(p.gate + (size_t)(q / p.wgs_per_gate) * H + c);
+      s += v;
+      if (of_gate && p.b_in) s0 += *(const v4f*)(p.part + ((size_t)q * 4 + 3) * H + c);
     }
   }
   red[0][row][lane] = s;
   red[1][row][lane] = s0;
   __syncthreads();
-  if (row != 0 || c >= H) return;
-  s = s0 = 0.f;
-  for (int q = 0; q < 32; ++q) {
-    s += red[0][q][lane];
-    s0 += red[1][q][lane];
+  const uint32_t x = threadIdx.x, col = blockIdx.x * 64u + x;   // a lane a column
+  if (x >= 64 || col >= H) return;
+  float a = 0.f, a0 = 0.f;
+#pragma unroll 8
+  for (int q = 0; q < 64; ++q) {
+    a += red[0][q][x / 4][x % 4];
+    a0 += red[1][q][x / 4][x % 4];
   }
-  if (kind >= 4) out[(size_t)(kind - 4) * H + c] = fmaf(p.w_in ? p.w_in[c] : 1.f, s, p.b_in ? p.b_in[c] * s0 : 0.f);
-  else out[c] = s;
+  if (of_gate) out[(size_t)(kind - 4) * H + col] = fmaf(p.w_in ? p.w_in[col] : 1.f, a, p.b_in ? p.b_in[col] * a0 : 0.f);
+  else out[col] = a;
 }
 
 }  // namespace gp

@@ -247,7 +247,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepArgs p) {
 
 // A bias gradient from the row tiles' sums: 32 columns a workgroup, 32 tiles at a
 // time, then those in order.
-__global__ __launch_bounds__(1024) inline void bias_sums_kernel(const float* sums, float* db, uint32_t N, uint32_t tiles) {
+static __global__ __launch_bounds__(1024) void bias_sums_kernel(const float* sums, float* db, uint32_t N, uint32_t tiles) {
   __shared__ float red[32][33];
   const uint32_t lane = threadIdx.x & 31, row = threadIdx.x >> 5, c = blockIdx.x * 32u + lane;
   float s = 0.f;

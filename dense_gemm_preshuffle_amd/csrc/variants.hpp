@@ -153,8 +153,9 @@
   X(DT, 256, 256, false) X(DT, 128, 256, false) X(DT, 128, 128, false) X(DT, 64, 128, false) \
   X(DT, 128, 256, true) X(DT, 128, 128, true) X(DT, 64, 128, true)
 #define GP_SMALL_LINEAR(X, DT) \
-  X(DT, 0, 1, 8, 2) X(DT, 0, 2, 8, 2) X(DT, 1, 1, 8, 2) X(DT, 1, 2, 8, 2) X(DT, 2, 1, 8, 2) X(DT, 2, 2, 8, 2) \
-  X(DT, 4, 1, 8, 2) X(DT, 4, 2, 8, 2) X(DT, 6, 1, 8, 1) X(DT, 6, 2, 8, 1) X(DT, 8, 1, 8, 1) X(DT, 8, 2, 8, 1)
+  X(DT, 0, 1, 8, 2) X(DT, 0, 2, 8, 1) X(DT, 1, 1, 8, 2) X(DT, 1, 2, 8, 1) X(DT, 2, 1, 4, 2) X(DT, 2, 2, 8, 1) \
+  X(DT, 4, 1, 4, 2) X(DT, 4, 2, 8, 1) X(DT, 4, 4, 8, 1) X(DT, 6, 1, 8, 1) X(DT, 6, 2, 8, 1) X(DT, 6, 4, 8, 1) \
+  X(DT, 8, 1, 4, 1) X(DT, 8, 2, 8, 1) X(DT, 8, 4, 8, 1)
 
 // Row-major B (BF16 / FP16, 16 x 16 blocks, 128-byte K tiles): X(dtype,
 // epilogue, tile_m, tile_n, stages, able to split K across workgroups). Three
