@@ -336,20 +336,29 @@ __device__ __forceinline__ float wave_sum(float v) {
   };
   return (row(0) + row(1)) + (row(2) + row(3));
 }
+// 64-bit values: two moves each. f: a function of two, associative and commutative
+// enough for the caller.
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp64(uint64_t v) {
+  return (uint64_t)dpp<CTRL>((uint32_t)(v >> 32)) << 32 | dpp<CTRL>((uint32_t)v);
+}
+__device__ __forceinline__ uint64_t readlane64(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+template <class T, class F>
+__device__ __forceinline__ T wave_reduce64(T v, F&& f) {
+  static_assert(sizeof(T) == 8, "64 bits");
+  auto step = [&](auto c) GP_INLINE { v = f(v, __builtin_bit_cast(T, dpp64<decltype(c)::value>(__builtin_bit_cast(uint64_t, v)))); };
+  step(std::integral_constant<int, kDppSwapPairs>{});
+  step(std::integral_constant<int, kDppSwapQuadHalves>{});
+  step(std::integral_constant<int, kDppHalfRowMirror>{});
+  step(std::integral_constant<int, kDppRowMirror>{});
+  auto row = [&](int r) GP_INLINE { return __builtin_bit_cast(T, readlane64(__builtin_bit_cast(uint64_t, v), 16 * r)); };
+  return f(f(row(0), row(1)), f(row(2), row(3)));
+}
 __device__ __forceinline__ double wave_sum64(double v) {
-  auto both = [](double x, auto&& f) GP_INLINE -> double {
-    const uint64_t u = __builtin_bit_cast(uint64_t, x);
-    return __builtin_bit_cast(double, (uint64_t)f((uint32_t)(u >> 32)) << 32 | f((uint32_t)u));
-  };
-  auto add = [&](auto c) GP_INLINE { v += both(v, [](uint32_t u) GP_INLINE { return dpp<decltype(c)::value>(u); }); };
-  add(std::integral_constant<int, kDppSwapPairs>{});
-  add(std::integral_constant<int, kDppSwapQuadHalves>{});
-  add(std::integral_constant<int, kDppHalfRowMirror>{});
-  add(std::integral_constant<int, kDppRowMirror>{});
-  auto row = [&](int r) GP_INLINE {
-    return both(v, [r](uint32_t u) GP_INLINE { return (uint32_t)__builtin_amdgcn_readlane((int)u, 16 * r); });
-  };
-  return (row(0) + row(1)) + (row(2) + row(3));
+  return wave_reduce64(v, [](double a, double b) GP_INLINE { return a + b; });
 }
 
 // The value of x, hidden from the optimizer: every quantity derived from the

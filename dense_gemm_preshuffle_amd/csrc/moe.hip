@@ -79,7 +79,10 @@ hipError_t launch_moe(int xl, bool up, const MoeArgs& a, hipStream_t s) {
   GP_MOE_CASE(1, 2, 8, 2, true)
   GP_MOE_CASE(2, 2, 8, 2, true)
   GP_MOE_CASE(4, 2, 8, 2, true)
-  GP_MOE_CASE(0, 1, 8, 2, false)
+  if (xl == 0 && !up) {
+    hipLaunchKernelGGL((moe_down_one_kernel<DT, 1, 16, 4>), dim3(a.F / 16), dim3(1024), 0, s, a);
+    return hipGetLastError();
+  }
   GP_MOE_CASE(1, 1, 8, 2, false)
   GP_MOE_CASE(2, 1, 8, 2, false)
   GP_MOE_CASE(4, 1, 8, 2, false)

@@ -1,8 +1,8 @@
 // A mixture-of-experts layer for a few tokens, for gfx950, in three launches:
 //   route   l = x Wr^T, p = softmax(l) or sigmoid(l), the k experts of largest p (+
 //           bias) of each token, their weights g
-//   up      h[p] = act(x Wg_e^T) * (x Wu_e^T)        for each pair p = (token, choice j)
-//   down    y = residual + sum over j of g_j (h[p] Wd_e^T)
+//   up      h[p] = g_j act(x Wg_e^T) * (x Wu_e^T)    for each pair p = (token, choice j)
+//   down    y = residual + sum over j of h[p] Wd_e^T
 // Bound by reading the chosen experts' weights from HBM, once each: a workgroup owns an
 // expert's NB column blocks and runs all its tokens through them, found in a list that
 // it makes from the choices itself. Nothing of an expert without tokens is read.
@@ -30,94 +30,86 @@ struct RouteArgs {
   float scale;
 };
 
-__device__ __forceinline__ double shfl_xor64(double v, int o) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __shfl_xor((uint32_t)u, o, 64), hi = __shfl_xor((uint32_t)(u >> 32), o, 64);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
 constexpr uint32_t kMaxExperts = 512;
 
-// The k experts of token m, by one wave: lane l has experts l, l + 64, ...
+// The k experts of token m, by one wave: lane l has experts l, l + 64, ... Each round
+// takes the largest key of the wave; a key orders as its double does, with NaN (1) below
+// every number and 0 for an expert that is not there or chosen already.
 __device__ __forceinline__ void choose_experts(const RouteArgs& p, uint32_t m, uint32_t lane) {
   constexpr int NE = kMaxExperts / 64;
-  constexpr uint32_t kNone = 0xffffffffu;
-  const double inf = __builtin_inf();
-  double score[NE], order[NE];
-  uint32_t left = 0;   // bit j: expert lane + 64 j is there and not chosen yet
-  double top = -inf;
+  auto key = [](double v) GP_INLINE -> uint64_t {
+    if (!(v == v)) return 1;
+    const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);   // (-0 as 0)
+    return u >> 63 ? ~u : u | 1ull << 63;
+  };
+  double score[NE];
+  uint64_t keys[NE];
+  double top = -__builtin_inf();
 #pragma unroll
   for (int j = 0; j < NE; ++j) {
-    score[j] = order[j] = -inf;
-    if (64u * j >= p.E) continue;
+    score[j] = 0.0;
+    keys[j] = 0;
     const uint32_t e = lane + 64u * j;
-    if (e < p.E) {
-      const uint64_t u = __hip_atomic_load((const uint64_t*)p.logits + (size_t)m * p.E + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      score[j] = __builtin_bit_cast(double, u);
-      left |= 1u << j;
-      // (a NaN is kept by the sum below, not by the maximum)
-      if (score[j] > top) top = score[j];
-    }
-  }
-  if (!p.sigmoid) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) top = fmax(top, shfl_xor64(top, o));
+    if (64u * j >= p.E || e >= p.E) continue;
+    const uint64_t u = __hip_atomic_load((const uint64_t*)p.logits + (size_t)m * p.E + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    score[j] = __builtin_bit_cast(double, u);
+    // without a bias the logits order the experts as their scores do, and do not saturate
+    keys[j] = key(score[j]);
+    top = fmax(top, score[j]);   // (a NaN is kept by the sum below)
   }
   double sum = 0.0;
+  if (!p.sigmoid) top = wave_reduce64(top, [](double a, double b) GP_INLINE { return fmax(a, b); });
 #pragma unroll
   for (int j = 0; j < NE; ++j) {
-    if (64u * j >= p.E) continue;
-    if (!(left >> j & 1u)) continue;
-    // without a bias the logits order the experts as their scores do, and do not saturate
-    const double l = score[j];
-    score[j] = p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top);
+    if (keys[j] == 0) continue;
+    score[j] = p.sigmoid ? 1.0 / (1.0 + exp(-score[j])) : exp(score[j] - top);
     sum += score[j];
-    order[j] = l;
   }
   if (!p.sigmoid) sum = wave_sum64(sum);
+  uint64_t best = 0;
+  uint32_t at = 0;   // the lane's largest key and its j
+  auto lane_best = [&]() GP_INLINE {
+    best = keys[0];
+    at = 0;
+#pragma unroll
+    for (int j = 1; j < NE; ++j)
+      if (keys[j] > best) best = keys[j], at = j;
+  };
 #pragma unroll
   for (int j = 0; j < NE; ++j) {
-    if (64u * j >= p.E) continue;
-    if (!(left >> j & 1u)) continue;
+    if (keys[j] == 0) continue;
     if (!p.sigmoid) score[j] /= sum;
-    if (p.bias) order[j] = score[j] + (double)p.bias[lane + 64 * j];
-    if (!(order[j] == order[j])) order[j] = -inf;   // NaN: after every number
+    if (p.bias) keys[j] = key(score[j] + (double)p.bias[lane + 64 * j]);
   }
-  double total = 0.0, mine = 0.0;   // lane j: the score of choice j
-  uint32_t id = 0;
+  lane_best();
+  uint32_t rank[NE];
+  double mine = 0.0;   // the lane's chosen scores
+#pragma unroll
+  for (int j = 0; j < NE; ++j) rank[j] = ~0u;
   for (uint32_t c = 0; c < p.k; ++c) {
-    double best = -inf, s = 0.0;
-    uint32_t at = kNone;   // ties, also of lanes, go to the lowest expert
+    const uint64_t most = wave_reduce64(best, [](uint64_t a, uint64_t b) GP_INLINE { return a > b ? a : b; });
+    // ties go to the lowest expert: the lowest j, then the lowest lane
+    uint64_t who = 0;
+    uint32_t j0 = 0;
+    for (; j0 < (uint32_t)NE; ++j0)
+      if ((who = __ballot(best == most && at == j0))) break;
+    if (lane == (uint32_t)__builtin_ctzll(who)) {
 #pragma unroll
-    for (int j = 0; j < NE; ++j) {
-      if (64u * j >= p.E) continue;
-      if ((left >> j & 1u) && (at == kNone || order[j] > best)) {
-        best = order[j];
-        s = score[j];
-        at = lane + 64u * j;
-      }
+      for (int j = 0; j < NE; ++j)
+        if ((uint32_t)j == j0) {
+          keys[j] = 0;
+          rank[j] = c;
+          mine += score[j];
+        }
+      lane_best();
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      const double ob = shfl_xor64(best, o), os = shfl_xor64(s, o);
-      const uint32_t oa = __shfl_xor(at, o, 64);
-      if (oa != kNone && (at == kNone || ob > best || (ob == best && oa < at))) {
-        best = ob;
-        s = os;
-        at = oa;
-      }
-    }
-    if (at % 64u == lane) left &= ~(1u << (at / 64u));
-    if (lane == c) {
-      id = at;
-      mine = s;
-    }
-    total += s;
   }
-  if (lane < p.k) {
-    if (p.normalize) mine /= total;
-    p.ids[(size_t)m * p.k + lane] = (int32_t)id;
-    p.gates[(size_t)m * p.k + lane] = (float)(mine * (double)p.scale);
+  const double total = p.normalize ? wave_sum64(mine) : 1.0;
+#pragma unroll
+  for (int j = 0; j < NE; ++j) {
+    if (rank[j] == ~0u) continue;
+    p.ids[(size_t)m * p.k + rank[j]] = (int32_t)(lane + 64 * j);
+    p.gates[(size_t)m * p.k + rank[j]] = (float)(score[j] / total * (double)p.scale);
   }
 }
 
@@ -174,7 +166,7 @@ struct MoeArgs {
   size_t expert_bytes;
   const int32_t* ids;       // [pairs]; outside [0, E): no expert, the pair adds nothing
   char* h;                  // up: [pairs][F]
-  const float* gates;       // down: [pairs]
+  const float* gates;       // up: [pairs]
   const char* res;          // down: [M][F], or null
   char* y;                  // down: [M][F]
   float* part;              // down: [pairs][F]
@@ -221,7 +213,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_kernel(MoeArgs p) {
   constexpr int XW = (ONE ? 2 : ROWS) * 128;
   constexpr int LDS = WAVES * (XW > NQ * 1024 ? XW : NQ * 1024);
   __shared__ __attribute__((aligned(16))) char lds[LDS];
-  __shared__ uint16_t list[kMaxPairs];
+  __shared__ uint16_t list[ONE ? 1 : kMaxPairs];
   __shared__ uint32_t count, word;
 
   const int tid = threadIdx.x;
@@ -231,13 +223,18 @@ __global__ __launch_bounds__(WAVES * 64) void moe_kernel(MoeArgs p) {
   const uint32_t slot = blockIdx.x / p.cols, bx = blockIdx.x % p.cols;
   const bool by_pair = p.slots == pairs;
   const uint32_t e = __builtin_amdgcn_readfirstlane(by_pair ? (uint32_t)p.ids[slot] : slot);
-  if (wave == 0) {
-    const uint32_t n = list_pairs(p, slot, by_pair, e, list);
-    if (lane == 0) count = n;
+  // one token: a slot is a pair (an expert that stands twice is read twice)
+  uint32_t n = e < p.E ? 1u : 0u;
+  if constexpr (!ONE) {
+    if (wave == 0) {
+      const uint32_t l = list_pairs(p, slot, by_pair, e, list);
+      if (lane == 0) count = l;
+    }
+    __syncthreads();
+    n = __builtin_amdgcn_readfirstlane(count);
   }
-  __syncthreads();
-  const uint32_t n = __builtin_amdgcn_readfirstlane(count);
   if (UP && n == 0) return;
+  auto pair_at = [&](uint32_t r) GP_INLINE -> uint32_t { return ONE ? slot : list[r]; };
 
   const uint32_t blocks = p.F / 16, block0 = bx * OB;
   const uint32_t nblock = min((uint32_t)OB, blocks - block0);   // real blocks of this workgroup
@@ -254,7 +251,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_kernel(MoeArgs p) {
   for (uint32_t r0 = 0; r0 < n; r0 += ROWS) {
     const uint32_t rows = min((uint32_t)ROWS, n - r0);
     auto a_row = [&](uint32_t r) GP_INLINE -> uint32_t {   // offset of a list entry's row
-      const uint32_t q = list[r0 + r];
+      const uint32_t q = pair_at(r0 + r);
       return (UP ? q / p.k : q) * Ka;
     };
     uint32_t x_off[XL > 0 ? XL : 1];
@@ -339,14 +336,16 @@ __global__ __launch_bounds__(WAVES * 64) void moe_kernel(MoeArgs p) {
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) v[i] += red[(w * NQ + NV * q + i) * 64 + lane];
       }
-      const uint32_t pair = list[r0 + row], col = (block0 + ob) * 16 + 4 * lane_hi;
+      const uint32_t pair = pair_at(r0 + row), col = (block0 + ob) * 16 + 4 * lane_hi;
       if constexpr (UP) {
-        // rounded to the type, as the matrix products take it
+        // weighted here, so that the down product adds a token's experts up as they are,
+        // and rounded to the type, as the matrix products take it
         v4f h;
+        const float g = p.gates[pair];
         with_act(p.act, [&](auto act_c) GP_INLINE {
           constexpr int A = decltype(act_c)::value;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) h[r] = activate_ffn<A>(v[0][r]) * v[1][r];
+          for (int r = 0; r < 4; ++r) h[r] = g * (activate_ffn<A>(v[0][r]) * v[1][r]);
         });
         *(v2i*)(p.h + ((size_t)pair * p.F + col) * 2) = pack_out4<DT>(h);
       } else {
@@ -358,7 +357,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_kernel(MoeArgs p) {
   }
   if constexpr (!UP) {
     // the last workgroup of the columns adds up each token's experts, in the order of
-    // its choices, weighted
+    // its choices
     if (!last_to_arrive(p.cnt + bx, p.slots, &word)) return;
     const __amdgpu_buffer_rsrc_t rp = make_rsrc(p.part, pairs * p.F * 4);
     for (uint32_t i = tid; i < p.M * nblock * 4; i += WAVES * 64) {
@@ -367,16 +366,95 @@ __global__ __launch_bounds__(WAVES * 64) void moe_kernel(MoeArgs p) {
       for (uint32_t j = 0; j < p.k; ++j) {
         const uint32_t q = m * p.k + j;
         if ((uint32_t)p.ids[q] >= p.E) continue;
-        const v4f o = __builtin_bit_cast(v4f, buf_load16_coh(rp, (q * p.F + col) * 4));
-        const float g = p.gates[q];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = fmaf(g, o[r], v[r]);
+        v += __builtin_bit_cast(v4f, buf_load16_coh(rp, (q * p.F + col) * 4));
       }
       const size_t off = ((size_t)m * p.F + col) * 2;
       if (p.res) v += widen4<DT>(*(const v2i*)(p.res + off));
       *(v2i*)(p.y + off) = pack_out4<DT>(v);
     }
   }
+}
+
+// The down product of one token: its k experts' products are one of K = k Ka. WAVES waves
+// split those chunks, so that a workgroup's columns are finished by itself: no partial
+// products in memory and no arrival, which take the general form 3 us of 11 (8 experts of
+// 2048 x 1024).
+template <int DT, int NB, int WAVES, int S>
+__global__ __launch_bounds__(WAVES * 64) void moe_down_one_kernel(MoeArgs p) {
+  __shared__ __attribute__((aligned(16))) char lds[WAVES * NB * 1024];
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63, lane_lo = lane & 15, lane_hi = lane >> 4;
+  const uint32_t Ka = p.Ka, Kb = p.Kb;
+  const uint32_t block0 = blockIdx.x * NB, nblock = min((uint32_t)NB, p.F / 16 - block0);
+  const uint32_t nchunk = Kb / 128, all = p.k * nchunk;
+  const uint32_t c0 = wave * all / WAVES, c1 = (wave + 1) * all / WAVES;
+  const int groups = (int)((c1 - c0 + S - 1) / S);
+  const int id = (uint32_t)lane < p.k ? p.ids[lane] : -1;   // lane j: choice j
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a, p.k * Ka);
+  constexpr uint32_t kOOB = 0x80000000u;
+  char* xw = lds + wave * (NB * 1024);
+  const uint32_t xcol = 4 * lane;
+  int xr[2][S];
+  v4i bf[2][S][2][NB];
+  v4f acc[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) acc[nb] = v4f{0.f, 0.f, 0.f, 0.f};
+  auto load = [&](auto par_c, int gr) GP_INLINE {
+    constexpr int par = decltype(par_c)::value;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const uint32_t c = c0 + (uint32_t)gr * S + s, j = min(c / nchunk, p.k - 1), k = c - j * nchunk;
+      const uint32_t e = (uint32_t)__builtin_amdgcn_readlane(id, (int)j);
+      const bool is = c < c1 && e < p.E;   // (else zeros from an empty resource)
+      const __amdgpu_buffer_rsrc_t rb =
+          make_rsrc(p.b + (is ? e : 0u) * p.expert_bytes + (size_t)block0 * 16 * Kb, is ? nblock * 16 * Kb : 0u);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        bf[par][s][0][nb] = buf_load16_nt(rb, nb * 16 * Kb + lane * 16, k * 2048);
+        bf[par][s][1][nb] = buf_load16_nt(rb, nb * 16 * Kb + lane * 16 + 1024, k * 2048);
+      }
+      xr[par][s] = buf_load4(ra, is && lane < 32 && 128 * k + xcol < Ka ? xcol : kOOB, j * Ka + 128 * k);
+    }
+  };
+  auto compute = [&](auto par_c) GP_INLINE {
+    constexpr int par = decltype(par_c)::value;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      *(int*)(xw + 4 * lane) = xr[par][s];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const v4i xf = *(const v4i*)(xw + (4 * t + lane_hi) * 16);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) acc[nb] = mfma<DT>(&bf[par][s][t][nb], &xf, acc[nb]);
+      }
+    }
+  };
+  using P0 = std::integral_constant<int, 0>;
+  using P1 = std::integral_constant<int, 1>;
+  if (groups > 0) {
+    load(P0{}, 0);
+    int gr = 0;
+    for (; gr + 2 <= groups; gr += 2) {
+      load(P1{}, gr + 1);
+      compute(P0{});
+      if (gr + 2 < groups) load(P0{}, gr + 2);
+      compute(P1{});
+    }
+    if (gr < groups) compute(P0{});
+  }
+  // (each wave's sums take the place of its own x)
+  v4f* red = (v4f*)lds;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) red[(wave * NB + nb) * 64 + lane] = acc[nb];
+  __syncthreads();
+  if (wave >= NB || (uint32_t)wave >= nblock || lane_lo != 0) return;
+  v4f v = red[wave * 64 + lane];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) v += red[(w * NB + wave) * 64 + lane];
+  const size_t off = ((block0 + wave) * 16 + 4 * lane_hi) * 2;
+  if (p.res) v += widen4<DT>(*(const v2i*)(p.res + off));
+  *(v2i*)(p.y + off) = pack_out4<DT>(v);
 }
 
 }  // namespace gp
