@@ -56,10 +56,13 @@ int plan_moe(int dtype, int64_t M, int64_t F, int64_t H, int64_t E, int64_t k, M
   if (r) return r;
   if (M > kMaxTokens || k > E || k > kMaxChoices || M * k > kMaxPairs) return GP_ESHAPE;
   if (H / 16 > kMaxSplitTiles - kRouteCounters || !fits(M * k, 4 * H) || !fits(M * k, 2 * F)) return GP_ESHAPE;
-  p->xl = M == 1 ? 0 : M <= 8 ? 1 : M <= 16 || M * k <= 6 * E ? 2 : 4;
+  // rows at a time for the longest list of an expert, about twice the average (further
+  // turns read the weights again, mostly from L2)
+  const int64_t most = M * k / E;
+  p->xl = M == 1 ? 0 : M <= 8 || most <= 3 ? 1 : M <= 16 || most <= 14 ? 2 : most <= 30 ? 4 : 8;
   p->slots = std::min(M * k, E);
   p->up_cols = F / 16;
-  p->down_cols = H / 16;
+  p->down_cols = p->xl == 0 ? H / 16 : (H / 16 + 1) / 2;
   p->off_logits = kCounterBytes;
   p->off_h = p->off_logits + align256(M * E * 8);
   p->off_part = p->off_h + align256(M * k * F * 2);
@@ -68,6 +71,16 @@ int plan_moe(int dtype, int64_t M, int64_t F, int64_t H, int64_t E, int64_t k, M
   return GP_OK;
 }
 
+// Variants: rows, 16-column blocks, waves, chunks of K in flight per group. Measured us
+// (both products, up's or down's variant alone changed), M, k of E, H x F:
+//   16, 8 of 64, 2048 x 1024: up 8 rows on 8 waves 143, 16 rows on 4 of one chunk 145, of two
+//     chunks on 8 159; down two blocks on 4 waves 135, one on 8 159 (8192 workgroups of 32 KB)
+//   64, 8 of 128, 2048 x 768: up 16 rows 312, 8 rows 319 (longest list 11), with 8 waves and two
+//     chunks 359; down two blocks on 4 waves 256, one on 8 359
+//   64, 2 of 4, 2048 x 4096: up 64 rows 67, 32 rows 75, 16 rows 97 (longest list 39)
+//   33, 2 of 8, 4096 x 14336: up 16 rows 452, 32 rows 458; down two blocks on 8 waves 462, one 470
+//   one token, 8 of 64, 2048 x 1024: up 8 waves of two chunks 20.8, 4 of four 21.4; down 8 waves
+//     20.8, 16 20.8, as the general form 23.7
 #define GP_MOE_CASE(XL, NB, W, S, UP)                                                                            \
   if (xl == XL && up == UP) {                                                                                    \
     hipLaunchKernelGGL((moe_kernel<DT, XL, NB, W, S, UP>), dim3(a.slots * a.cols), dim3(W * 64), 0, s, a);       \
@@ -76,16 +89,18 @@ int plan_moe(int dtype, int64_t M, int64_t F, int64_t H, int64_t E, int64_t k, M
 template <int DT>
 hipError_t launch_moe(int xl, bool up, const MoeArgs& a, hipStream_t s) {
   GP_MOE_CASE(0, 2, 8, 2, true)
-  GP_MOE_CASE(1, 2, 8, 2, true)
-  GP_MOE_CASE(2, 2, 8, 2, true)
-  GP_MOE_CASE(4, 2, 8, 2, true)
-  if (xl == 0 && !up) {
-    hipLaunchKernelGGL((moe_down_one_kernel<DT, 1, 16, 4>), dim3(a.F / 16), dim3(1024), 0, s, a);
+  GP_MOE_CASE(1, 2, 8, 1, true)
+  GP_MOE_CASE(2, 2, 4, 1, true)
+  GP_MOE_CASE(4, 2, 4, 1, true)
+  GP_MOE_CASE(8, 2, 4, 1, true)
+  if (xl == 0) {
+    hipLaunchKernelGGL((moe_down_one_kernel<DT, 1, 8, 2>), dim3(a.cols), dim3(512), 0, s, a);
     return hipGetLastError();
   }
-  GP_MOE_CASE(1, 1, 8, 2, false)
-  GP_MOE_CASE(2, 1, 8, 2, false)
-  GP_MOE_CASE(4, 1, 8, 2, false)
+  GP_MOE_CASE(1, 2, 4, 1, false)
+  GP_MOE_CASE(2, 2, 4, 1, false)
+  GP_MOE_CASE(4, 2, 8, 1, false)
+  GP_MOE_CASE(8, 2, 8, 1, false)
   return hipErrorInvalidValue;
 }
 #undef GP_MOE_CASE

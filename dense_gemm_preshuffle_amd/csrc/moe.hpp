@@ -32,40 +32,50 @@ struct RouteArgs {
 
 constexpr uint32_t kMaxExperts = 512;
 
-// The k experts of token m, by one wave: lane l has experts l, l + 64, ... Each round
-// takes the largest key of the wave; a key orders as its double does, with NaN (1) below
-// every number and 0 for an expert that is not there or chosen already.
+// The k experts of token m, by one wave: lane l has experts l, l + 64, ... (NE of them).
+// Each round takes the largest key of the wave; a key orders as its double does, with NaN
+// (1) below every number and 0 for an expert that is not there or chosen already.
+// Scores that the result does not need are not taken: without a bias the logits order
+// the experts as their scores do (and do not saturate), and in normalised softmax
+// weights the sum over all experts cancels.
+template <int NE>
 __device__ __forceinline__ void choose_experts(const RouteArgs& p, uint32_t m, uint32_t lane) {
-  constexpr int NE = kMaxExperts / 64;
   auto key = [](double v) GP_INLINE -> uint64_t {
     if (!(v == v)) return 1;
     const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);   // (-0 as 0)
     return u >> 63 ? ~u : u | 1ull << 63;
   };
-  double score[NE];
+  double l[NE];
   uint64_t keys[NE];
   double top = -__builtin_inf();
 #pragma unroll
   for (int j = 0; j < NE; ++j) {
-    score[j] = 0.0;
+    l[j] = 0.0;
     keys[j] = 0;
     const uint32_t e = lane + 64u * j;
-    if (64u * j >= p.E || e >= p.E) continue;
+    if (e >= p.E) continue;
     const uint64_t u = __hip_atomic_load((const uint64_t*)p.logits + (size_t)m * p.E + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    score[j] = __builtin_bit_cast(double, u);
-    // without a bias the logits order the experts as their scores do, and do not saturate
-    keys[j] = key(score[j]);
-    top = fmax(top, score[j]);   // (a NaN is kept by the sum below)
+    l[j] = __builtin_bit_cast(double, u);
+    keys[j] = key(l[j]);
+    top = fmax(top, l[j]);
   }
-  double sum = 0.0;
   if (!p.sigmoid) top = wave_reduce64(top, [](double a, double b) GP_INLINE { return fmax(a, b); });
+  // (softmax: the score times the sum over the experts)
+  auto score = [&](double v) GP_INLINE { return p.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - top); };
+  double sum = 1.0;
+  if (p.bias || (!p.sigmoid && !p.normalize)) {
+    double s[NE], mine = 0.0;
 #pragma unroll
-  for (int j = 0; j < NE; ++j) {
-    if (keys[j] == 0) continue;
-    score[j] = p.sigmoid ? 1.0 / (1.0 + exp(-score[j])) : exp(score[j] - top);
-    sum += score[j];
+    for (int j = 0; j < NE; ++j) {
+      s[j] = keys[j] ? score(l[j]) : 0.0;
+      mine += s[j];
+    }
+    if (!p.sigmoid) sum = wave_sum64(mine);
+    if (p.bias)
+#pragma unroll
+      for (int j = 0; j < NE; ++j)
+        if (keys[j]) keys[j] = key(s[j] / sum + (double)p.bias[lane + 64 * j]);
   }
-  if (!p.sigmoid) sum = wave_sum64(sum);
   uint64_t best = 0;
   uint32_t at = 0;   // the lane's largest key and its j
   auto lane_best = [&]() GP_INLINE {
@@ -75,15 +85,8 @@ __device__ __forceinline__ void choose_experts(const RouteArgs& p, uint32_t m, u
     for (int j = 1; j < NE; ++j)
       if (keys[j] > best) best = keys[j], at = j;
   };
-#pragma unroll
-  for (int j = 0; j < NE; ++j) {
-    if (keys[j] == 0) continue;
-    if (!p.sigmoid) score[j] /= sum;
-    if (p.bias) keys[j] = key(score[j] + (double)p.bias[lane + 64 * j]);
-  }
   lane_best();
   uint32_t rank[NE];
-  double mine = 0.0;   // the lane's chosen scores
 #pragma unroll
   for (int j = 0; j < NE; ++j) rank[j] = ~0u;
   for (uint32_t c = 0; c < p.k; ++c) {
@@ -99,26 +102,62 @@ __device__ __forceinline__ void choose_experts(const RouteArgs& p, uint32_t m, u
         if ((uint32_t)j == j0) {
           keys[j] = 0;
           rank[j] = c;
-          mine += score[j];
         }
       lane_best();
     }
   }
-  const double total = p.normalize ? wave_sum64(mine) : 1.0;
+  double mine = 0.0;   // the lane's chosen scores
+#pragma unroll
+  for (int j = 0; j < NE; ++j)
+    if (rank[j] != ~0u) {
+      l[j] = score(l[j]);
+      mine += l[j];
+    }
+  const double total = p.normalize ? wave_sum64(mine) : sum;
 #pragma unroll
   for (int j = 0; j < NE; ++j) {
     if (rank[j] == ~0u) continue;
     p.ids[(size_t)m * p.k + rank[j]] = (int32_t)(lane + 64 * j);
-    p.gates[(size_t)m * p.k + rank[j]] = (float)(score[j] / total * (double)p.scale);
+    p.gates[(size_t)m * p.k + rank[j]] = (float)(l[j] / total * (double)p.scale);
   }
+}
+
+// Sums of N values (a power of two up to 16) over each row of 16 lanes: a step hands one
+// half of the values to the other half of the lanes and adds what comes back, so that N
+// values take N - 1 exchanges and not 4 N. The lane ends up with value lane % 16 /
+// (16 / N) of its row.
+template <int N>
+__device__ __forceinline__ double row_sums(double (&v)[N], uint32_t lane) {
+  auto step = [&](auto n_c, auto ctrl_c, uint32_t bit) GP_INLINE {
+    constexpr int n = decltype(n_c)::value, ctrl = decltype(ctrl_c)::value;
+    auto other = [](double x) GP_INLINE { return __builtin_bit_cast(double, dpp64<ctrl>(__builtin_bit_cast(uint64_t, x))); };
+    if constexpr (n > 1) {
+      const bool up = lane & bit;
+#pragma unroll
+      for (int i = 0; i < n / 2; ++i) {
+        const double keep = up ? v[i + n / 2] : v[i], give = up ? v[i] : v[i + n / 2];
+        v[i] = keep + other(give);
+      }
+    } else {
+      v[0] += other(v[0]);
+    }
+  };
+  constexpr auto left = [](int s) { return N >> s > 1 ? N >> s : 1; };
+  step(std::integral_constant<int, left(0)>{}, std::integral_constant<int, kDppRowMirror>{}, 8);
+  step(std::integral_constant<int, left(1)>{}, std::integral_constant<int, kDppHalfRowMirror>{}, 4);
+  step(std::integral_constant<int, left(2)>{}, std::integral_constant<int, kDppSwapQuadHalves>{}, 2);
+  step(std::integral_constant<int, left(3)>{}, std::integral_constant<int, kDppSwapPairs>{}, 1);
+  return v[0];
 }
 
 template <int DT, int TB, int EB>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
-  __shared__ double red[4][TB * EB];
+  constexpr int N = TB * EB;
+  __shared__ double red[16][N];   // of each row of 16 lanes
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const uint32_t e0 = blockIdx.x * EB, m0 = blockIdx.y * TB;
-  double acc[TB][EB] = {};
+  double acc[N] = {};
+#pragma unroll TB == 1 ? 2 : 1
   for (uint32_t c = tid; c < p.H / 8; c += 256) {
     v4i xv[TB], wv[EB];
 #pragma unroll
@@ -134,29 +173,43 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
       for (int t = 0; t < TB; ++t) {
         const double x = (double)widen16<DT>((uint32_t)xv[t][i / 2], i & 1);
 #pragma unroll
-        for (int e = 0; e < EB; ++e) acc[t][e] = fma(x, w[e], acc[t][e]);
+        for (int e = 0; e < EB; ++e) acc[t * EB + e] = fma(x, w[e], acc[t * EB + e]);
       }
     }
   }
-#pragma unroll
-  for (int t = 0; t < TB; ++t)
-#pragma unroll
-    for (int e = 0; e < EB; ++e) {
-      const double v = wave_sum64(acc[t][e]);
-      if (lane == 0) red[wave][t * EB + e] = v;
-    }
+  const double row = row_sums<N>(acc, lane);
+  if (lane % (16 / N) == 0) red[tid / 16][lane % 16 / (16 / N)] = row;
   __syncthreads();
-  if (tid < TB * EB) {
+  if (tid < N) {
+    double v = 0.0;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) v += red[r][tid];
     const uint32_t t = tid / EB, e = tid % EB;
-    const double v = ((red[0][tid] + red[1][tid]) + red[2][tid]) + red[3][tid];
     if (m0 + t < p.M && e0 + e < p.E)
       __hip_atomic_store((uint64_t*)p.logits + (size_t)(m0 + t) * p.E + e0 + e, __builtin_bit_cast(uint64_t, v),
                          __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  __shared__ uint32_t word;
-  if (!last_to_arrive(p.cnt + blockIdx.y, gridDim.x, &word)) return;
-  for (uint32_t t = wave; t < TB; t += 4)
-    if (m0 + t < p.M) choose_experts(p, m0 + t, lane);
+  auto choose = [&](uint32_t m) GP_INLINE {
+    if (p.E <= 64) choose_experts<1>(p, m, lane);
+    else if (p.E <= 128) choose_experts<2>(p, m, lane);
+    else if (p.E <= 256) choose_experts<4>(p, m, lane);
+    else choose_experts<8>(p, m, lane);
+  };
+  if constexpr (TB == 1) {
+    // one wave stores, arrives and chooses: no barrier (as last_to_arrive otherwise)
+    if (wave != 0) return;
+    __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xF << 8));   // vmcnt(0): the logits are stored
+    uint32_t before = 0;
+    if (lane == 0) before = __hip_atomic_fetch_add(p.cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if ((uint32_t)__builtin_amdgcn_readfirstlane((int)before) != gridDim.x - 1) return;
+    if (lane == 0) __hip_atomic_store(p.cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    choose(m0);
+  } else {
+    __shared__ uint32_t word;
+    if (!last_to_arrive(p.cnt + blockIdx.y, gridDim.x, &word)) return;
+    for (uint32_t t = wave; t < TB; t += 4)
+      if (m0 + t < p.M) choose(m0 + t);
+  }
 }
 
 // ---- the experts' products ----
