@@ -270,14 +270,22 @@ def _dt(x) -> int:
     return DTYPES[x] if isinstance(x, str) else int(x)
 
 
+@functools.lru_cache(maxsize=None)
+def _cuda():
+    """torch's current device index, and the handle of a device's current stream (looked up once: an import
+    statement in a call takes 0.3 us)."""
+    from torch import _C
+
+    return _C._cuda_getDevice, _C._cuda_getCurrentRawStream
+
+
 def _stream(stream):
     """The handle of a stream argument: None is torch's current stream, an int a handle, else a torch stream."""
     if stream is None:
-        from torch import _C
-
         # the handle alone: making the Stream object of torch.cuda.current_stream()
         # took 2.6 us of the 9 us that a small product's call spent on the host
-        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+        device, raw = _cuda()
+        return raw(device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -727,16 +735,21 @@ def gemm_backward(dtype, dc, a, b, want_da=True, want_db=True, da=None, db=None,
 
 
 @functools.lru_cache(maxsize=None)
-def _uint8():
+def _types():
+    """(float32, int32, uint8) of torch, and its empty_like."""
     import torch
 
-    return torch.uint8
+    return torch.float32, torch.int32, torch.uint8, torch.empty_like
 
 
 def _device() -> int:
-    from torch import _C
+    return _cuda()[0]()
 
-    return _C._cuda_getDevice()
+
+def _is(t, dtype, shape, index) -> bool:
+    """A contiguous tensor of this type and shape on device `index`. The operators below check each tensor with it
+    once, and name the wrong one (_want) only where a check has failed."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
 
 
 def _here(where, name, t, stream):
@@ -791,33 +804,36 @@ def gemm_linear(dtype, x, w_shuf, bias=None, act="none", residual=None, save=Fal
     """y = act(x W^T + bias) + residual: x [M, K], w_shuf from gemm_linear_preshuffle, bias fp32 [N], residual
     [M, N], either of them None. Returns y, or (y, z) with save=True, z = x W^T + bias in x's type. y may be the
     residual. Without a workspace one is made for the call where the plan needs it."""
-    dt, t = _half(dtype)
     where = "gemm_linear"
-    _here(where, "x", x, stream)
-    M, K = x.shape
-    device = x.device
+    dt, t = _half(dtype)
+    M, K = shape = x.shape
+    index, device = x.get_device(), x.device
+    if stream is not None or index < 0 or index != _device():
+        _here(where, "x", x, stream)
+    f32, _, u8, _ = _types()
     Kp = -(-K // 64) * 64
-    N = _nbytes(w_shuf) // (2 * Kp) if K else 0
-    _want("gemm_linear: x", x, (M, K), t)
-    _want("gemm_linear: w_shuf", w_shuf, (2 * N * Kp,), _uint8(), device)
+    N = w_shuf.numel() // (2 * Kp) if K else 0
+    out = (M, N)
+    if not (_is(x, t, shape, index) and _is(w_shuf, u8, (2 * N * Kp,), index)
+            and (residual is None or _is(residual, t, out, index)) and (bias is None or _is(bias, f32, (N,), index))
+            and (y is None or _is(y, t, out, index)) and (z is None or _is(z, t, out, index))):
+        for name, v, d, sh in (("x", x, t, shape), ("w_shuf", w_shuf, u8, (2 * N * Kp,)), ("residual", residual, t, out),
+                               ("bias", bias, f32, (N,)), ("y", y, t, out), ("z", z, t, out)):
+            if v is not None:
+                _want(f"{where}: {name}", v, sh, d, device)
     if not save and z is not None:
-        raise ValueError("gemm_linear: z is written with save=True")
-    for name, v in (("residual", residual), ("y", y), ("z", z)):
-        if v is not None and not _fits(v, (M, N), t, device):
-            _want(f"gemm_linear: {name}", v, (M, N), t, device)
-    if bias is not None:
-        import torch
-
-        _want("gemm_linear: bias", bias, (N,), torch.float32, device)
+        raise ValueError(f"{where}: z is written with save=True")
     with _on(stream, device):
-        y = x.new_empty((M, N)) if y is None else y
+        y = x.new_empty(out) if y is None else y
         if save and z is None:
-            z = x.new_empty((M, N))
+            z = x.new_empty(out)
         if workspace is None:
             workspace = linear_workspace(dt, M, N, K, device)
-    _check(load_library().gemm_linear(dt, x.data_ptr(), w_shuf.data_ptr(), _ptr(bias), _act(act), _ptr(residual),
-                                      y.data_ptr(), _ptr(z), M, N, K, _ptr(workspace),
-                                      _workspace_bytes(where, workspace, device), _stream(stream)), where)
+    status = load_library().gemm_linear(dt, x.data_ptr(), w_shuf.data_ptr(), _ptr(bias), _act(act), _ptr(residual),
+                                        y.data_ptr(), _ptr(z), M, N, K, _ptr(workspace),
+                                        _workspace_bytes(where, workspace, device), _stream(stream))
+    if status:
+        _check(status, where)
     return (y, z) if save else y
 
 
@@ -892,21 +908,24 @@ def _norm(kind) -> int:
     return NORMS[kind] if isinstance(kind, str) else int(kind)
 
 
-def _norm_args(where, t, M, H, dev, rows, vectors, gate):
-    """Checks of the [M, H] tensors, the fp32 vectors over the columns and the gate; the gate's rows."""
-    import torch
-
-    for name, v in rows:
-        if v is not None and not _fits(v, (M, H), t, dev):
-            _want(f"{where}: {name}", v, (M, H), t, dev)
-    for name, v in vectors:
-        if v is not None and not _fits(v, (H,), torch.float32, dev):
-            _want(f"{where}: {name}", v, (H,), torch.float32, dev)
+def _norm_args(where, t, shape, index, dev, w_in, b_in, w_out, b_out, gate, **rows) -> int:
+    """Checks of the fp32 vectors over the columns, the gate and, by name, the [M, H] tensors; the gate's rows."""
+    f32, vec = _types()[0], shape[1:]
+    if not ((w_out is None or _is(w_out, f32, vec, index)) and (w_in is None or _is(w_in, f32, vec, index))
+            and (b_out is None or _is(b_out, f32, vec, index)) and (b_in is None or _is(b_in, f32, vec, index))):
+        for name, v in (("w_in", w_in), ("b_in", b_in), ("w_out", w_out), ("b_out", b_out)):
+            if v is not None:
+                _want(f"{where}: {name}", v, vec, f32, dev)
+    for name in rows:
+        v = rows[name]
+        if v is not None and not _is(v, t, shape, index):
+            _want(f"{where}: {name}", v, shape, t, dev)
     if gate is None:
         return 0
-    if not _fits(gate, (gate.shape[0], H), torch.float32, dev):
-        _want(f"{where}: gate", gate, (gate.shape[0], H), torch.float32, dev)
-    return gate.shape[0]
+    gates = gate.shape[0]
+    if not _is(gate, f32, (gates, shape[1]), index):
+        _want(f"{where}: gate", gate, (gates, shape[1]), f32, dev)
+    return gates
 
 
 def gemm_norm(dtype, x, residual=None, scale=1.0, norm_in="none", w_in=None, b_in=None, gate=None, norm_out="rms",
@@ -917,22 +936,25 @@ def gemm_norm(dtype, x, residual=None, scale=1.0, norm_in="none", w_in=None, b_i
     is not stored and None. r may be the residual or x, y may be x."""
     where = "gemm_norm"
     dt, t = _half(dtype)
-    M, H = x.shape
-    dev = x.device
-    _here(where, "x", x, stream)
+    M, H = shape = x.shape
+    index, dev = x.get_device(), x.device
+    if stream is not None or index < 0 or index != _device():
+        _here(where, "x", x, stream)
     kin, kout = _norm(norm_in), _norm(norm_out)
     if (r is not None and not want_r) or (y is not None and not kout):
         raise ValueError(f"{where}: an output is given that is not computed")
-    gates = _norm_args(where, t, M, H, dev, (("x", x), ("residual", residual), ("r", r), ("y", y)),
-                       (("w_in", w_in), ("b_in", b_in), ("w_out", w_out), ("b_out", b_out)), gate)
+    gates = _norm_args(where, t, shape, index, dev, w_in, b_in, w_out, b_out, gate, x=x, residual=residual, r=r, y=y)
     with _on(stream, dev):
+        like = _types()[3]
         if want_r and r is None:
-            r = x.new_empty((M, H))
+            r = like(x)
         if kout and y is None:
-            y = x.new_empty((M, H))
-    _check(load_library().gemm_norm(dt, x.data_ptr(), _ptr(residual), scale, kin, _ptr(w_in), _ptr(b_in), _ptr(gate),
-                                    gates, kout, _ptr(w_out), _ptr(b_out), eps, _ptr(r), _ptr(y), M, H,
-                                    _stream(stream)), where)
+            y = like(x)
+    status = load_library().gemm_norm(dt, x.data_ptr(), _ptr(residual), scale, kin, _ptr(w_in), _ptr(b_in), _ptr(gate),
+                                      gates, kout, _ptr(w_out), _ptr(b_out), eps, _ptr(r), _ptr(y), M, H,
+                                      _stream(stream))
+    if status:
+        _check(status, where)
     return r, y
 
 
@@ -955,27 +977,26 @@ def gemm_norm_backward(dtype, dy, dr, x, r, scale=1.0, norm_in="none", w_in=None
     reaches r by other ways (None: nothing), r as gemm_norm returned it (None with norm_out "none"). x may be None
     where neither the gate's gradient nor one through norm_in needs it. With want_params the gradients of the
     parameters that are given are computed, in fp32."""
-    import torch
-
     where = "gemm_norm_backward"
     dt, t = _half(dtype)
     lead = dy if dy is not None else dr
     if lead is None:
         raise ValueError(f"{where}: neither dy nor dr is given")
-    _here(where, "dr" if dy is None else "dy", lead, stream)
-    M, H = lead.shape
-    dev = lead.device
+    M, H = shape = lead.shape
+    index, dev = lead.get_device(), lead.device
+    if stream is not None or index < 0 or index != _device():
+        _here(where, "dr" if dy is None else "dy", lead, stream)
     if (dx is not None and not want_dx) or (dresidual is not None and not want_dresidual):
         raise ValueError(f"{where}: an output is given that is not computed")
-    gates = _norm_args(where, t, M, H, dev, (("dy", dy), ("dr", dr), ("x", x), ("r", r), ("dx", dx),
-                                             ("dresidual", dresidual)),
-                       (("w_in", w_in), ("b_in", b_in), ("w_out", w_out), ("b_out", b_out)), gate)
+    gates = _norm_args(where, t, shape, index, dev, w_in, b_in, w_out, b_out, gate, dy=dy, dr=dr, x=x, r=r, dx=dx,
+                       dresidual=dresidual)
     with _on(stream, dev):
+        like = _types()[3]
         if want_dx and dx is None:
-            dx = lead.new_empty((M, H))
+            dx = like(lead)
         if want_dresidual and dresidual is None:
-            dresidual = lead.new_empty((M, H))
-        grads = [torch.empty_like(v) if v is not None and want_params else None for v in (w_in, b_in, gate, w_out, b_out)]
+            dresidual = like(lead)
+        grads = [like(v) if v is not None and want_params else None for v in (w_in, b_in, gate, w_out, b_out)]
         if workspace is None and any(g is not None for g in grads):
             workspace = norm_backward_workspace(dt, M, H, gates, dev)
         _check(load_library().gemm_norm_backward(dt, _ptr(dy), _ptr(dr), _ptr(x), _ptr(r), scale, _norm(norm_in),
