@@ -165,7 +165,7 @@ int check_linear(int dtype, int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0) return GP_EINVAL;
   if (!half_type(dtype)) return GP_EDTYPE;
   if (M >= kMaxBytes || N >= kMaxBytes || K >= kMaxBytes) return GP_ESHAPE;
-  if (N % 16 || K % 32) return GP_ESHAPE;
+  if (N % 16 || K % 16) return GP_ESHAPE;
   if (!fits(M, 2 * K) || !fits(N, 2 * whole_k(K)) || !fits(M, 2 * N)) return GP_ESHAPE;
   return GP_OK;
 }
@@ -315,12 +315,12 @@ bool plan_pair(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t Nb, int64
   return found;
 }
 
-// gated: dc itself is made by the call ([M][Np] in the workspace; N % 16 is enough).
+// gated: dc itself is made by the call ([M][Np] in the workspace); else N % 32 == 0.
 int make_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, bool gated, BackwardPlan* p) {
   if (M <= 0 || N <= 0 || K <= 0) return GP_EINVAL;
   if (!half_type(dtype)) return GP_EDTYPE;
   if (M >= kMaxBytes / 4 || N >= kMaxBytes || K >= kMaxBytes) return GP_ESHAPE;
-  if (N % (gated ? 16 : 32) || K % 32) return GP_ESHAPE;
+  if (N % (gated ? 16 : 32) || K % 16) return GP_ESHAPE;
   p->Mp = pad_k(M);
   p->Np = gated ? pad_k(N) : N;
   if (!fits(p->Mp, 2 * K) || !fits(p->Np, 2 * K) || !fits(p->Mp, 2 * p->Np)) return GP_ESHAPE;
@@ -383,6 +383,12 @@ int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool
     s.plan = *p;
   }
   return r;
+}
+
+// gemm_backward: its forward products take whole 64-byte blocks of K.
+int plan_plain_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, BackwardPlan* p) {
+  const int r = plan_backward(dtype, M, N, K, want_da, want_db, false, p);
+  return r == GP_OK && K % 32 ? GP_ESHAPE : r;
 }
 
 uint32_t tiles64(int64_t R, int64_t C) { return (uint32_t)(((R + 63) / 64) * ((C + 63) / 64)); }
@@ -792,7 +798,7 @@ int gemm_linear_backward(int dtype, const void* dy, const void* z, const void* x
 int gemm_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int want_da, int want_db, size_t* bytes) {
   if (!bytes || (!want_da && !want_db)) return GP_EINVAL;
   BackwardPlan p;
-  const int r = plan_backward(dtype, M, N, K, want_da != 0, want_db != 0, false, &p);
+  const int r = plan_plain_backward(dtype, M, N, K, want_da != 0, want_db != 0, &p);
   if (r) return r;
   *bytes = (size_t)p.bytes;
   return GP_OK;
@@ -803,7 +809,7 @@ int gemm_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, int want_da, 
   if (!da || !db || (!want_da && !want_db)) return GP_EINVAL;
   BackwardPlan p;
   const int r = gated ? plan_gated_backward(dtype, M, N, K, want_da != 0, want_db != 0, &p)
-                      : plan_backward(dtype, M, N, K, want_da != 0, want_db != 0, false, &p);
+                      : plan_plain_backward(dtype, M, N, K, want_da != 0, want_db != 0, &p);
   if (r) return r;
   *da = *db = gemm_plan_info();
   auto fill = [&](const Plan& q, bool rows, int64_t m, int64_t n, int64_t k, gemm_plan_info* out) {
@@ -833,7 +839,7 @@ int gemm_backward(int dtype, const void* dc, const void* a, const void* b, void*
   if ((da && !b) || (db && !a)) return GP_EINVAL;
   if (!is_aligned16(a) || !is_aligned16(b) || !is_aligned16(da) || !is_aligned16(db)) return GP_EINVAL;
   BackwardPlan p;
-  int r = plan_backward(dtype, M, N, K, da != nullptr, db != nullptr, false, &p);
+  int r = plan_plain_backward(dtype, M, N, K, da != nullptr, db != nullptr, &p);
   if (r) return r;
   if (!workspace || (int64_t)workspace_bytes < p.bytes) return GP_EWORKSPACE;
   if (!is_aligned16(workspace)) return GP_EINVAL;

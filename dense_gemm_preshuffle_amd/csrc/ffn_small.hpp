@@ -100,10 +100,11 @@ __global__ __launch_bounds__(WAVES * 64) void ffn_small_kernel(GatedArgs p) {
         bf[par][s][0][nb] = buf_load16_nt(rb, (nb * 16 * Kb + lane * 16) | skip, k * 2048);
         bf[par][s][1][nb] = buf_load16_nt(rb, (nb * 16 * Kb + lane * 16 + 1024) | skip, k * 2048);
       }
-      const uint32_t xo = (128 * k + xcol < Ka ? x_off : kOOB) | skip;
-      if constexpr (ONE) xr[par][s][0][0] = buf_load4(ra, xo, 128 * k);
+      // (or-ed in: a sum would pass 2^32 for the longest rows)
+      const uint32_t past = (128 * k + xcol < Ka ? 0u : kOOB) | skip;
+      if constexpr (ONE) xr[par][s][0][0] = buf_load4(ra, x_off | past, 128 * k);
 #pragma unroll
-      for (int i = 0; i < XL; ++i) xr[par][s][i] = buf_load16(ra, xo + 8 * i * Ka, 128 * k);
+      for (int i = 0; i < XL; ++i) xr[par][s][i] = buf_load16(ra, (x_off + 8 * i * Ka) | past, 128 * k);
     }
   };
   auto compute = [&](auto par_c) GP_INLINE {

@@ -467,7 +467,7 @@ int gemm_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, int want_da, 
  *   z = x W^T + bias,  y = act(z) + residual
  *
  * x [M][K], W [N][K], z / y / residual [M][N] of one type (GP_BF16 or GP_F16, else
- * GP_EDTYPE), bias fp32 [N]. M is free, N % 16 == 0, K % 32 == 0 (else GP_ESHAPE),
+ * GP_EDTYPE), bias fp32 [N]. M is free, N % 16 == 0, K % 16 == 0 (else GP_ESHAPE),
  * every matrix below 2^31 bytes.
  *
  * gemm_linear_preshuffle -- w [N][K] -> w_shuf (2 N K' bytes, K' = K rounded up to
@@ -679,9 +679,9 @@ int gemm_moe_route(int dtype, const void* x, const void* router, const float* bi
 /*
  * gemm_moe_experts -- the experts' products for choices and weights that the caller
  * has. An id outside [0, E) (an expert that is elsewhere, or none) adds nothing; an
- * expert may stand twice for a token. h = act(gate) * up is rounded to the type
- * between the two products (as gemm_gated stores it), all else stays fp32; y is
- * rounded once.
+ * expert may stand twice for a token. g_j act(gate) * up, the operand of the second
+ * product, is rounded to the type (in FP16 infinite beyond 65504), all else stays
+ * fp32; y is rounded once.
  *   residual    device [M][H], or NULL. y may be the residual; it is not x.
  * The same call gives the same bits.
  */

@@ -1,6 +1,6 @@
 """References in 64 bits and error bounds for the mixture-of-experts layer: the router in float64 (the library's
-own precision there), each pair's products as tests/_ffn.py bounds them (h is rounded to the type between them),
-the weighted sum in fp32."""
+own precision there), each pair's products as tests/_ffn.py bounds them (the weighted h is rounded to the type
+between them), the sum over the choices in fp32."""
 from __future__ import annotations
 
 from tests import _ffn as F64
@@ -35,11 +35,12 @@ def experts64(dtype, x, w13, w2, ids, gates, act, residual):
             if not len(rows):
                 continue
             (h, _, _), (eh, _, _) = F64.gated64(x[rows], w13[ex], act)
-            o, eo = F64.product64(h, w2[ex].double(), F64.rounded(dtype, h, eh))
             g = gates[rows, j].double()[:, None]
-            y[rows] += g * o
-            e[rows] += g.abs() * eo
-            mag[rows] += (g * o).abs() + g.abs() * eo
+            h, eh = g * h, g.abs() * eh + E32 * (g * h).abs()
+            o, eo = F64.product64(h, w2[ex].double(), F64.rounded(dtype, h, eh))
+            y[rows] += o
+            e[rows] += eo
+            mag[rows] += o.abs() + eo
     if residual is not None:
         y = y + residual.double()
         mag = mag + residual.double().abs()

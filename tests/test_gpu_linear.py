@@ -26,7 +26,7 @@ def _normal(gen, *shape, t, scale=1.0):
 # rows: one token, each small variant's last and first count, the tiles' first, edge
 # tiles; N: one block, columns no tile divides; K: one 64-byte block, odd block
 # counts (K shares that differ), K split across workgroups
-SHAPES = [(1, 16, 32), (1, 4096, 96), (1, 9232, 2048), (3, 2064, 160), (8, 48, 544), (9, 8208, 96), (16, 256, 512), (17, 48, 544),
+SHAPES = [(1, 16, 32), (1, 272, 16), (5, 1040, 48), (40, 528, 2064), (130, 2048, 2064), (300, 272, 80), (1025, 1040, 1040), (1, 4096, 96), (1, 9232, 2048), (3, 2064, 160), (8, 48, 544), (9, 8208, 96), (16, 256, 512), (17, 48, 544),
           (32, 8448, 160), (33, 272, 1024), (48, 8208, 352), (64, 1040, 352), (64, 8448, 416), (64, 512, 8192), (65, 144, 512),
           (65, 112, 160), (100, 16, 64), (129, 1040, 96), (300, 2064, 512), (512, 1024, 8192), (777, 1040, 2048),
           (256, 4096, 4096), (1025, 4112, 1024), (2048, 8192, 256), (2100, 8208, 1056)]
@@ -112,7 +112,7 @@ def test_rows_do_not_mix(dtype, M):
             assert bool(wrong.any()) if bad_x else (bool(wrong[3]) and int(wrong.sum()) == 1)
 
 
-BACKWARD = [(1, 32, 32), (1, 16, 32), (2, 96, 96), (31, 544, 160), (31, 528, 160), (130, 2064, 2048), (4100, 1040, 512), (33, 1056, 544), (65, 2080, 160), (130, 2080, 2048), (257, 1056, 1024),
+BACKWARD = [(1, 32, 32), (3, 64, 16), (130, 2048, 2064), (300, 272, 80), (70, 1040, 1040), (4100, 544, 1040), (1, 16, 32), (2, 96, 96), (31, 544, 160), (31, 528, 160), (130, 2064, 2048), (4100, 1040, 512), (33, 1056, 544), (65, 2080, 160), (130, 2080, 2048), (257, 1056, 1024),
             (500, 512, 4096), (1000, 4128, 256), (2049, 1024, 1024), (4100, 992, 512)]
 
 

@@ -40,7 +40,8 @@ def test_sizes():
     for bad in ((0, 32, 32), (-1, 32, 32), (4, 0, 32), (4, 32, 0)):
         assert size(f, BF16, *bad)[0] == EINVAL
     assert size(f, FP8, 4, 32, 32)[0] == EDTYPE
-    for bad in ((4, 24, 32), (4, 32, 48), (2 ** 31, 32, 32), (4, 2 ** 31, 32), (4, 32, 2 ** 31), (2 ** 62, 2 ** 62, 32),
+    assert size(f, BF16, 4, 32, 48)[0] == OK
+    for bad in ((4, 24, 32), (4, 32, 40), (2 ** 31, 32, 32), (4, 2 ** 31, 32), (4, 32, 2 ** 31), (2 ** 62, 2 ** 62, 32),
                 (2 ** 20, 32, 2 ** 20), (32, 2 ** 20, 2 ** 20), (2 ** 20, 2 ** 20, 32)):
         assert size(f, BF16, *bad)[0] == ESHAPE, bad
     assert gp.load_library().gemm_linear_workspace_size(BF16, 4, 32, 32, None) == EINVAL
@@ -60,14 +61,14 @@ def test_backward_sizes():
     assert n(dx=0, dw=0) < n(dw=0)
     assert size(f, BF16, 4, 32, 32, 0, 0, 0, 0)[0] == size(f, BF16, 4, 32, 32, 4, 1, 1, 1)[0] == EINVAL
     assert size(f, BF16, 4, 48, 32, 0, 1, 1, 1)[0] == size(f, BF16, 4, 48, 32, 0, 0, 0, 1)[0] == OK
-    assert size(f, BF16, 4, 40, 32, 0, 1, 1, 1)[0] == size(f, BF16, 4, 48, 48, 2, 0, 0, 1)[0] == ESHAPE
+    assert size(f, BF16, 4, 40, 32, 0, 1, 1, 1)[0] == size(f, BF16, 4, 48, 40, 2, 0, 0, 1)[0] == ESHAPE
     assert size(f, FP8, 4, 32, 32, 0, 1, 1, 1)[0] == EDTYPE
 
 
 def test_forward_arguments(lib):
-    def call(dtype=BF16, x=P, w=P, bias=P, act=2, res=P, y=P, z=P, M=4, N=32, K=48, ws=None):
+    def call(dtype=BF16, x=P, w=P, bias=P, act=2, res=P, y=P, z=P, M=4, N=32, K=40, ws=None):
         return lib.gemm_linear(dtype, x, w, bias, act, res, y, z, M, N, K, ws, 0, None)
-    assert call() == ESHAPE                                            # (K = 48: everything before it passes)
+    assert call() == ESHAPE                                            # (K = 40: everything before it passes)
     assert call(x=None) == call(w=None) == call(y=None) == call(act=-1) == call(act=4) == EINVAL
     for name in ("x", "w", "bias", "res", "y", "z"):
         assert call(**{name: MIS}) == EINVAL, name
@@ -80,7 +81,7 @@ def test_preshuffle_arguments(lib):
     f = lib.gemm_linear_preshuffle
     assert f(None, P, 32, 32, BF16, None) == f(P, None, 32, 32, BF16, None) == f(P, MIS, 32, 32, BF16, None) == EINVAL
     assert f(P, ctypes.c_void_p(0x100000 + 2032), 32, 32, BF16, None) == EINVAL     # overlap
-    assert f(P, Q, 24, 32, BF16, None) == f(P, Q, 32, 16, BF16, None) == ESHAPE
+    assert f(P, Q, 24, 32, BF16, None) == f(P, Q, 32, 24, BF16, None) == ESHAPE
     assert f(P, Q, 32, 32, FP8, None) == EDTYPE
 
 
