@@ -270,11 +270,13 @@ int64_t pad_k(int64_t k) {
 // (M 1 to 2821) da took 0.20 to 0.92 of the time that it takes from copies, db 0.58
 // to 1.02 (a as it is: 10 x 10304 x 4480 25.0 us, from copies 117; 29 x 224 x 1728 db
 // 11.9, 11.8).
-bool plan_rows(int64_t M, int64_t N, int64_t Kb, const Plan* other, double copied, Plan* p, double* took) {
-  const double us = *took = choose_tile_us(kRowsTimes, M, N, Kb, false, p);
+bool plan_rows(int64_t M, int64_t N, int64_t Kb, const Plan* other, double copied, Plan* p, double* took,
+               double* took_copies) {
+  const double us = *took = *took_copies = choose_tile_us(kRowsTimes, M, N, Kb, false, p);
   if (!other || other->kernel != GP_KERNEL_TILE) return true;
   for (const TileTime& t : kRowsTimes)
-    if (t.tm == other->tm && t.tn == other->tn) return us <= tile_us(t, M, N, Kb, other->ks, 0.85) + copied / 4.9e6;
+    if (t.tm == other->tm && t.tn == other->tn)
+      return us <= (*took_copies = tile_us(t, M, N, Kb, other->ks, 0.85) + copied / 4.9e6);
   return true;
 }
 
@@ -316,7 +318,11 @@ bool plan_pair(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t Nb, int64
 }
 
 // gated: dc itself is made by the call ([M][Np] in the workspace); else N % 32 == 0.
-int make_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, bool gated, BackwardPlan* p) {
+// linear: both products may also leave the copies for one launch, where its expected
+// time is below theirs (130 x 2064 x 2048 17.4 us for 23.5, 32 x 1024 x 4096 13.9 for
+// 16.9; gemm_backward and the gated one keep the plans, and so the bits, that they had).
+int make_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, bool gated, bool linear,
+                       BackwardPlan* p) {
   if (M <= 0 || N <= 0 || K <= 0) return GP_EINVAL;
   if (!half_type(dtype)) return GP_EDTYPE;
   if (M >= kMaxBytes / 4 || N >= kMaxBytes || K >= kMaxBytes) return GP_ESHAPE;
@@ -330,15 +336,21 @@ int make_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, bool want_da,
   // ranges) 24 took the same time within 2%, 4 up to 8% less, 3 more: da of 1500 x
   // 5984 x 800 40.5 us against 34.9, db of 1319 x 5280 x 704 21.1 against 19.1.
   Plan copies, copies_b;   // (one each: the planner sets what differs from a new Plan)
-  double us_a = 0, us_b = 0;
+  double us_a = 0, us_b = 0, copies_a_us = 0, copies_b_us = 0;
   int r = plan_gemm(dtype, M, K, p->Np, &copies);
-  p->da_rows = plan_rows(M, K, 2 * whole_k(p->Np), r ? nullptr : &copies, 4.0 * p->Np * K, &p->da, &us_a);
+  p->da_rows = plan_rows(M, K, 2 * whole_k(p->Np), r ? nullptr : &copies, 4.0 * p->Np * K, &p->da, &us_a, &copies_a_us);
   if (!p->da_rows) p->da = copies;
   r = plan_gemm(dtype, N, K, p->Mp, &copies_b);
-  p->db_rows = plan_rows(K, N, 2 * p->Mp, r ? nullptr : &copies_b, (gated ? 2.0 : 4.0) * p->Mp * N, &p->db, &us_b);
+  p->db_rows = plan_rows(K, N, 2 * p->Mp, r ? nullptr : &copies_b, (gated ? 2.0 : 4.0) * p->Mp * N, &p->db, &us_b, &copies_b_us);
   if (!p->db_rows) p->db = copies_b;
-  p->pair = p->da_rows && p->db_rows &&
-            plan_pair(M, K, whole_k(p->Np) / 64, K, N, p->Mp / 64, us_a + us_b, &p->da, &p->db) && want_da && want_db;
+  if (linear) {
+    us_a = std::min(us_a, copies_a_us);
+    us_b = std::min(us_b, copies_b_us);
+  }
+  p->pair = (linear || (p->da_rows && p->db_rows)) &&
+            plan_pair(M, K, whole_k(p->Np) / 64, K, N, p->Mp / 64, us_a + us_b, &p->da, &p->db);
+  if (p->pair) p->da_rows = p->db_rows = true;
+  p->pair = p->pair && want_da && want_db;
   const int64_t part_a = want_da ? plan_workspace(p->da, M, K) : 0;
   const int64_t part_b = want_db ? (p->db_rows ? plan_workspace(p->db, K, N) : plan_workspace(p->db, N, K)) : 0;
   int64_t parts = std::max(part_a, part_b);
@@ -363,13 +375,14 @@ int make_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, bool want_da,
 // A plan depends on these numbers alone and takes 3 to 6 us to make, as long as a
 // launch; a training loop asks for a few of them over and over. Kept per thread,
 // the latest of each slot.
-int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, bool gated, BackwardPlan* p) {
+int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, bool gated, bool linear,
+                  BackwardPlan* p) {
   struct Slot {
     int64_t key[4] = {-1, 0, 0, 0};
     BackwardPlan plan;
   };
   static thread_local Slot slots[32];
-  const int64_t key[4] = {(int64_t)dtype * 8 + want_da * 4 + want_db * 2 + gated, M, N, K};
+  const int64_t key[4] = {(int64_t)dtype * 16 + linear * 8 + want_da * 4 + want_db * 2 + gated, M, N, K};
   uint64_t h = 0;
   for (int64_t k : key) h = (h ^ (uint64_t)k) * 0x9E3779B97F4A7C15ull;
   Slot& s = slots[h >> 59];
@@ -377,7 +390,7 @@ int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool
     *p = s.plan;
     return GP_OK;
   }
-  const int r = make_backward_plan(dtype, M, N, K, want_da, want_db, gated, p);
+  const int r = make_backward_plan(dtype, M, N, K, want_da, want_db, gated, linear, p);
   if (r == GP_OK) {
     std::copy(key, key + 4, s.key);
     s.plan = *p;
@@ -387,7 +400,7 @@ int plan_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool
 
 // gemm_backward: its forward products take whole 64-byte blocks of K.
 int plan_plain_backward(int dtype, int64_t M, int64_t N, int64_t K, bool want_da, bool want_db, BackwardPlan* p) {
-  const int r = plan_backward(dtype, M, N, K, want_da, want_db, false, p);
+  const int r = plan_backward(dtype, M, N, K, want_da, want_db, false, false, p);
   return r == GP_OK && K % 32 ? GP_ESHAPE : r;
 }
 
@@ -424,14 +437,19 @@ TileArgs rows_args(const Plan& p, const void* a, int64_t lda, const void* b, voi
 // output gradient, rows of ldc elements; gate: the pointwise backward that makes
 // it first (else null; linear: the linear layer's). Stops at the first launch that
 // fails.
-int run_backward(int dtype, const BackwardPlan& p, const GateGradArgs* gate, bool linear, const void* dc, int64_t ldc,
-                 const void* a, const void* b, void* da, void* db, int64_t M, int64_t N, int64_t K, char* ws,
-                 hipStream_t s) {
+int run_backward(int dtype, const BackwardPlan& p, const GateGradArgs* gate, bool linear, const BiasJob* bias,
+                 const void* dc, int64_t ldc, const void* a, const void* b, void* da, void* db, int64_t M, int64_t N,
+                 int64_t K, char* ws, hipStream_t s) {
   PrepArgs t = {};
   uint64_t blocks = 0;
+  if (bias) {
+    t.bias = *bias;
+    blocks = bias->blocks;
+  }
   if (gate) {
     t.gate = *gate;
-    blocks = t.gate.blocks = tiles64(p.Mp, t.gate.F);
+    t.gate.blocks = tiles64(p.Mp, t.gate.F);
+    blocks += t.gate.blocks;
   }
   int jobs = 0;
   auto copy = [&](const void* src, int64_t off, int64_t R, int64_t C, int64_t Kp, bool preshuffled) {
@@ -498,25 +516,30 @@ int run_backward(int dtype, const BackwardPlan& p, const GateGradArgs* gate, boo
 int plan_gated_backward(int dtype, int64_t M, int64_t F, int64_t H, bool dx, bool dw, BackwardPlan* p) {
   const int r = check_gated(dtype, M, F, H);
   if (r) return r;
-  return plan_backward(dtype, M, 2 * F, H, dx, dw, true, p);
+  return plan_backward(dtype, M, 2 * F, H, dx, dw, true, false, p);
 }
 
 // gemm_linear_backward: the products of gemm_backward, on a dz that the call makes where
 // there is an activation or N is no whole number of 64-byte blocks. Its workspace is
 // the products' (dz among it), then the row tiles' sums of the bias gradient.
+// Up to so many rows the bias gradient is summed from dy itself (bias_strip), above from the
+// row tiles' sums: 130 x 2064 x 2048 19.3 us and 21.0, 300 x 4096 x 1024 27.9 and 27.0, 500 x 2048 x
+// 2048 30.5 and 28.
+constexpr int64_t kStripRows = 192;
 struct LinearBackwardPlan {
   BackwardPlan products;
-  bool made = false;
+  bool made = false, strips = false;
   int64_t off_sums = 0, bytes = 0;
 };
 int plan_linear_backward(int dtype, int64_t M, int64_t N, int64_t K, int act, bool dx, bool dw, bool db,
                          LinearBackwardPlan* p) {
   p->made = act != GP_ACT_NONE || N % 32;
   // (the sizes are checked as for the products, also where only the sums are wanted)
-  const int r = plan_backward(dtype, M, N, K, dx || !dw, dw, p->made, &p->products);
+  const int r = plan_backward(dtype, M, N, K, dx || !dw, dw, p->made, true, &p->products);
   if (r) return r;
+  p->strips = db && M <= kStripRows;
   p->off_sums = dx || dw ? align256(p->products.bytes) : 0;
-  p->bytes = std::max<int64_t>(p->off_sums + (db ? (p->products.Mp + 63) / 64 * N * 4 : 0), 256);
+  p->bytes = std::max<int64_t>(p->off_sums + (db && !p->strips ? (p->products.Mp + 63) / 64 * N * 4 : 0), 256);
   return GP_OK;
 }
 
@@ -767,28 +790,41 @@ int gemm_linear_backward(int dtype, const void* dy, const void* z, const void* x
   t.gate = act == GP_ACT_NONE ? nullptr : (const char*)z;
   t.d = p.made && (dx || (dw && q.db_rows)) ? ws + q.off_d : nullptr;
   t.dt = dw && !q.db_rows ? ws + q.off_ct : nullptr;
-  t.sums = dbias ? (float*)(ws + p.off_sums) : nullptr;
+  t.sums = dbias && !p.strips ? (float*)(ws + p.off_sums) : nullptr;
   t.M = (uint32_t)M;
   t.F = (uint32_t)N;
   t.Mp = (uint32_t)q.Mp;
   t.Np = (uint32_t)q.Np;
   t.tiles_c = (uint32_t)((N + 63) / 64);
   t.act = act;
-  // the products last: where no product is wanted nothing but the sums runs
-  const bool pass = p.made || dbias;
+  BiasJob strips = {};
+  if (p.strips) {
+    strips.dy = (const char*)dy;
+    strips.z = t.gate;
+    strips.db = dbias;
+    strips.M = (uint32_t)M;
+    strips.N = (uint32_t)N;
+    strips.blocks = (uint32_t)((N + 63) / 64);
+    strips.act = act;
+  }
+  // the pass over dy: where dz is made, or row tiles summed
+  const bool pass = (p.made && products) || t.sums;
   if (products) {
-    r = run_backward(dtype, q, pass ? &t : nullptr, true, p.made ? (const void*)(ws + q.off_d) : dy, p.made ? q.Np : N, x, w,
-                     dx, dw, M, N, K, ws, s);
+    r = run_backward(dtype, q, pass ? &t : nullptr, true, p.strips ? &strips : nullptr,
+                     p.made ? (const void*)(ws + q.off_d) : dy, p.made ? q.Np : N, x, w, dx, dw, M, N, K, ws, s);
   } else {
     PrepArgs only = {};
-    only.gate = t;
-    only.gate.blocks = tiles64(q.Mp, N);
+    if (pass) {
+      only.gate = t;
+      only.gate.blocks = tiles64(q.Mp, N);
+    }
+    only.bias = strips;
     forget_hip_error();
     auto* prep = dtype == GP_BF16 ? prep_kernel<DT_BF16, true> : prep_kernel<DT_F16, true>;
-    hipLaunchKernelGGL(prep, dim3(only.gate.blocks), dim3(256), 0, s, only);
+    hipLaunchKernelGGL(prep, dim3(only.gate.blocks + only.bias.blocks), dim3(256), 0, s, only);
     r = report_hip(hipGetLastError(), "kernel launch");
   }
-  if (r || !dbias) return r;
+  if (r || !t.sums) return r;
   forget_hip_error();
   hipLaunchKernelGGL(bias_sums_kernel, dim3((uint32_t)((N + 31) / 32)), dim3(1024), 0, s, (const float*)t.sums, dbias,
                      (uint32_t)N, (uint32_t)((q.Mp + 63) / 64));
@@ -844,7 +880,7 @@ int gemm_backward(int dtype, const void* dc, const void* a, const void* b, void*
   if (!workspace || (int64_t)workspace_bytes < p.bytes) return GP_EWORKSPACE;
   if (!is_aligned16(workspace)) return GP_EINVAL;
   if ((r = require_gfx950())) return r;
-  return run_backward(dtype, p, nullptr, false, dc, N, a, b, da, db, M, N, K, (char*)workspace, (hipStream_t)stream);
+  return run_backward(dtype, p, nullptr, false, nullptr, dc, N, a, b, da, db, M, N, K, (char*)workspace, (hipStream_t)stream);
 }
 
 int gemm_gated_backward_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, int want_dx, int want_dw,
@@ -885,7 +921,7 @@ int gemm_gated_backward(int dtype, const void* dh, const void* gate, const void*
   t.Np = (uint32_t)p.Np;
   t.tiles_c = (uint32_t)((F + 63) / 64);
   t.act = act;
-  return run_backward(dtype, p, &t, false, ws + p.off_d, p.Np, x, w, dx, dw, M, 2 * F, H, ws, (hipStream_t)stream);
+  return run_backward(dtype, p, &t, false, nullptr, ws + p.off_d, p.Np, x, w, dx, dw, M, 2 * F, H, ws, (hipStream_t)stream);
 }
 
 }  // extern "C"

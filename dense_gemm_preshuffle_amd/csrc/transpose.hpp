@@ -215,12 +215,54 @@ __device__ __forceinline__ void gate_grad_tile(Tile64& tg, Tile64& tu, const Gat
   if constexpr (!LINEAR) store_transposed(tu, p.dt + (size_t)p.F * p.Mp * 2, c0, r0, p.F, p.Mp);
 }
 
+// A linear layer's bias gradient of few rows, from dy and z themselves: 64 columns a
+// workgroup, all rows of them, 32 at a time. Read twice (they lie in L2), but the sums
+// of row tiles take a launch more.
+struct BiasJob {
+  const char *dy, *z;   // [M][N]; z null: no activation
+  float* db;
+  uint32_t M, N, blocks;
+  int act;
+};
+template <int DT>
+__device__ __forceinline__ void bias_strip(float* red, const BiasJob& p, uint32_t block) {
+  const uint32_t q = threadIdx.x & 7, c0 = block * 64u, c = c0 + 8 * q;
+  float sum[8] = {};
+  with_act(p.z ? p.act : (int)ACT_NONE, [&](auto act_c) GP_INLINE {
+    constexpr int A = decltype(act_c)::value;
+    if (c >= p.N) return;
+#pragma unroll 4
+    for (uint32_t r = threadIdx.x >> 3; r < p.M; r += 32) {
+      const size_t off = ((size_t)r * p.N + c) * 2;
+      const v4i dy = *(const v4i*)(p.dy + off);
+      v4i z = v4i{0, 0, 0, 0};
+      if constexpr (A != ACT_NONE) z = *(const v4i*)(p.z + off);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float value, slope;
+        activate_grad<A>(widen16<DT>((uint32_t)z[i / 2], i & 1), value, slope);
+        sum[i] = fmaf(widen16<DT>((uint32_t)dy[i / 2], i & 1), slope, sum[i]);
+      }
+    }
+  });
+  // the wave's rows through its lanes, the four waves' through LDS, in order
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    for (int o = 8; o < 64; o <<= 1) sum[i] += __shfl_xor(sum[i], o, 64);
+    if ((threadIdx.x & 63) < 8) red[(threadIdx.x >> 6) * 64 + 8 * q + i] = sum[i];
+  }
+  __syncthreads();
+  const uint32_t k = threadIdx.x;
+  if (k < 64 && c0 + k < p.N) p.db[c0 + k] = ((red[k] + red[64 + k]) + red[128 + k]) + red[192 + k];
+}
+
 // Everything the backward products need beforehand, in one launch (a launch costs
 // the host as much as a small pass takes): the pointwise backward, up to three
 // copies, and the arrival counters of K splits set to zero.
 struct PrepArgs {
   GateGradArgs gate;   // blocks 0: none
   CopyJob copy[3];     // blocks 0: none
+  BiasJob bias;        // LINEAR alone; blocks 0: none
   uint32_t* cnt;       // null: none
   uint32_t ncnt;
 };
@@ -243,6 +285,8 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepArgs p) {
     }
     b -= p.copy[i].blocks;
   }
+  if constexpr (LINEAR)
+    if (b < p.bias.blocks) bias_strip<DT>((float*)t0.d, p.bias, b);
 }
 
 // A bias gradient from the row tiles' sums: 32 columns a workgroup, 32 tiles at a
