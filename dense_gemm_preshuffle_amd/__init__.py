@@ -762,6 +762,22 @@ def _here(where, name, t, stream):
         raise ValueError(f"{where}: {name} is on {t.device}, the stream on {stream.device}")
 
 
+@functools.lru_cache(maxsize=None)
+def _compiled():
+    """The compiled marshalling (csrc/marshal.cpp) of calls on the current stream, bound to the library; None where
+    it is not built. Its functions do what the Python below them does, in 1 us and not 5, and return None where
+    anything is not as it should be: the Python then names what."""
+    lib = load_library()
+    try:
+        from . import _marshal
+    except ImportError:
+        return None
+    _marshal.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+        "gemm_norm", "gemm_norm_backward", "gemm_norm_backward_workspace_size", "gemm_linear",
+        "gemm_linear_workspace_size", "gemm_linear_backward", "gemm_linear_backward_workspace_size")))
+    return _marshal
+
+
 # ---- linear layer with its epilogue ----
 
 def gemm_linear_preshuffle(w, dtype, out=None, stream=None):
@@ -806,6 +822,10 @@ def gemm_linear(dtype, x, w_shuf, bias=None, act="none", residual=None, save=Fal
     residual. Without a workspace one is made for the call where the plan needs it."""
     where = "gemm_linear"
     dt, t = _half(dtype)
+    if stream is None and x.is_cuda and (fast := _compiled()) is not None:
+        out = fast.linear(dt, x, w_shuf, bias, _act(act), residual, bool(save), y, z, workspace, _device(), _stream(None))
+        if out is not None:
+            return out
     M, K = shape = x.shape
     index, device = x.get_device(), x.device
     if stream is not None or index < 0 or index != _device():
@@ -862,6 +882,11 @@ def gemm_linear_backward(dtype, dy, z, x, w, act="none", want_dx=True, want_dw=T
 
     where = "gemm_linear_backward"
     dt, t = _half(dtype)
+    if stream is None and dy.is_cuda and (fast := _compiled()) is not None:
+        out = fast.linear_backward(dt, dy, z, x, w, _act(act), bool(want_dx), bool(want_dw), bool(want_dbias), dx, dw, dbias,
+                                   workspace, _device(), _stream(None))
+        if out is not None:
+            return out
     _here(where, "dy", dy, stream)
     M, N = dy.shape
     dev = dy.device
@@ -936,6 +961,11 @@ def gemm_norm(dtype, x, residual=None, scale=1.0, norm_in="none", w_in=None, b_i
     is not stored and None. r may be the residual or x, y may be x."""
     where = "gemm_norm"
     dt, t = _half(dtype)
+    if stream is None and x.is_cuda and (fast := _compiled()) is not None:
+        out = fast.norm(dt, x, residual, scale, _norm(norm_in), w_in, b_in, gate, _norm(norm_out), w_out, b_out, eps,
+                        bool(want_r), r, y, _device(), _stream(None))
+        if out is not None:
+            return out
     M, H = shape = x.shape
     index, dev = x.get_device(), x.device
     if stream is not None or index < 0 or index != _device():
@@ -979,6 +1009,12 @@ def gemm_norm_backward(dtype, dy, dr, x, r, scale=1.0, norm_in="none", w_in=None
     parameters that are given are computed, in fp32."""
     where = "gemm_norm_backward"
     dt, t = _half(dtype)
+    if stream is None and getattr(dr if dy is None else dy, "is_cuda", False) and (fast := _compiled()) is not None:
+        out = fast.norm_backward(dt, dy, dr, x, r, scale, _norm(norm_in), w_in, b_in, gate, _norm(norm_out), w_out, b_out,
+                                 eps, bool(want_dx), bool(want_dresidual), bool(want_params), dx, dresidual, workspace,
+                                 _device(), _stream(None))
+        if out is not None:
+            return NormGrads._make(out)
     lead = dy if dy is not None else dr
     if lead is None:
         raise ValueError(f"{where}: neither dy nor dr is given")

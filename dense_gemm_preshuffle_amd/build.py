@@ -2,9 +2,11 @@
 
     python -m dense_gemm_preshuffle_amd.build        (or build() from Python)
 
-Every translation unit under csrc/ is compiled with hipcc for gfx950 only,
+Every HIP translation unit under csrc/ is compiled with hipcc for gfx950 only,
 in parallel, and linked into dense_gemm_preshuffle_amd/libgemm_preshuffle.so.
-The build fails if any kernel spills registers or uses scratch memory.
+The build fails if any kernel spills registers or uses scratch memory. csrc/marshal.cpp
+(host code against torch's headers) becomes dense_gemm_preshuffle_amd/_marshal.so, a
+module of the Python binding.
 """
 from __future__ import annotations
 
@@ -27,8 +29,10 @@ PROBE_SRCS = [os.path.join(PKG, "probe", f) for f in ("stream_read.hip", "mfma_r
 # probe would then measure instead of the MFMA.
 PROBE_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 PROBE_LIB = os.path.join(PKG, "libgp_probe.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # no packed fp32 (v_pk_*_f32) instructions in any kernel
@@ -81,12 +85,33 @@ def spilling(res: dict) -> list:
     return bad
 
 
+def build_marshal() -> str:
+    """The binding's compiled marshalling, against the installed torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    include = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    tmp = MARSHAL + ".tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in include), os.path.join(CSRC, "marshal.cpp"),
+           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"marshal.cpp failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(jobs: int | None = None, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     jobs = jobs or min(len(srcs), max(1, min(16, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(jobs) as ex:
+        marshal = ex.submit(build_marshal)
         done = list(ex.map(_compile, srcs))
+        marshal.result()
     objs = [o for o, _ in done]
     res = {k: v for _, r in done for k, v in r.items()}
     bad = spilling(res)
@@ -105,13 +130,13 @@ def build(jobs: int | None = None, verbose: bool = False) -> str:
         raise RuntimeError(f"probe build failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, PROBE_LIB)
     if verbose:
-        print(f"built {LIB} and {PROBE_LIB}")
+        print(f"built {LIB}, {PROBE_LIB} and {MARSHAL}")
     return LIB
 
 
 def clean() -> None:
     shutil.rmtree(BUILD, ignore_errors=True)
-    for f in (LIB, PROBE_LIB):
+    for f in (LIB, PROBE_LIB, MARSHAL):
         if os.path.exists(f):
             os.remove(f)
 

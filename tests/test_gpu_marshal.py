@@ -1,0 +1,110 @@
+"""The compiled marshalling of the linear layer's and the norms' calls against the binding's Python: the same results
+and the same refusals."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def _calls():
+    import torch
+
+    import dense_gemm_preshuffle_amd as gp
+
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    normal = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    half = lambda *s: normal(*s).bfloat16()
+    x, res, z, dy, w = half(40, 512), half(40, 336), half(40, 336), half(40, 336), half(336, 512)
+    w_shuf, bias = gp.gemm_linear_preshuffle(w, "bf16"), normal(336)
+    long = half(40, 6720)
+    long_w = gp.gemm_linear_preshuffle(half(336, 6720), "bf16")
+    ws = gp.linear_workspace("bf16", 40, 336, 6720)
+    a, b, c, d = (half(12, 264) for _ in range(4))
+    v = [normal(264) for _ in range(4)]
+    gate = normal(3, 264)
+    kw = dict(norm_in="rms", w_in=v[0], b_in=v[1], gate=gate, norm_out="layer", w_out=v[2], b_out=v[3], scale=0.5, eps=1e-5)
+    nws = gp.norm_backward_workspace("bf16", 12, 264, 3)
+    lws = gp.linear_backward_workspace("bf16", 40, 336, 512)
+    y, r = torch.empty_like(res), torch.empty_like(a)
+    return {
+        "linear": lambda: gp.gemm_linear("bf16", x, w_shuf),
+        "linear all": lambda: gp.gemm_linear("bf16", x, w_shuf, bias=bias, act="gelu", residual=res, save=True, y=y),
+        "linear split": lambda: gp.gemm_linear("bf16", long, long_w, workspace=ws),
+        "linear own workspace": lambda: gp.gemm_linear("bf16", long, long_w),
+        "linear backward": lambda: gp.gemm_linear_backward("bf16", dy, z, x, w, act="silu"),
+        "linear backward one": lambda: gp.gemm_linear_backward("bf16", dy, None, x, None, want_dx=False, want_dbias=False, workspace=lws),
+        "linear backward bias": lambda: gp.gemm_linear_backward("bf16", dy, None, None, None, want_dx=False, want_dw=False),
+        "norm": lambda: gp.gemm_norm("bf16", a),
+        "norm all": lambda: gp.gemm_norm("bf16", a, residual=b, r=r, **kw),
+        "norm y": lambda: gp.gemm_norm("bf16", a, residual=b, want_r=False, **kw),
+        "norm r": lambda: gp.gemm_norm("bf16", a, norm_in="rms", norm_out="none"),
+        "norm backward": lambda: gp.gemm_norm_backward("bf16", a, b, c, d, **kw),
+        "norm backward workspace": lambda: gp.gemm_norm_backward("bf16", a, None, c, d, workspace=nws, dx=r, **kw),
+        "norm backward data": lambda: gp.gemm_norm_backward("bf16", a, b, None, d, want_params=False, want_dresidual=False),
+        # refused
+        "type": lambda: gp.gemm_linear("bf16", x.half(), w_shuf), "rows": lambda: gp.gemm_linear("bf16", x, w_shuf, residual=res[:4]),
+        "z": lambda: gp.gemm_linear("bf16", x, w_shuf, z=z), "host": lambda: gp.gemm_norm("bf16", a.cpu()),
+        "stride": lambda: gp.gemm_norm("bf16", a[:, ::2]), "gate": lambda: gp.gemm_norm("bf16", a, gate=normal(5, 264)),
+        "vector": lambda: gp.gemm_norm("bf16", a, w_out=normal(263)), "half vector": lambda: gp.gemm_norm("bf16", a, w_out=half(264)),
+        "eps": lambda: gp.gemm_norm("bf16", a, eps=-1.0), "nothing": lambda: gp.gemm_norm("bf16", a, want_r=False, norm_out="none"),
+        "1-d": lambda: gp.gemm_norm("bf16", a[0]), "empty": lambda: gp.gemm_norm("bf16", a[:0]),
+        "small workspace": lambda: gp.gemm_norm_backward("bf16", a, b, c, d, workspace=nws[:64], **kw),
+        "dx": lambda: gp.gemm_norm_backward("bf16", a, b, c, d, want_dx=False, dx=r, **kw),
+        "w": lambda: gp.gemm_linear_backward("bf16", dy, None, x, w[:, :256]), "x": lambda: gp.gemm_linear_backward("bf16", dy, None, None, w),
+        "no z": lambda: gp.gemm_linear_backward("bf16", dy, None, x, w, act="silu"),
+        "list": lambda: gp.gemm_norm("bf16", a, residual=[1.0]),
+    }
+
+
+def _flat(out):
+    import torch
+
+    return [out] if isinstance(out, torch.Tensor) else list(out)
+
+
+def test_both_ways(monkeypatch):
+    import torch
+
+    import dense_gemm_preshuffle_amd as gp
+
+    assert gp._compiled() is not None, "not built"
+    calls = _calls()
+
+    def run():
+        got = {}
+        for name, f in calls.items():
+            try:
+                got[name] = [None if v is None else v.clone() for v in _flat(f())]
+            except Exception as e:
+                got[name] = type(e)
+        return got
+    compiled = run()
+    monkeypatch.setattr(gp, "_compiled", lambda: None)
+    python = run()
+    refused = list(calls).index("type")
+    for i, name in enumerate(calls):
+        a, b = compiled[name], python[name]
+        if i >= refused:
+            assert isinstance(a, type) and a is b, name
+            continue
+        assert len(a) == len(b) and all((p is None) == (q is None) and (p is None or torch.equal(p, q)) for p, q in zip(a, b)), name
+
+
+def test_current_stream():
+    """Calls under torch's stream context run on that stream, and their outputs belong to it."""
+    import torch
+
+    import dense_gemm_preshuffle_amd as gp
+
+    x = torch.randn(300, 4096, device="cuda").bfloat16()
+    want = gp.gemm_norm("bf16", x)[1].clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        big = torch.randn(8192, 8192, device="cuda")
+        for _ in range(5):
+            big = big @ big * 1e-4
+        y = x * 1                    # written after the products on the side stream
+        out = gp.gemm_norm("bf16", y)[1]
+    side.synchronize()
+    assert torch.equal(out, want)
