@@ -8,8 +8,11 @@
 // twice; y is taken from r before r is rounded. Everything between the loads and
 // the one rounding of each output is fp32; a layer norm takes the mean first and
 // the squares of the centred values after it, which a mean far from zero does not
-// spoil. A workgroup takes consecutive rows and keeps the columns' parameters in
-// registers for all of them.
+// spoil. The grid is what the CUs hold at once; a workgroup takes every so-manyth
+// row (the rows under way at a time then lie together: 8192 x 8192 94 us, in runs of rows
+// of a workgroup's own 105), loads the next while it reduces one, and keeps the columns'
+// parameters in registers. Measured (residual, RMS norm): 16384 x 4096 98 us, 5.5 TB/s; 777 x
+// 7168 14.3, there two rows' latency after each other; one row of 4096 3.2.
 #pragma once
 
 #include "gp_common.hpp"
@@ -221,11 +224,13 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_kernel(NormArgs p) {
 // and over the rows, with T1 = sum t n1 and T0 = sum t within each gate row,
 //   dw_out = sum dy n, db_out = sum dy, dgate = w_in T1 + b_in T0,
 //   dw_in = sum gate T1, db_in = sum gate T0,
-// so that four column sums serve all five parameters. A workgroup adds them up over
-// its rows in fp32 (in registers, or in LDS for the longest rows, where a thread
-// alone touches its columns) and stores them once; norm_sums_kernel adds the
-// workgroups' sums in a fixed order. The statistics are taken again from x and r,
-// which are read anyway.
+// so that four column sums serve all five parameters. A workgroup adds them up over its
+// rows (every so-manyth of one gate row) in fp32, in registers, or in LDS for the longest
+// rows, where a thread alone touches its columns, and stores them once; norm_sums_kernel
+// adds the workgroups' sums in a fixed order. The statistics are taken again from x and r,
+// which are read anyway. IN: there is a norm_in or a gate; without them dx is t, and x is
+// not read. Measured, bound by HBM: 16384 x 4096, a gate per sequence and a layer norm, 178 us
+// (805 MB at 4.8 TB/s and the sums, 7 us of them); RMS norm alone 131 us (671 MB, 5.1 TB/s).
 struct NormGradArgs {
   const char *dy, *dr, *x, *r;              // [M][H]; dy null: no norm_out, dr null: none; x, r null: not needed
   const float *w_in, *gate, *w_out;
@@ -308,7 +313,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_grad_kernel(NormGradAr
       for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int h = 0; h < 2; ++h) far_at(k, c, h) = v4f{0.f, 0.f, 0.f, 0.f};
-  // adds a v (or a v w)
+  // adds v (one) or v w to sum k
   auto add = [&](auto k_c, int c, const float (&v)[8], const float (&w)[8], bool one) GP_INLINE {
     constexpr int k = decltype(k_c)::value;
     if constexpr (k < NREG) {
