@@ -433,13 +433,20 @@ TileArgs rows_args(const Plan& p, const void* a, int64_t lda, const void* b, voi
   return g;
 }
 
+int launch_sums(const RowSums& sums, hipStream_t s) {
+  forget_hip_error();
+  hipLaunchKernelGGL(bias_sums_kernel, dim3(sums.blocks), dim3(1024), 0, s, sums);
+  return report_hip(hipGetLastError(), "kernel launch");
+}
+
 // Launches, in order, what has to run once the pointers are valid. dc: the
 // output gradient, rows of ldc elements; gate: the pointwise backward that makes
-// it first (else null; linear: the linear layer's). Stops at the first launch that
-// fails.
+// it first (else null; linear: the linear layer's). bias, sums (null: none): a linear
+// layer's bias gradient, of few rows or from the row tiles' sums. Stops at the first
+// launch that fails.
 int run_backward(int dtype, const BackwardPlan& p, const GateGradArgs* gate, bool linear, const BiasJob* bias,
-                 const void* dc, int64_t ldc, const void* a, const void* b, void* da, void* db, int64_t M, int64_t N,
-                 int64_t K, char* ws, hipStream_t s) {
+                 const RowSums* sums, const void* dc, int64_t ldc, const void* a, const void* b, void* da, void* db,
+                 int64_t M, int64_t N, int64_t K, char* ws, hipStream_t s) {
   PrepArgs t = {};
   uint64_t blocks = 0;
   if (bias) {
@@ -493,7 +500,8 @@ int run_backward(int dtype, const BackwardPlan& p, const GateGradArgs* gate, boo
       rb.part = ws + p.db_part;
     }
     forget_hip_error();
-    return report_hip(bf16 ? launch_pair_bf16(ra, rb, s) : launch_pair_f16(ra, rb, s), "kernel launch");
+    const RowSums last = sums ? *sums : RowSums{};
+    return report_hip(bf16 ? launch_pair_bf16(ra, rb, last, s) : launch_pair_f16(ra, rb, last, s), "kernel launch");
   }
   auto launch_rows = [&](const Plan& plan, const TileArgs& g, bool t) {
     forget_hip_error();
@@ -510,7 +518,7 @@ int run_backward(int dtype, const BackwardPlan& p, const GateGradArgs* gate, boo
                   : launch_gemm(dtype, p.db, ws + p.off_ct, ws + p.off_at, db, N, K, ws, s);
     if (r) return r;
   }
-  return GP_OK;
+  return sums ? launch_sums(*sums, s) : GP_OK;
 }
 
 int plan_gated_backward(int dtype, int64_t M, int64_t F, int64_t H, bool dx, bool dw, BackwardPlan* p) {
@@ -809,26 +817,21 @@ int gemm_linear_backward(int dtype, const void* dy, const void* z, const void* x
   }
   // the pass over dy: where dz is made, or row tiles summed
   const bool pass = (p.made && products) || t.sums;
-  if (products) {
-    r = run_backward(dtype, q, pass ? &t : nullptr, true, p.strips ? &strips : nullptr,
-                     p.made ? (const void*)(ws + q.off_d) : dy, p.made ? q.Np : N, x, w, dx, dw, M, N, K, ws, s);
-  } else {
-    PrepArgs only = {};
-    if (pass) {
-      only.gate = t;
-      only.gate.blocks = tiles64(q.Mp, N);
-    }
-    only.bias = strips;
-    forget_hip_error();
-    auto* prep = dtype == GP_BF16 ? prep_kernel<DT_BF16, true> : prep_kernel<DT_F16, true>;
-    hipLaunchKernelGGL(prep, dim3(only.gate.blocks + only.bias.blocks), dim3(256), 0, s, only);
-    r = report_hip(hipGetLastError(), "kernel launch");
+  const RowSums sums = {t.sums, dbias, (uint32_t)N, (uint32_t)((q.Mp + 63) / 64), (uint32_t)((N + 31) / 32)};
+  if (products)
+    return run_backward(dtype, q, pass ? &t : nullptr, true, p.strips ? &strips : nullptr, t.sums ? &sums : nullptr,
+                        p.made ? (const void*)(ws + q.off_d) : dy, p.made ? q.Np : N, x, w, dx, dw, M, N, K, ws, s);
+  PrepArgs only = {};
+  if (pass) {
+    only.gate = t;
+    only.gate.blocks = tiles64(q.Mp, N);
   }
-  if (r || !t.sums) return r;
+  only.bias = strips;
   forget_hip_error();
-  hipLaunchKernelGGL(bias_sums_kernel, dim3((uint32_t)((N + 31) / 32)), dim3(1024), 0, s, (const float*)t.sums, dbias,
-                     (uint32_t)N, (uint32_t)((q.Mp + 63) / 64));
-  return report_hip(hipGetLastError(), "kernel launch");
+  auto* prep = dtype == GP_BF16 ? prep_kernel<DT_BF16, true> : prep_kernel<DT_F16, true>;
+  hipLaunchKernelGGL(prep, dim3(only.gate.blocks + only.bias.blocks), dim3(256), 0, s, only);
+  r = report_hip(hipGetLastError(), "kernel launch");
+  return r || !t.sums ? r : launch_sums(sums, s);
 }
 
 int gemm_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int want_da, int want_db, size_t* bytes) {
@@ -880,7 +883,7 @@ int gemm_backward(int dtype, const void* dc, const void* a, const void* b, void*
   if (!workspace || (int64_t)workspace_bytes < p.bytes) return GP_EWORKSPACE;
   if (!is_aligned16(workspace)) return GP_EINVAL;
   if ((r = require_gfx950())) return r;
-  return run_backward(dtype, p, nullptr, false, nullptr, dc, N, a, b, da, db, M, N, K, (char*)workspace, (hipStream_t)stream);
+  return run_backward(dtype, p, nullptr, false, nullptr, nullptr, dc, N, a, b, da, db, M, N, K, (char*)workspace, (hipStream_t)stream);
 }
 
 int gemm_gated_backward_workspace_size(int dtype, int64_t M, int64_t F, int64_t H, int want_dx, int want_dw,
@@ -921,7 +924,7 @@ int gemm_gated_backward(int dtype, const void* dh, const void* gate, const void*
   t.Np = (uint32_t)p.Np;
   t.tiles_c = (uint32_t)((F + 63) / 64);
   t.act = act;
-  return run_backward(dtype, p, &t, false, nullptr, ws + p.off_d, p.Np, x, w, dx, dw, M, 2 * F, H, ws, (hipStream_t)stream);
+  return run_backward(dtype, p, &t, false, nullptr, nullptr, ws + p.off_d, p.Np, x, w, dx, dw, M, 2 * F, H, ws, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -1208,19 +1208,30 @@ __global__ __launch_bounds__(64 * tile_waves(TM, TN) * KG, tile_wgs_per_cu(TM, T
 }
 
 // Both products of a backward pass in one launch, on 64 x 128 tiles, for sizes at
-// which either alone leaves CUs idle: workgroups [0, na) compute a (EPI_ROWS),
-// those from na8 on (na rounded up to a multiple of 8, the XCDs) b (EPI_ROWS_T).
+// which either alone leaves CUs idle: a (EPI_ROWS) and b (EPI_ROWS_T), first the one
+// whose workgroups go over more of K, on workgroups [0, n), the other from n8 on (n
+// rounded up to a multiple of 8, the XCDs); a linear layer's bias gradient behind both,
+// where other workgroups end.
 struct PairArgs {
   TileArgs a, b;
-  uint32_t na, na8;
+  RowSums bias;
+  uint32_t n, n8, b_first, end;   // end: first workgroup of the bias gradient
 };
 template <int DT>
 __global__ __launch_bounds__(256, 2) void gemm_pair_kernel(PairArgs p) {
   constexpr int LA = TileCfg<DT, 16, 64, 128, 128, EPI_ROWS, 3>::LDS, LB = TileCfg<DT, 16, 64, 128, 128, EPI_ROWS_T, 3>::LDS;
   __shared__ __attribute__((aligned(16))) char lds[LA > LB ? LA : LB];
-  const uint32_t w = blockIdx.x;
-  if (w < p.na) gemm_tile_body<DT, 16, 64, 128, 128, EPI_ROWS, 3, false, 1, true, true>(p.a, w, lds);
-  else if (w >= p.na8) gemm_tile_body<DT, 16, 64, 128, 128, EPI_ROWS_T, 3, false, 1, true, true>(p.b, w - p.na8, lds);
+  static_assert(sizeof(lds) >= sizeof(float[32][33]), "LDS of the sums");
+  uint32_t w = blockIdx.x;
+  if (w >= p.end) {
+    row_sums_block<256>((float(*)[33])lds, p.bias, w - p.end);
+    return;
+  }
+  const bool second = w >= p.n8;
+  if (!second && w >= p.n) return;
+  if (second) w -= p.n8;
+  if (second == (p.b_first != 0)) gemm_tile_body<DT, 16, 64, 128, 128, EPI_ROWS, 3, false, 1, true, true>(p.a, w, lds);
+  else gemm_tile_body<DT, 16, 64, 128, 128, EPI_ROWS_T, 3, false, 1, true, true>(p.b, w, lds);
 }
 
 }  // namespace gp

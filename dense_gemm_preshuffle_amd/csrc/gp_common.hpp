@@ -361,6 +361,36 @@ __device__ __forceinline__ double wave_sum64(double v) {
   return wave_reduce64(v, [](double a, double b) GP_INLINE { return a + b; });
 }
 
+// Sums of the rows of sums [tiles][N] into db [N]: 32 columns c0 .. c0 + 31, 32 partial
+// sums each of every 32nd row, then those in order, on any number of threads (the same
+// bits). red: 32 x 33 floats of LDS.
+struct RowSums {
+  const float* sums;
+  float* db;
+  uint32_t N, tiles, blocks;   // blocks: workgroups, one per 32 columns; 0: none
+};
+template <int THREADS>
+__device__ __forceinline__ void row_sums_block(float (*red)[33], const RowSums& p, uint32_t block) {
+  constexpr int G = THREADS / 32, EACH = 32 / G;
+  const uint32_t lane = threadIdx.x & 31, row = threadIdx.x >> 5, c = block * 32u + lane;
+  float s[EACH] = {};
+  if (c < p.N) {
+#pragma unroll(4 / EACH > 0 ? 4 / EACH : 1)
+    for (uint32_t q = row; q < p.tiles; q += 32)
+#pragma unroll
+      for (int e = 0; e < EACH; ++e)
+        if (e == 0 || q + e * G < p.tiles) s[e] += p.sums[(size_t)(q + e * G) * p.N + c];
+  }
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) red[row + e * G][lane] = s[e];
+  __syncthreads();
+  if (row != 0 || c >= p.N) return;
+  float total = s[0];
+#pragma unroll
+  for (int q = 1; q < 32; ++q) total += red[q][lane];
+  p.db[c] = total;
+}
+
 // The value of x, hidden from the optimizer: every quantity derived from the
 // result is computed where this call stands. Used at the start of epilogues
 // so that their per-lane addresses are not hoisted above the K loop, where

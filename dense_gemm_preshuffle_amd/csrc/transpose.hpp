@@ -109,6 +109,19 @@ __device__ __forceinline__ void activate_grad(float g, float& value, float& slop
   }
 }
 
+// Of 8 columns' partial sums on lanes 8 apart (lane % 8: the columns): the total of column
+// lane / 8. At each step a lane sends the half of its columns that it gives up: 7
+// exchanges, where every lane's totals of all 8 would take 24.
+__device__ __forceinline__ float sum_over_rows(const float (&sum)[8]) {
+  const bool h2 = threadIdx.x & 32, h1 = threadIdx.x & 16, h0 = threadIdx.x & 8;
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = (h2 ? sum[4 + i] : sum[i]) + __shfl_xor(h2 ? sum[i] : sum[4 + i], 32, 64);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) b[i] = (h1 ? a[2 + i] : a[i]) + __shfl_xor(h1 ? a[i] : a[2 + i], 16, 64);
+  return (h0 ? b[1] : b[0]) + __shfl_xor(h0 ? b[0] : b[1], 8, 64);
+}
+
 // The gated block's pointwise backward: from dh, gate and up ([M][F]),
 //   dg = dh * up * act'(gate), du = dh * act(gate)
 // in fp32, rounded once to the 16-bit type the matrix products read (the
@@ -196,11 +209,8 @@ __device__ __forceinline__ void gate_grad_tile(Tile64& tg, Tile64& tu, const Gat
     if (p.sums) {
       // the wave's 16 rows through its lanes (q is lane % 8), the four waves' through LDS, in order
       float* red = (float*)tu.d;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        for (int o = 8; o < 64; o <<= 1) sum[i] += __shfl_xor(sum[i], o, 64);
-        if ((threadIdx.x & 63) < 8) red[(threadIdx.x >> 6) * 64 + 8 * q + i] = sum[i];
-      }
+      const float own = sum_over_rows(sum);
+      red[(threadIdx.x & 192) + 8 * q + (threadIdx.x >> 3 & 7)] = own;
       __syncthreads();
       const uint32_t k = threadIdx.x;
       if (k < 64 && c0 + k < p.F)
@@ -246,11 +256,8 @@ __device__ __forceinline__ void bias_strip(float* red, const BiasJob& p, uint32_
     }
   });
   // the wave's rows through its lanes, the four waves' through LDS, in order
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    for (int o = 8; o < 64; o <<= 1) sum[i] += __shfl_xor(sum[i], o, 64);
-    if ((threadIdx.x & 63) < 8) red[(threadIdx.x >> 6) * 64 + 8 * q + i] = sum[i];
-  }
+  const float own = sum_over_rows(sum);
+  red[(threadIdx.x & 192) + 8 * q + (threadIdx.x >> 3 & 7)] = own;
   __syncthreads();
   const uint32_t k = threadIdx.x;
   if (k < 64 && c0 + k < p.N) p.db[c0 + k] = ((red[k] + red[64 + k]) + red[128 + k]) + red[192 + k];
@@ -289,22 +296,10 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepArgs p) {
     if (b < p.bias.blocks) bias_strip<DT>((float*)t0.d, p.bias, b);
 }
 
-// A bias gradient from the row tiles' sums: 32 columns a workgroup, 32 tiles at a
-// time, then those in order.
-static __global__ __launch_bounds__(1024) void bias_sums_kernel(const float* sums, float* db, uint32_t N, uint32_t tiles) {
+// A bias gradient from the row tiles' sums.
+static __global__ __launch_bounds__(1024) void bias_sums_kernel(RowSums p) {
   __shared__ float red[32][33];
-  const uint32_t lane = threadIdx.x & 31, row = threadIdx.x >> 5, c = blockIdx.x * 32u + lane;
-  float s = 0.f;
-  if (c < N) {
-#pragma unroll 4
-    for (uint32_t q = row; q < tiles; q += 32) s += sums[(size_t)q * N + c];
-  }
-  red[row][lane] = s;
-  __syncthreads();
-  if (row != 0 || c >= N) return;
-#pragma unroll
-  for (int q = 1; q < 32; ++q) s += red[q][lane];
-  db[c] = s;
+  row_sums_block<1024>(red, p, blockIdx.x);
 }
 
 }  // namespace gp
