@@ -371,11 +371,11 @@ struct RowSums {
 };
 template <int THREADS>
 __device__ __forceinline__ void row_sums_block(float (*red)[33], const RowSums& p, uint32_t block) {
-  constexpr int G = THREADS / 32, EACH = 32 / G;
+  constexpr int G = THREADS / 32, EACH = 32 / G, U = EACH < 4 ? 4 : 1;
   const uint32_t lane = threadIdx.x & 31, row = threadIdx.x >> 5, c = block * 32u + lane;
   float s[EACH] = {};
   if (c < p.N) {
-#pragma unroll(4 / EACH > 0 ? 4 / EACH : 1)
+#pragma unroll U
     for (uint32_t q = row; q < p.tiles; q += 32)
 #pragma unroll
       for (int e = 0; e < EACH; ++e)
