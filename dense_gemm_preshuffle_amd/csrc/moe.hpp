@@ -17,7 +17,8 @@ namespace gp {
 // depend on the order of a sum (the products of 16-bit values are exact; an fp32 sum
 // of 4096 is off by 1e-6, as far as two of 128 scores lie apart once in some
 // thousand tokens). A workgroup takes EB experts and TB tokens; the last of a token
-// block to finish chooses for its tokens, a wave for each.
+// block to finish chooses for its tokens, a wave for each. Bound by latency: one token,
+// 8 of 64 experts, H 2048 5.8 us (0.26 MB; 2 of them launch, 2 the arrival and the choice).
 struct RouteArgs {
   const char *x, *wr;       // [M][H], [E][H]
   const float* bias;        // [E] added for the choice alone, or null
@@ -255,6 +256,8 @@ __device__ __forceinline__ uint32_t list_pairs(const MoeArgs& p, uint32_t slot, 
 // groups of S chunks of weights in flight; x passes through a piece of LDS of the
 // wave's own. XL: 16-byte loads of a per lane and chunk, 8 XL rows at a time; 0: one
 // row. Longer lists take further turns, which find the weights in L2 or read them again.
+// Measured: 33 tokens, 2 of 8 experts of 4096 x 14336, up 313 us (1.88 GB, 6.0 TB/s), down
+// 145 (0.94 GB, 6.5 TB/s); one token, 8 of 64 of 2048 x 1024, up 13.2 (67 MB, 5.1 TB/s).
 template <int DT, int XL, int NB, int WAVES, int S, bool UP>
 __global__ __launch_bounds__(WAVES * 64) void moe_kernel(MoeArgs p) {
   constexpr bool ONE = XL == 0;
@@ -431,7 +434,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_kernel(MoeArgs p) {
 // The down product of one token: its k experts' products are one of K = k Ka. WAVES waves
 // split those chunks, so that a workgroup's columns are finished by itself: no partial
 // products in memory and no arrival, which take the general form 3 us of 11 (8 experts of
-// 2048 x 1024).
+// 2048 x 1024: 8.4 us, 4.0 TB/s; launch and the waves' join are 2.5 of them).
 template <int DT, int NB, int WAVES, int S>
 __global__ __launch_bounds__(WAVES * 64) void moe_down_one_kernel(MoeArgs p) {
   __shared__ __attribute__((aligned(16))) char lds[WAVES * NB * 1024];

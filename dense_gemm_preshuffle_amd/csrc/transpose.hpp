@@ -136,7 +136,8 @@ __device__ __forceinline__ float sum_over_rows(const float (&sum)[8]) {
 // (gate; null without an activation):
 //   d = dy * act'(z)   [M][Np], zeros from F to Np,   dt = d^T [F][Mp]
 // and, where sums is not null, the sum of d over each tile's 64 rows in fp32, before
-// its rounding ([row tiles][F]; bias_sums_kernel adds them up).
+// its rounding ([row tiles][F]; RowSums adds them up). 2000 x 7168, GELU, with a copy of x
+// (2048 columns) 25 us, 104 MB at 4.1 TB/s; the sums another 4 us where they are a launch.
 struct GateGradArgs {
   const char *dh, *gate, *up;
   char *d, *dt;
