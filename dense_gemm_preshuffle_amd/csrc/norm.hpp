@@ -12,7 +12,7 @@
 // row (the rows under way at a time then lie together: 8192 x 8192 94 us, in runs of rows
 // of a workgroup's own 105), loads the next while it reduces one, and keeps the columns'
 // parameters in registers. Measured (residual, RMS norm): 16384 x 4096 98 us, 5.5 TB/s; 777 x
-// 7168 14.3, there two rows' latency after each other; one row of 4096 3.2.
+// 7168 11.1 (4.0 TB/s: three or four rows after each other on a CU); one row of 4096 3.2.
 #pragma once
 
 #include "gp_common.hpp"
