@@ -153,9 +153,10 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor dw_in = grad(w_in, vec), db_in = grad(b_in, vec), dgate = grad(g, gate_sizes), dw_out = grad(w_out, vec),
                      db_out = grad(b_out, vec);
     at::Tensor ws;
-    if (const at::Tensor* t = p.tensor(19)) {
-      if (t->device() != p.device || !t->is_contiguous()) return none();
-      ws = *t;
+    const at::Tensor* given = p.tensor(19);
+    if (!p.ok || (given && (given->device() != p.device || !given->is_contiguous()))) return none();
+    if (given) {
+      ws = *given;
     } else if (params && (w_in || b_in || g || w_out || b_out)) {
       size_t bytes = 0;
       if (p_norm_backward_size(dt, M, H, gates, &bytes)) return none();
@@ -191,7 +192,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* stream = (void*)p.num(11);
     if (!p.ok || (a[8] != Py_None && !save)) return none();
     const at::Tensor* ws = p.tensor(9);
-    if (ws && (ws->device() != p.device || !ws->is_contiguous())) return none();
+    if (!p.ok || (ws && (ws->device() != p.device || !ws->is_contiguous()))) return none();
     size_t need = 0;   // (without a workspace a call that needs one makes it in Python)
     if (!ws && (p_linear_size(dt, M, N, K, &need) || need)) return none();
     const at::Tensor y = output(p, 7, true, rows, x->options()), z = output(p, 8, save, rows, x->options());
@@ -225,9 +226,10 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if ((want_dx && !wd) || (want_dw && !xd) || (act && !zd)) return none();
     const at::TensorOptions half = dy->options();
     at::Tensor ws;
-    if (const at::Tensor* t = p.tensor(12)) {
-      if (t->device() != p.device || !t->is_contiguous()) return none();
-      ws = *t;
+    const at::Tensor* given = p.tensor(12);
+    if (!p.ok || (given && (given->device() != p.device || !given->is_contiguous()))) return none();
+    if (given) {
+      ws = *given;
     } else {
       size_t bytes = 0;
       if (p_linear_backward_size(dt, M, N, K, act, want_dx, want_dw, want_db, &bytes)) return none();

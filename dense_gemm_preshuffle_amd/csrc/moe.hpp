@@ -199,7 +199,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
   if constexpr (TB == 1) {
     // one wave stores, arrives and chooses: no barrier (as last_to_arrive otherwise)
     if (wave != 0) return;
-    __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xF << 8));   // vmcnt(0): the logits are stored
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the logits are stored
     uint32_t before = 0;
     if (lane == 0) before = __hip_atomic_fetch_add(p.cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if ((uint32_t)__builtin_amdgcn_readfirstlane((int)before) != gridDim.x - 1) return;

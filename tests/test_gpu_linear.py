@@ -113,7 +113,8 @@ def test_rows_do_not_mix(dtype, M):
 
 
 BACKWARD = [(1, 32, 32), (3, 64, 16), (130, 2048, 2064), (300, 272, 80), (70, 1040, 1040), (4100, 544, 1040), (1, 16, 32), (2, 96, 96), (31, 544, 160), (31, 528, 160), (130, 2064, 2048), (4100, 1040, 512), (33, 1056, 544), (65, 2080, 160), (130, 2080, 2048), (257, 1056, 1024),
-            (500, 512, 4096), (1000, 4128, 256), (2049, 1024, 1024), (4100, 992, 512)]
+            (500, 512, 4096), (1000, 4128, 256), (2049, 1024, 1024), (4100, 992, 512),
+            (2300, 480, 1376), (3001, 256, 2048)]   # dw's workgroups the longer ones of the launch of both
 
 
 @pytest.mark.parametrize("dtype", F64.TYPES)

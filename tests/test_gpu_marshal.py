@@ -53,6 +53,9 @@ def _calls():
         "w": lambda: gp.gemm_linear_backward("bf16", dy, None, x, w[:, :256]), "x": lambda: gp.gemm_linear_backward("bf16", dy, None, None, w),
         "no z": lambda: gp.gemm_linear_backward("bf16", dy, None, x, w, act="silu"),
         "list": lambda: gp.gemm_norm("bf16", a, residual=[1.0]),
+        "workspace list": lambda: gp.gemm_linear("bf16", x, w_shuf, workspace=[1]),
+        "backward workspace list": lambda: gp.gemm_linear_backward("bf16", dy, None, x, w, workspace=[1]),
+        "norm workspace list": lambda: gp.gemm_norm_backward("bf16", a, b, c, d, workspace=[1], **kw),
     }
 
 
