@@ -57,11 +57,25 @@ NormPlan plan_norm(int64_t M, int64_t H) {
   return p;
 }
 
-NormPlan plan_norm_grad(int64_t M, int64_t H, int64_t gates) {
+// Backward: fewer, since each workgroup writes its columns' sums, 16 bytes a column, and
+// the next launch reads them, where a row's element takes 12 in all: one per CU of 8
+// waves and more, two of fewer waves, and two of 8 where a norm_in's reductions want
+// something beside them and the rows are many. Measured us (both launches, a norm_out
+// alone unless named): 16384 x 4096 169 with 256 workgroups, 184 with 512; 2000 x 4096
+// 26.0 and 31.2; with a norm_in 1500 x 4096 25.2 and 28.6, 2500 x 4096 33.4 and 34.7, 4000 x
+// 3000 53.0 and 46.5; 16384 x 2048 with a norm_in 121 with 256, 82 with 512, 91 with 1024;
+// 8192 x 512 15.1 with 512, 17.0 with 1024. Of those no more than share the rows evenly:
+// 332 x 8680 23.3 with 166, 25.6 with 256. A workgroup stays within one gate row; where whole
+// shares of the gate rows would leave a quarter of the CUs idle there is one more each.
+NormPlan plan_norm_grad(int64_t M, int64_t H, int64_t gates, int norm_in) {
   NormPlan p;
   row_shape(M, H, &p);
-  const int64_t rpw = norm_threads(p.wpr) / (64 * p.wpr), G = std::max<int64_t>(gates, 1), of_gate = M / G;
-  p.per_gate = std::min(std::max<int64_t>(resident(p) / G, 1), (of_gate + rpw - 1) / rpw);
+  const int64_t rpw = norm_threads(p.wpr) / (64 * p.wpr), G = std::max<int64_t>(gates, 1);
+  const int64_t per_cu = p.wpr < 8 || (p.wpr * p.c == 8 && norm_in != GP_NORM_NONE && M >= 3000) ? 2 : 1;
+  const int64_t turns = (M / G + rpw - 1) / rpw;   // of one workgroup's, all rows of a gate row
+  const int64_t cus = 256 * per_cu, whole = std::max<int64_t>(cus / G, 1);
+  const int64_t most = whole * G < cus * 3 / 4 ? whole + 1 : whole, each = (turns + most - 1) / most;
+  p.per_gate = (turns + each - 1) / each;
   p.wgs = G * p.per_gate;
   return p;
 }
@@ -139,7 +153,8 @@ int gemm_norm_backward_workspace_size(int dtype, int64_t M, int64_t H, int64_t g
   if (!bytes) return GP_EINVAL;
   const int e = check_norm(dtype, M, H, gates);
   if (e) return e;
-  *bytes = (size_t)(plan_norm_grad(M, H, gates).wgs * 4 * H * 4);
+  // (the most that any norm_in takes)
+  *bytes = (size_t)(plan_norm_grad(M, H, gates, GP_NORM_RMS).wgs * 4 * H * 4);
   return GP_OK;
 }
 
@@ -162,7 +177,7 @@ int gemm_norm_backward(int dtype, const void* dy, const void* dr, const void* x,
     return GP_EINVAL;
   int e = check_norm(dtype, M, H, gates);
   if (e) return e;
-  const NormPlan p = plan_norm_grad(M, H, gates);
+  const NormPlan p = plan_norm_grad(M, H, gates, norm_in);
   const bool sums = dw_in || db_in || dgate || dw_out || db_out;
   if (sums && (!workspace || (int64_t)workspace_bytes < p.wgs * 4 * H * 4)) return GP_EWORKSPACE;
   if ((e = require_gfx950())) return e;

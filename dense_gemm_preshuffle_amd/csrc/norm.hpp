@@ -229,8 +229,8 @@ __global__ __launch_bounds__(norm_threads(WPR)) void norm_kernel(NormArgs p) {
 // rows, where a thread alone touches its columns, and stores them once; norm_sums_kernel
 // adds the workgroups' sums in a fixed order. The statistics are taken again from x and r,
 // which are read anyway. IN: there is a norm_in or a gate; without them dx is t, and x is
-// not read. Measured, bound by HBM: 16384 x 4096, a gate per sequence and a layer norm, 178 us
-// (805 MB at 4.8 TB/s and the sums, 7 us of them); RMS norm alone 131 us (671 MB, 5.1 TB/s).
+// not read. Measured, bound by HBM: 16384 x 4096, a gate per sequence and a layer norm, 169 us
+// (805 MB at 4.8 TB/s, the sums' launch among them).
 struct NormGradArgs {
   const char *dy, *dr, *x, *r;              // [M][H]; dy null: no norm_out, dr null: none; x, r null: not needed
   const float *w_in, *gate, *w_out;
