@@ -68,6 +68,15 @@ constexpr TileTime kGatedTimes[] = {{256, 256, 1.02, 15.4, 0}, {128, 256, 0.56, 
 //     128 x 256 in two ranges. The gated product's times would choose 3% above, 35% at worst.
 constexpr TileTime kLinearTimes[] = {{256, 256, 0.72, 32.0, 0}, {128, 256, 0.533, 8.0, 3.45}, {128, 128, 0.41, 2.5, 2.3},
                                      {64, 128, 0.325, 0.6, 1.25}};
+// the linear layer's backward products on row-major operands, dx and dw: 160 shapes (M 200
+//     to 8192, N and K 512 to 14336, fp16) on every tile with up to 8 ranges: dx 1.4% above
+//     the best on average, 19% at worst, dw 0.7% and 23%; by kRowsTimes 3.4% and 5.2%. dx of
+//     2000 x 7168 x 2048 65 on 128 x 128, 76 on 256 x 256 in four ranges; 2636 x 4672 x 6432 192
+//     on 128 x 128, 246 on 256 x 256; dw of 6044 x 1600 x 11136 279 on 128 x 128, 340.
+constexpr TileTime kLinearDxTimes[] = {{256, 256, 1.23, 8.9, 2.19}, {128, 256, 0.73, 3.44, 2.35}, {128, 128, 0.416, 1.55, 1.76},
+                                       {64, 128, 0.334, 0.854, 0.796}};
+constexpr TileTime kLinearDwTimes[] = {{256, 256, 1.13, 8.68, 2.66}, {128, 256, 0.735, 3.01, 2.48}, {128, 128, 0.362, 1.52, 1.6},
+                                       {64, 128, 0.276, 0.893, 0.585}};
 double tile_us(const TileTime& t, int64_t M, int64_t N, int64_t Kb, int64_t ks, double speed = 1.0) {
   const double fill = (double)(((M + t.tm - 1) / t.tm) * ((N + t.tn - 1) / t.tn) * ks) / 256;
   const double rounds = fill <= 4 ? std::ceil(fill) : fill + 0.5;
@@ -270,11 +279,11 @@ int64_t pad_k(int64_t k) {
 // (M 1 to 2821) da took 0.20 to 0.92 of the time that it takes from copies, db 0.58
 // to 1.02 (a as it is: 10 x 10304 x 4480 25.0 us, from copies 117; 29 x 224 x 1728 db
 // 11.9, 11.8).
-bool plan_rows(int64_t M, int64_t N, int64_t Kb, const Plan* other, double copied, Plan* p, double* took,
-               double* took_copies) {
-  const double us = *took = *took_copies = choose_tile_us(kRowsTimes, M, N, Kb, false, p);
+bool plan_rows(const TileTime (&times)[4], int64_t M, int64_t N, int64_t Kb, const Plan* other, double copied, Plan* p,
+               double* took, double* took_copies) {
+  const double us = *took = *took_copies = choose_tile_us(times, M, N, Kb, false, p);
   if (!other || other->kernel != GP_KERNEL_TILE) return true;
-  for (const TileTime& t : kRowsTimes)
+  for (const TileTime& t : times)
     if (t.tm == other->tm && t.tn == other->tn)
       return us <= (*took_copies = tile_us(t, M, N, Kb, other->ks, 0.85) + copied / 4.9e6);
   return true;
@@ -338,10 +347,12 @@ int make_backward_plan(int dtype, int64_t M, int64_t N, int64_t K, bool want_da,
   Plan copies, copies_b;   // (one each: the planner sets what differs from a new Plan)
   double us_a = 0, us_b = 0, copies_a_us = 0, copies_b_us = 0;
   int r = plan_gemm(dtype, M, K, p->Np, &copies);
-  p->da_rows = plan_rows(M, K, 2 * whole_k(p->Np), r ? nullptr : &copies, 4.0 * p->Np * K, &p->da, &us_a, &copies_a_us);
+  p->da_rows = plan_rows(linear ? kLinearDxTimes : kRowsTimes, M, K, 2 * whole_k(p->Np), r ? nullptr : &copies,
+                         4.0 * p->Np * K, &p->da, &us_a, &copies_a_us);
   if (!p->da_rows) p->da = copies;
   r = plan_gemm(dtype, N, K, p->Mp, &copies_b);
-  p->db_rows = plan_rows(K, N, 2 * p->Mp, r ? nullptr : &copies_b, (gated ? 2.0 : 4.0) * p->Mp * N, &p->db, &us_b, &copies_b_us);
+  p->db_rows = plan_rows(linear ? kLinearDwTimes : kRowsTimes, K, N, 2 * p->Mp, r ? nullptr : &copies_b,
+                         (gated ? 2.0 : 4.0) * p->Mp * N, &p->db, &us_b, &copies_b_us);
   if (!p->db_rows) p->db = copies_b;
   if (linear) {
     us_a = std::min(us_a, copies_a_us);
