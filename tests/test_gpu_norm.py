@@ -38,7 +38,10 @@ SHAPES = [(1, 8, 0, "none", "rms"), (1, 4096, 1, "rms", "layer"), (3, 512, 3, "l
           (130, 1024, 0, "rms", "rms"), (64, 1032, 32, "layer", "layer"), (257, 2048, 1, "none", "rms"), (18, 2056, 9, "rms", "none"),
           (256, 4096, 256, "layer", "rms"), (77, 4104, 0, "none", "layer"), (33, 8192, 1, "rms", "layer"),
           (12, 8200, 4, "layer", "rms"), (40, 16384, 2, "rms", "layer"), (9000, 264, 6, "rms", "rms"),
-          (2500, 2048, 5, "none", "layer"), (600, 16384, 1, "layer", "rms")]
+          (2500, 2048, 5, "none", "layer"), (600, 16384, 1, "layer", "rms"),
+          # rows shared unevenly by gate rows that leave CUs idle; both sides of 3000 rows
+          (129 * 5, 264, 129, "none", "rms"), (86 * 7, 4096, 86, "rms", "layer"), (200 * 3, 8200, 200, "none", "layer"),
+          (2999, 2568, 0, "rms", "rms"), (3000, 2568, 0, "rms", "rms")]
 
 
 @pytest.mark.parametrize("dtype", F64.TYPES)
