@@ -866,7 +866,8 @@ def gemm_linear_backward_workspace_size(dtype, M: int, N: int, K: int, act="silu
 
 def linear_backward_workspace(dtype, M: int, N: int, K: int, act="silu", want_dx=True, want_dw=True, want_dbias=True,
                               device="cuda"):
-    """A device workspace for gemm_linear_backward (its contents need not be set)."""
+    """A device workspace for gemm_linear_backward (its contents need not be set); one for any activation serves
+    act="none" too."""
     import torch
 
     return torch.empty(gemm_linear_backward_workspace_size(dtype, M, N, K, act, want_dx, want_dw, want_dbias),

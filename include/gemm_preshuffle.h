@@ -516,7 +516,8 @@ int gemm_linear_backward(int dtype, const void* dy, const void* z, const void* x
                          void* dw, float* dbias, int64_t M, int64_t N, int64_t K, void* workspace,
                          size_t workspace_bytes, void* stream);
 
-/* Host-only: the workspace bytes of gemm_linear_backward. */
+/* Host-only: the workspace bytes of gemm_linear_backward. Those of any activation serve
+ * act GP_ACT_NONE too. */
 int gemm_linear_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int act, int want_dx, int want_dw,
                                         int want_dbias, size_t* bytes);
 

@@ -151,6 +151,28 @@ def test_backward(dtype, M, N, K):
         assert got[0] is None and got[1] is None and torch.equal(got[2], db[0])
 
 
+@pytest.mark.parametrize("M,N,K", [(2706, 32, 8608), (3870, 3808, 9376)])
+def test_backward_without_an_activation_on_the_default_workspace(M, N, K):
+    """The workspace for any activation serves the call without one where that call's plans need more than its own."""
+    import torch
+
+    import dense_gemm_preshuffle_amd as gp
+
+    dtype, t = "fp16", torch.float16
+    gen = _gen(M)
+    x, w, dy = _normal(gen, M, K, t=t), _normal(gen, N, K, t=t, scale=K ** -0.5), _normal(gen, M, N, t=t, scale=0.1)
+    say(f"linear backward {dtype} {M}x{N}x{K} none on the workspace of any activation")
+    ws = gp.linear_backward_workspace(dtype, M, N, K)
+    want = gp.gemm_linear_backward(dtype, dy, None, x, w)
+    got = gp.gemm_linear_backward(dtype, dy, None, x, w, workspace=ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    ref = L64.backward64(dtype, dy, None, x, w, "none")
+    F64.within(dtype, got[0], *ref["dx"], "dx")
+    F64.within(dtype, got[1], *ref["dw"], "dw")
+    N64.within32(got[2], *ref["dbias"], "dbias")
+
+
 @pytest.mark.parametrize("act", F64.ACTS)
 def test_gradients_against_differences(act):
     """Each gradient along a direction against central differences of the layer in float64."""

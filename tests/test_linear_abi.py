@@ -65,6 +65,23 @@ def test_backward_sizes():
     assert size(f, FP8, 4, 32, 32, 0, 1, 1, 1)[0] == EDTYPE
 
 
+def test_backward_workspace_of_an_activation_serves_none():
+    """A workspace for any activation holds a call without one, at sizes where the two run on other plans too."""
+    f = "gemm_linear_backward_workspace_size"
+    rng = random.Random(7)
+    cases = [(F16, 3677, 4064, 14304, 1, 1, 1), (F16, 3870, 3808, 9376, 1, 1, 1)]
+    while len(cases) < 12000:
+        M = int(math.exp(rng.uniform(0, math.log(16384))))
+        N, K = (16 * int(math.exp(rng.uniform(0, math.log(1024)))) for _ in range(2))
+        wants = rng.choice(((1, 1, 1), (1, 1, 0), (1, 0, 0), (0, 1, 0), (0, 1, 1), (1, 0, 1), (0, 0, 1)))
+        cases.append((rng.choice((BF16, F16)), M, N, K, *wants))
+    for c in cases:
+        none = size(f, *c[:4], 0, *c[4:])
+        assert none[0] == OK, c
+        of = [size(f, *c[:4], act, *c[4:]) for act in (1, 2, 3)]
+        assert all(s == OK and n >= none[1] for s, n in of) and len(set(of)) == 1, (c, none, of)
+
+
 def test_forward_arguments(lib):
     def call(dtype=BF16, x=P, w=P, bias=P, act=2, res=P, y=P, z=P, M=4, N=32, K=40, ws=None):
         return lib.gemm_linear(dtype, x, w, bias, act, res, y, z, M, N, K, ws, 0, None)
