@@ -142,7 +142,7 @@ def prepare(case, seed):
                 s["w_shuf"] = gp.gemm_linear_preshuffle(s["w"], case["dtype"])
                 s["ws"] = gp.linear_workspace(case["dtype"], M, N, K)
             else:
-                s["ws"] = gp.linear_backward_workspace(case["dtype"], M, N, K)
+                s["ws"] = gp.linear_backward_workspace(case["dtype"], M, N, K, act=case["act"])
         return s
     if case["op"] in ("norm", "norm_backward"):
         M, H, G = case["M"], case["H"], case["groups"]
