@@ -71,11 +71,22 @@ bool is_true(PyObject* o) { return o == Py_True; }
 
 void* data_of(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
-// the tensor that was given, else a new one
-at::Tensor output(Args& p, int i, bool wanted, at::IntArrayRef sizes, const at::TensorOptions& options) {
+// The interpreter's lock, given up for a scope: allocation and launch may wait (for memory,
+// for queue space, for the library's code to be loaded), and other Python threads, or a
+// host callback that the queue itself waits for, need the lock meanwhile. No Python object,
+// and no tensor that has one, is touched in the scope; what it yields is wrapped after it.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// the tensor that was given, else none yet
+at::Tensor given(Args& p, int i) {
   const at::Tensor* t = p.tensor(i);
-  if (t) return *t;
-  return wanted ? at::empty(sizes, options) : at::Tensor();
+  return t ? *t : at::Tensor();
+}
+void make(at::Tensor& t, bool wanted, at::IntArrayRef sizes, const at::TensorOptions& options) {
+  if (wanted && !t.defined()) t = at::empty(sizes, options);
 }
 
 PyObject* wrap(const at::Tensor& t) {
@@ -113,9 +124,16 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float scale = (float)p.real(3), eps = (float)p.real(11);
     void* stream = (void*)p.num(16);
     if (!p.ok || (a[13] != Py_None && !want_r) || (a[14] != Py_None && !kout)) return none();
-    const at::Tensor r = output(p, 13, want_r, rows, x->options()), y = output(p, 14, kout != 0, rows, x->options());
-    if (p_norm(dt, xd, res, scale, kin, w_in, b_in, g, gates, kout, w_out, b_out, eps, data_of(r), data_of(y), M, H, stream))
-      return none();
+    const at::TensorOptions half = x->options();
+    at::Tensor r = given(p, 13), y = given(p, 14);
+    int status;
+    {
+      Unlocked scope;
+      make(r, want_r, rows, half);
+      make(y, kout != 0, rows, half);
+      status = p_norm(dt, xd, res, scale, kin, w_in, b_in, g, gates, kout, w_out, b_out, eps, data_of(r), data_of(y), M, H, stream);
+    }
+    if (status) return none();
     return Py_BuildValue("NN", wrap(r), wrap(y));
   } catch (...) {
     return none();
@@ -147,25 +165,31 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float scale = (float)p.real(5), eps = (float)p.real(13);
     void* stream = (void*)p.num(21);
     if (!p.ok || (a[17] != Py_None && !want_dx) || (a[18] != Py_None && !want_dres)) return none();
-    const at::TensorOptions f32 = first->options().dtype(at::kFloat);
-    const at::Tensor dx = output(p, 17, want_dx, rows, first->options()), dres = output(p, 18, want_dres, rows, first->options());
-    auto grad = [&](const void* of, at::IntArrayRef sizes) { return params && of ? at::empty(sizes, f32) : at::Tensor(); };
-    const at::Tensor dw_in = grad(w_in, vec), db_in = grad(b_in, vec), dgate = grad(g, gate_sizes), dw_out = grad(w_out, vec),
-                     db_out = grad(b_out, vec);
-    at::Tensor ws;
-    const at::Tensor* given = p.tensor(19);
-    if (!p.ok || (given && (given->device() != p.device || !given->is_contiguous()))) return none();
-    if (given) {
-      ws = *given;
-    } else if (params && (w_in || b_in || g || w_out || b_out)) {
-      size_t bytes = 0;
-      if (p_norm_backward_size(dt, M, H, gates, &bytes)) return none();
-      ws = at::empty({(int64_t)bytes}, first->options().dtype(at::kByte));
+    const at::TensorOptions half = first->options(), f32 = half.dtype(at::kFloat);
+    at::Tensor dx = given(p, 17), dres = given(p, 18), ws = given(p, 19), dw_in, db_in, dgate, dw_out, db_out;
+    if (!p.ok || (ws.defined() && (ws.device() != p.device || !ws.is_contiguous()))) return none();
+    int status = GP_OK;
+    {
+      Unlocked scope;
+      make(dx, want_dx, rows, half);
+      make(dres, want_dres, rows, half);
+      make(dw_in, params && w_in, vec, f32);
+      make(db_in, params && b_in, vec, f32);
+      make(dgate, params && g, gate_sizes, f32);
+      make(dw_out, params && w_out, vec, f32);
+      make(db_out, params && b_out, vec, f32);
+      if (!ws.defined() && params && (w_in || b_in || g || w_out || b_out)) {
+        size_t bytes = 0;
+        status = p_norm_backward_size(dt, M, H, gates, &bytes);
+        if (!status) ws = at::empty({(int64_t)bytes}, half.dtype(at::kByte));
+      }
+      if (!status)
+        status = p_norm_backward(dt, dyd, drd, xd, rd, scale, kin, w_in, b_in, g, gates, kout, w_out, eps, data_of(dx),
+                                 data_of(dres), (float*)data_of(dw_in), (float*)data_of(db_in), (float*)data_of(dgate),
+                                 (float*)data_of(dw_out), (float*)data_of(db_out), M, H, data_of(ws),
+                                 ws.defined() ? ws.nbytes() : 0, stream);
     }
-    if (p_norm_backward(dt, dyd, drd, xd, rd, scale, kin, w_in, b_in, g, gates, kout, w_out, eps, data_of(dx), data_of(dres),
-                        (float*)data_of(dw_in), (float*)data_of(db_in), (float*)data_of(dgate), (float*)data_of(dw_out),
-                        (float*)data_of(db_out), M, H, data_of(ws), ws.defined() ? ws.nbytes() : 0, stream))
-      return none();
+    if (status) return none();
     return Py_BuildValue("NNNNNNN", wrap(dx), wrap(dres), wrap(dw_in), wrap(db_in), wrap(dgate), wrap(dw_out), wrap(db_out));
   } catch (...) {
     return none();
@@ -191,14 +215,25 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool save = is_true(a[6]);
     void* stream = (void*)p.num(11);
     if (!p.ok || (a[8] != Py_None && !save)) return none();
-    const at::Tensor* ws = p.tensor(9);
-    if (!p.ok || (ws && (ws->device() != p.device || !ws->is_contiguous()))) return none();
-    size_t need = 0;   // (without a workspace a call that needs one makes it in Python)
-    if (!ws && (p_linear_size(dt, M, N, K, &need) || need)) return none();
-    const at::Tensor y = output(p, 7, true, rows, x->options()), z = output(p, 8, save, rows, x->options());
-    if (p_linear(dt, xd, wd, bias, act, res, data_of(y), data_of(z), M, N, K, ws ? ws->data_ptr() : nullptr,
-                 ws ? ws->nbytes() : 0, stream))
-      return none();
+    const at::Tensor ws = given(p, 9);
+    if (!p.ok || (ws.defined() && (ws.device() != p.device || !ws.is_contiguous()))) return none();
+    const at::TensorOptions half = x->options();
+    at::Tensor y = given(p, 7), z = given(p, 8);
+    int status = GP_OK;
+    {
+      Unlocked scope;
+      size_t need = 0;   // (without a workspace a call that needs one makes it in Python)
+      if (!ws.defined()) status = p_linear_size(dt, M, N, K, &need);
+      if (!status && !need) {
+        make(y, true, rows, half);
+        make(z, save, rows, half);
+        status = p_linear(dt, xd, wd, bias, act, res, data_of(y), data_of(z), M, N, K, data_of(ws),
+                          ws.defined() ? ws.nbytes() : 0, stream);
+      } else {
+        status = GP_EWORKSPACE;
+      }
+    }
+    if (status) return none();
     return save ? Py_BuildValue("NN", wrap(y), wrap(z)) : wrap(y);
   } catch (...) {
     return none();
@@ -225,21 +260,25 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!p.ok || (a[9] != Py_None && !want_dx) || (a[10] != Py_None && !want_dw) || (a[11] != Py_None && !want_db)) return none();
     if ((want_dx && !wd) || (want_dw && !xd) || (act && !zd)) return none();
     const at::TensorOptions half = dy->options();
-    at::Tensor ws;
-    const at::Tensor* given = p.tensor(12);
-    if (!p.ok || (given && (given->device() != p.device || !given->is_contiguous()))) return none();
-    if (given) {
-      ws = *given;
-    } else {
-      size_t bytes = 0;
-      if (p_linear_backward_size(dt, M, N, K, act, want_dx, want_dw, want_db, &bytes)) return none();
-      ws = at::empty({(int64_t)bytes}, half.dtype(at::kByte));
+    at::Tensor dx = given(p, 9), dw = given(p, 10), db = given(p, 11), ws = given(p, 12);
+    if (!p.ok || (ws.defined() && (ws.device() != p.device || !ws.is_contiguous()))) return none();
+    int status = GP_OK;
+    {
+      Unlocked scope;
+      if (!ws.defined()) {
+        size_t bytes = 0;
+        status = p_linear_backward_size(dt, M, N, K, act, want_dx, want_dw, want_db, &bytes);
+        if (!status) ws = at::empty({(int64_t)bytes}, half.dtype(at::kByte));
+      }
+      if (!status) {
+        make(dx, want_dx, xs, half);
+        make(dw, want_dw, ws_, half);
+        make(db, want_db, bs, half.dtype(at::kFloat));
+        status = p_linear_backward(dt, dyd, zd, xd, wd, act, data_of(dx), data_of(dw), (float*)data_of(db), M, N, K,
+                                   data_of(ws), ws.nbytes(), stream);
+      }
     }
-    const at::Tensor dx = output(p, 9, want_dx, xs, half), dw = output(p, 10, want_dw, ws_, half),
-                     db = output(p, 11, want_db, bs, half.dtype(at::kFloat));
-    if (p_linear_backward(dt, dyd, zd, xd, wd, act, data_of(dx), data_of(dw), (float*)data_of(db), M, N, K, data_of(ws),
-                          ws.nbytes(), stream))
-      return none();
+    if (status) return none();
     return Py_BuildValue("NNN", wrap(dx), wrap(dw), wrap(db));
   } catch (...) {
     return none();

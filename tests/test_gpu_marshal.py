@@ -111,3 +111,36 @@ def test_current_stream():
         out = gp.gemm_norm("bf16", y)[1]
     side.synchronize()
     assert torch.equal(out, want)
+
+
+def test_the_interpreter_runs_meanwhile(tmp_path):
+    """The entry points are called without the interpreter's lock, allocation and launch may wait: a copy of the module
+    is bound to CPython's own question whether this thread holds the lock, whose 0 for "no" reads as success."""
+    import ctypes
+    import importlib.machinery
+    import importlib.util
+    import shutil
+
+    import torch
+
+    import dense_gemm_preshuffle_amd as gp
+
+    path = shutil.copy(gp._compiled().__file__, tmp_path / "_marshal.so")
+    loader = importlib.machinery.ExtensionFileLoader("_marshal", str(path))
+    m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+    loader.exec_module(m)
+    held = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    assert ctypes.PyDLL(None).PyGILState_Check() == 1       # (as such a call would answer with the lock)
+    m.bind(*[held] * 7)
+    half, f32 = dict(dtype=torch.bfloat16, device="cuda"), dict(device="cuda")
+    a, v, w = torch.zeros(4, 64, **half), torch.zeros(64, **f32), torch.zeros(32, 64, **half)
+    laid, dy = torch.zeros(2 * 32 * 64, dtype=torch.uint8, device="cuda"), torch.zeros(4, 32, **half)
+    bf16, here = gp.GP_BF16, torch.cuda.current_device()
+    y = m.linear(bf16, a, laid, None, 0, None, False, None, None, None, here, 0)
+    assert y is not None and y.shape == (4, 32)
+    out = m.linear_backward(bf16, dy, None, a, w, 0, True, True, True, None, None, None, None, here, 0)
+    assert [tuple(t.shape) for t in out] == [(4, 64), (32, 64), (32,)]
+    out = m.norm(bf16, a, a, 1.0, 1, v, None, None, 1, v, None, 1e-6, True, None, None, here, 0)
+    assert [tuple(t.shape) for t in out] == [(4, 64)] * 2
+    out = m.norm_backward(bf16, a, a, a, a, 1.0, 1, v, None, None, 1, v, None, 1e-6, True, True, True, None, None, None, here, 0)
+    assert [None if t is None else tuple(t.shape) for t in out] == [(4, 64)] * 2 + [(64,), None, None, (64,), None]
