@@ -241,6 +241,19 @@ def source_hash() -> str:
     return h.hexdigest()
 
 
+def marshal_hash() -> str:
+    """SHA-256 of what the binding's compiled marshalling is built from: its source, the header whose signatures it
+    calls through, and torch's version."""
+    import hashlib
+
+    import torch
+
+    h = hashlib.sha256(torch.__version__.encode())
+    for f in (os.path.join(_PKG, "csrc", "marshal.cpp"), os.path.join(os.path.dirname(_PKG), "include", "gemm_preshuffle.h")):
+        h.update(open(f, "rb").read())
+    return h.hexdigest()
+
+
 def header_functions() -> list:
     """Names of the functions the public header declares."""
     hdr = os.path.join(os.path.dirname(_PKG), "include", "gemm_preshuffle.h")
@@ -765,12 +778,23 @@ def _here(where, name, t, stream):
 @functools.lru_cache(maxsize=None)
 def _compiled():
     """The compiled marshalling (csrc/marshal.cpp) of calls on the current stream, bound to the library; None where
-    it is not built. Its functions do what the Python below them does, in 1 us and not 5, and return None where
+    it is not built, or from other sources than these: against another header it would call the entry points through
+    other signatures. Its functions do what the Python below them does, in 1 us and not 5, and return None where
     anything is not as it should be: the Python then names what."""
     lib = load_library()
     try:
         from . import _marshal
     except ImportError:
+        return None
+    try:
+        same = getattr(_marshal, "sources", None) == marshal_hash()
+    except OSError:    # (no sources beside the binding)
+        same = False
+    if not same:
+        import warnings
+
+        warnings.warn("the compiled marshalling (_marshal.so) was built from other sources than these: calls go through "
+                      "ctypes until it is built again", stacklevel=2)
         return None
     _marshal.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
         "gemm_norm", "gemm_norm_backward", "gemm_norm_backward_workspace_size", "gemm_linear",

@@ -93,10 +93,12 @@ def build_marshal() -> str:
     import torch
     from torch.utils import cpp_extension
 
+    from . import marshal_hash
+
     include = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
     tmp = MARSHAL + ".tmp"
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           *(f"-I{d}" for d in include), os.path.join(CSRC, "marshal.cpp"),
+           f'-DGP_MARSHAL_SOURCES="{marshal_hash()}"', *(f"-I{d}" for d in include), os.path.join(CSRC, "marshal.cpp"),
            "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -314,4 +314,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+// sources: the hash of what it was built from, which the binding compares before it binds
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "sources", GP_MARSHAL_SOURCES)) Py_CLEAR(m);
+  return m;
+}
