@@ -49,6 +49,7 @@ __device__ __forceinline__ void choose_experts(const RouteArgs& p, uint32_t m, u
   double l[NE];
   uint64_t keys[NE];
   double top = -__builtin_inf();
+  bool nan = false;
 #pragma unroll
   for (int j = 0; j < NE; ++j) {
     l[j] = 0.0;
@@ -58,9 +59,15 @@ __device__ __forceinline__ void choose_experts(const RouteArgs& p, uint32_t m, u
     const uint64_t u = __hip_atomic_load((const uint64_t*)p.logits + (size_t)m * p.E + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     l[j] = __builtin_bit_cast(double, u);
     keys[j] = key(l[j]);
+    nan = nan || keys[j] == 1;
     top = fmax(top, l[j]);
   }
-  if (!p.sigmoid) top = wave_reduce64(top, [](double a, double b) GP_INLINE { return fmax(a, b); });
+  // (fmax passes over NaN, but the sum over the experts would not: one makes every softmax
+  // score NaN, also where that sum cancels and the expert is not chosen)
+  if (!p.sigmoid) {
+    top = wave_reduce64(top, [](double a, double b) GP_INLINE { return fmax(a, b); });
+    if (__ballot(nan)) top = __builtin_nan("");
+  }
   // (softmax: the score times the sum over the experts)
   auto score = [&](double v) GP_INLINE { return p.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - top); };
   double sum = 1.0;

@@ -666,7 +666,9 @@ int gemm_moe_preshuffle(int dtype, const void* w13, const void* w2, void* w_shuf
  * gemm_moe_route -- the router: ids int32 [M][k] and gates fp32 [M][k]. Logits and
  * scores are taken in 64 bits, so that the choice depends on the inputs alone. NaN
  * counts as less than any number in the choice (ids are distinct experts always) and
- * stays NaN in the weights.
+ * stays NaN in the weights: in one logit it makes all softmax weights of the token NaN
+ * (without a bias the choice goes by the logits then), sigmoid weights where that
+ * expert is chosen.
  *   bias        device fp32 [E], added to the scores for the choice alone, or NULL.
  *   score       GP_SCORE_*.
  *   workspace   as for gemm_ex_ws (its first 64 KiB zero before the first call and

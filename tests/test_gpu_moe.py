@@ -129,6 +129,35 @@ def test_ties_and_not_finite():
         assert not bool(torch.isfinite(y[2]).any())
 
 
+@pytest.mark.parametrize("M", [1, 5])
+def test_one_expert_not_finite(M):
+    """NaN in one expert's router row: softmax weights have it through the sum over the experts, whichever are chosen;
+    sigmoid weights only where that expert is."""
+    import torch
+
+    import dense_gemm_preshuffle_amd as gp
+
+    E, k, H, F = 70, 5, 96, 48
+    x, router, _, _, _, bias = _layer("bf16", M, E, k, H, F, 9)
+    for bad in (3, 69):
+        wr = router.clone()
+        wr[bad, 7] = float("nan")
+        for normalize in (True, False):
+            for b in (None, bias):
+                say(f"moe router NaN in expert {bad}, normalize {normalize}, bias {b is not None}")
+                ids, gates = gp.gemm_moe_route("bf16", x, wr, k, bias=b, normalize=normalize)
+                assert bool(torch.isnan(gates).all())
+                assert all(len(set(row)) == k and all(0 <= i < E for i in row) for row in ids.tolist())
+                assert b is not None or not bool((ids == bad).any())
+                ids, gates = gp.gemm_moe_route("bf16", x, wr, k, bias=b, score="sigmoid", normalize=normalize)
+                assert not bool((ids == bad).any()) and bool(torch.isfinite(gates).all())
+                # (all experts: that one is chosen last)
+                ids, gates = gp.gemm_moe_route("bf16", x, wr[64:].contiguous(), 6, score="sigmoid", normalize=normalize)
+                if bad == 69:
+                    assert bool((ids[:, 5] == 5).all()) and bool(torch.isnan(gates[:, 5]).all())
+                    assert bool(torch.isnan(gates[:, :5]).all()) if normalize else bool(torch.isfinite(gates[:, :5]).all())
+
+
 def test_streams_graph_and_one_workspace():
     """A side stream, a captured and replayed layer, one workspace through layers of different sizes."""
     import torch
