@@ -975,6 +975,8 @@ def _norm_args(where, t, shape, index, dev, w_in, b_in, w_out, b_out, gate, **ro
     gates = gate.shape[0]
     if not _is(gate, f32, (gates, shape[1]), index):
         _want(f"{where}: gate", gate, (gates, shape[1]), f32, dev)
+    if not gates:    # (its data pointer is null, which would read as no gate)
+        raise ValueError(f"{where}: a gate without rows")
     return gates
 
 

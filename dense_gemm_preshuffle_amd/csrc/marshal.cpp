@@ -113,6 +113,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::IntArrayRef rows = x->sizes(), vec = rows.slice(1);
     const at::Tensor* gate = p.tensor(7);
     const int64_t gates = gate && gate->dim() == 2 ? gate->size(0) : 0;
+    if (gate && !gates) return none();
     const int64_t gate_rows[2] = {gates, H};
     const bool want_r = is_true(a[12]);
     void *xd = p.data(1, p.half, rows), *res = p.data(2, p.half, rows);
@@ -153,6 +154,7 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::IntArrayRef rows = first->sizes(), vec = rows.slice(1);
     const at::Tensor* gate = p.tensor(9);
     const int64_t gates = gate && gate->dim() == 2 ? gate->size(0) : 0;
+    if (gate && !gates) return none();
     const int64_t gate_rows[2] = {gates, H};
     const at::IntArrayRef gate_sizes(gate_rows, 2);
     void *dyd = p.data(1, p.half, rows), *drd = p.data(2, p.half, rows), *xd = p.data(3, p.half, rows), *rd = p.data(4, p.half, rows);

@@ -230,3 +230,19 @@ def test_another_device_is_refused(monkeypatch):
         gp.gemm_norm("bf16", x)
     with pytest.raises(ValueError, match="current device"):
         gp.gemm_norm_backward("bf16", x, None, x, x)
+
+
+@pytest.mark.parametrize("compiled", [True, False])
+def test_a_gate_without_rows_is_refused(monkeypatch, compiled):
+    """Zero rows of a gate divide no M: an error, not a call without a gate."""
+    import torch
+
+    import dense_gemm_preshuffle_amd as gp
+
+    if not compiled:
+        monkeypatch.setattr(gp, "_compiled", lambda: None)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    gate = torch.empty(0, 64, device="cuda")
+    for call in (lambda: gp.gemm_norm("bf16", x, gate=gate), lambda: gp.gemm_norm_backward("bf16", x, x, x, x, gate=gate)):
+        with pytest.raises(ValueError, match="gate"):
+            call()
