@@ -1190,8 +1190,8 @@ def gemm_moe_experts(dtype, x, weights: MoeWeights, ids, gates, act="silu", resi
 
 def gemm_moe(dtype, x, router, weights: MoeWeights, k: int, bias=None, score="softmax", normalize=True, scale=1.0,
              act="silu", residual=None, y=None, ids=None, gates=None, workspace=None, stream=None):
-    """(y, ids, gates): gemm_moe_route, then gemm_moe_experts on what it chose. Without a workspace (moe_workspace)
-    one is made for the call."""
+    """(y, ids, gates): gemm_moe_route, then gemm_moe_experts on what it chose. Up to 256 tokens, 32 experts each and 4096
+    pairs of them. Without a workspace (moe_workspace) one is made for the call."""
     where = "gemm_moe"
     dt, t = _half(dtype)
     _here(where, "x", x, stream)

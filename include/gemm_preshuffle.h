@@ -649,9 +649,10 @@ int gemm_norm_backward_workspace_size(int dtype, int64_t M, int64_t H, int64_t g
  *
  * for generated tokens: bound by reading the chosen experts' weights, once each. x, y
  * and residual are [M][H], the router Wr [E][H], of one type (GP_BF16 or GP_F16,
- * else GP_EDTYPE). F % 16 == 0, H % 32 == 0, M <= 256, k <= 32 and <= E, E <= 512, an
- * expert's matrix below 2^31 bytes (else GP_ESHAPE); the experts' weights together of
- * any size.
+ * else GP_EDTYPE). F % 16 == 0, H % 32 == 0, M <= 256, k <= 32 and <= E, M k <= 4096 (k
+ * above 16 for fewer tokens), E <= 512, H <= 258048, each of an expert's matrices (K filled up
+ * to a multiple of 64), M k rows of 4 H bytes and of 2 F bytes below 2^31 bytes, min(M k, E)
+ * max(F, H / 2) below 2^26 (else GP_ESHAPE); the experts' weights together of any size.
  *
  * gemm_moe_weights_size -- host-only: bytes of the laid-out weights.
  * gemm_moe_preshuffle -- w13 [E][2F][H] (an expert's F gate rows, then its F up

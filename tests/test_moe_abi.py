@@ -52,6 +52,25 @@ def test_workspace_size():
         assert size(*bad) == ESHAPE, bad
 
 
+@pytest.mark.parametrize("inside,outside", [
+    # (M, F, H, E, k): the last size on each side of a limit of the header
+    ((256, 16, 32, 4, 1), (257, 16, 32, 4, 1)), ((128, 16, 32, 32, 32), (129, 16, 32, 32, 32)),
+    ((256, 16, 32, 64, 16), (256, 16, 32, 64, 17)), ((4, 16, 32, 64, 32), (4, 16, 32, 64, 33)),
+    ((4, 16, 32, 3, 3), (4, 16, 32, 3, 4)), ((4, 16, 32, 512, 1), (4, 16, 32, 513, 1)),
+    ((1, 16, 258048, 4, 1), (1, 16, 258080, 4, 1)),
+    ((256, 16, 131072 - 32, 64, 16), (256, 16, 131072, 64, 16)),                      # M k rows of 4 H bytes
+    ((256, 2 ** 18 - 16, 32, 64, 16), (256, 2 ** 18, 32, 64, 16)),                    # and of 2 F
+    ((1, 2 ** 23 - 16, 64, 4, 1), (1, 2 ** 23, 64, 4, 1)),                            # an expert's matrix
+    ((64, 2 ** 17 - 16, 32, 512, 8), (64, 2 ** 17, 32, 512, 8)),                      # min(M k, E) F
+    ((64, 16, 258048, 512, 1), (64, 16, 258080, 512, 1))])
+def test_documented_limits(inside, outside):
+    lib, n = gp.load_library(), ctypes.c_size_t()
+
+    def size(M, F, H, E, k):
+        return lib.gemm_moe_workspace_size(BF16, M, F, H, E, k, ctypes.byref(n))
+    assert size(*inside) == OK and size(*outside) == ESHAPE
+
+
 def test_arguments(lib):
     def route(dtype=BF16, x=P, wr=P, bias=P, score=0, ids=P, gates=P, M=2, H=48, E=8, k=2, ws=P, n=1 << 30):
         return lib.gemm_moe_route(dtype, x, wr, bias, score, 1, 1.0, ids, gates, M, H, E, k, ws, n, None)
