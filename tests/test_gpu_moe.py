@@ -158,6 +158,39 @@ def test_one_expert_not_finite(M):
                     assert bool(torch.isnan(gates[:, :5]).all()) if normalize else bool(torch.isfinite(gates[:, :5]).all())
 
 
+def test_weights_beyond_4_gib():
+    """Experts whose weights lie more than 2^32 bytes into the given and the laid-out ones, in both matrices: against
+    float64, and one token against the same experts laid out alone."""
+    import torch
+
+    import dense_gemm_preshuffle_amd as gp
+
+    E, F, H, k, gen = 300, 2048, 4096, 2, _gen(12)
+    used = [0, 43, 171, 299]     # (171 and 43 lie 2^32 bytes before 299 in the one and the other matrix)
+    w13 = torch.zeros(E, 2 * F, H, dtype=torch.bfloat16, device="cuda")
+    w2 = torch.zeros(E, H, F, dtype=torch.bfloat16, device="cuda")
+    for e in used:
+        w13[e].normal_(0.0, H ** -0.5, generator=gen)
+        w2[e].normal_(0.0, F ** -0.5, generator=gen)
+    assert 299 * w13[0].nbytes > 2 ** 32 and 299 * w2[0].nbytes > 2 ** 32
+    weights = gp.gemm_moe_preshuffle(w13, w2, "bf16")
+    few13, few2 = w13[used].contiguous(), w2[used].contiguous()
+    del w13, w2
+    few = gp.gemm_moe_preshuffle(few13, few2, "bf16")
+    for M in (1, 5, 40):
+        x = torch.randn(M, H, generator=gen, device="cuda").bfloat16()
+        gates = torch.rand(M, k, generator=gen, device="cuda") + 0.1
+        at = torch.randint(0, len(used), (M, k), generator=gen, device="cuda")
+        at[0, 0] = 3
+        ids = torch.tensor(used, device="cuda")[at].int()
+        say(f"moe beyond 4 GiB: {M} tokens")
+        y = gp.gemm_moe_experts("bf16", x, weights, ids, gates)
+        torch.cuda.synchronize()
+        F64.within("bf16", y, *M64.experts64("bf16", x, few13, few2, at.int(), gates, "silu", None), "y")
+        if M == 1:
+            assert torch.equal(y, gp.gemm_moe_experts("bf16", x, few, at.int(), gates))
+
+
 def test_streams_graph_and_one_workspace():
     """A side stream, a captured and replayed layer, one workspace through layers of different sizes."""
     import torch
