@@ -14,7 +14,8 @@
 // layout: read from memory in that layout each lane touches another line. What
 // lies past K or the wave's share is loaded as zeros (an offset outside the
 // buffer resource), which add nothing. Linear, measured: one row, 4096 x 4096, 6.7 us a call
-// (33.6 MB, 5.0 TB/s); 37 rows, 4096 x 14336, 27.4 (119 MB, 4.3 TB/s).
+// (33.6 MB, 5.0 TB/s); 37 rows, 4096 x 14336, 27.4 (119 MB at the least, 4.3 TB/s; 132 cross the
+// L2 fabric: x into every XCD's L2, and the sums of four K ranges out and back).
 #pragma once
 
 #include "gp_common.hpp"

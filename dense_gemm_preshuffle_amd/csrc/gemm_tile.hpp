@@ -1047,7 +1047,7 @@ __device__ __forceinline__ void gemm_tile_body(const TileArgs& p, uint32_t w, ch
     // the epilogue. An edge tile's rows and columns that belong to its neighbour are
     // read (in place they may change meanwhile), added up and not stored. Bound by the
     // matrix units at the clock that the power limit leaves: 8192 x 4096 x 14336 with bias
-    // and residual 675 us a call, 1.43 PFLOP/s.
+    // and residual 680 us a call, 1.42 PFLOP/s.
     constexpr int CH_ROW = TN * C::OB / 16, PASSES = TM * CH_ROW / C::THREADS;
     static_assert(EPI != EPI_LINEAR || TM * CH_ROW % C::THREADS == 0, "whole passes");
     const size_t base = ((size_t)m0 * p.N + n0) * C::OB;
