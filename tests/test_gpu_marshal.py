@@ -144,3 +144,43 @@ def test_the_interpreter_runs_meanwhile(tmp_path):
     assert [tuple(t.shape) for t in out] == [(4, 64)] * 2
     out = m.norm_backward(bf16, a, a, a, a, 1.0, 1, v, None, None, 1, v, None, 1e-6, True, True, True, None, None, None, here, 0)
     assert [None if t is None else tuple(t.shape) for t in out] == [(4, 64)] * 2 + [(64,), None, None, (64,), None]
+
+
+def test_calls_from_several_threads():
+    """Each thread on a stream of its own, all at once: every call of a thread gives the bits of its first."""
+    import threading
+
+    import torch
+
+    import dense_gemm_preshuffle_amd as gp
+
+    wrong = []
+
+    def work(k):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                gen = torch.Generator(device="cuda")
+                gen.manual_seed(k)
+                half = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()
+                x, w, dy, z, a = half(40 + k, 512), half(336, 512), half(40 + k, 336), half(40 + k, 336), half(60, 1024)
+                w_shuf, w_out = gp.gemm_linear_preshuffle(w, "bf16"), torch.ones(1024, device="cuda")
+
+                def step():
+                    out = [gp.gemm_linear("bf16", x, w_shuf, act="silu")]
+                    out += gp.gemm_linear_backward("bf16", dy, z, x, w, act="gelu")
+                    out += gp.gemm_norm("bf16", a, w_out=w_out)
+                    return out + [v for v in gp.gemm_norm_backward("bf16", a, a, a, a, w_out=w_out) if v is not None]
+                first = [v.clone() for v in step()]
+                for i in range(100):
+                    if not all(torch.equal(p, q) for p, q in zip(step(), first)):
+                        wrong.append((k, i))
+                stream.synchronize()
+        except Exception as e:
+            wrong.append((k, repr(e)))
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:5]

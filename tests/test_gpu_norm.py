@@ -246,3 +246,55 @@ def test_a_gate_without_rows_is_refused(monkeypatch, compiled):
     for call in (lambda: gp.gemm_norm("bf16", x, gate=gate), lambda: gp.gemm_norm_backward("bf16", x, x, x, x, gate=gate)):
         with pytest.raises(ValueError, match="gate"):
             call()
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_every_subset_of_the_gradients(seed):
+    """Any of the backward pass's outputs may be missing, and x where none of the rest needs it: the same bits as of all
+    of them together, which are within their bounds."""
+    import random
+
+    import torch
+
+    import dense_gemm_preshuffle_amd as gp
+
+    rng, gen = random.Random(seed), torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    G = rng.choice([0, 0, 1, rng.randint(2, 256)])
+    M = max(G, 1) * rng.randint(1, max(1, 600 // max(G, 1)))
+    H = 8 * rng.choice([rng.randint(1, 64), rng.randint(65, 256), rng.randint(257, 1024), rng.randint(1025, 2048)])
+    M = M if M * H <= 1 << 22 else max(G, 1)
+    kin, kout = rng.choice(["none", "rms", "layer"]), rng.choice(["none", "rms", "layer"])
+    dtype = rng.choice(F64.TYPES)
+    dt, t = gp.DTYPES[dtype], F64.torch_type(dtype)
+    x, r, dy, dr = (torch.randn(M, H, generator=gen, device="cuda").to(t) for _ in range(4))
+    w_in, b_in, w_out, b_out = (torch.randn(H, generator=gen, device="cuda") if kind != "none" and rng.random() < 0.7 else None
+                                for kind in (kin, kin, kout, kout))
+    gate = torch.randn(G, H, generator=gen, device="cuda") if G else None
+    dy, r = (dy, r) if kout != "none" else (None, None)
+    dr = None if dy is not None and rng.random() < 0.3 else dr
+    possible = [True, True, kin != "none", kin != "none", G > 0, kout != "none", kout != "none"]
+    say(f"seed {seed}: norm backward {dtype} {M}x{H} gates {G} {kin} -> {kout}")
+    size = gp.gemm_norm_backward_workspace_size(dtype, M, H, G)
+
+    def call(want):
+        shapes = [(M, H)] * 2 + [(H,), (H,), (G, H), (H,), (H,)]
+        out = [torch.full(s, float("nan"), dtype=t if i < 2 else torch.float32, device="cuda") if want[i] else None
+               for i, s in enumerate(shapes)]
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        use_x = (kin != "none" and (want[0] or want[2])) or want[4]
+        gp._check(gp.load_library().gemm_norm_backward(
+            dt, gp._ptr(dy), gp._ptr(dr), gp._ptr(x) if use_x else None, gp._ptr(r), 0.7, gp.NORMS[kin], gp._ptr(w_in), gp._ptr(b_in),
+            gp._ptr(gate), G, gp.NORMS[kout], gp._ptr(w_out), 1e-5, *map(gp._ptr, out), M, H, gp._ptr(ws) if any(want[2:]) else None,
+            size, gp._stream(None)), "gemm_norm_backward")
+        return out
+    whole = call(possible)
+    ref = N64.backward64(dy, dr, x, r, 0.7, kin, w_in, b_in, gate, kout, w_out, b_out, 1e-5)
+    for name, v in zip(gp.NormGrads._fields, whole):
+        if v is not None:
+            (N64.within32(v, *ref[name], name) if v.dtype == torch.float32 else F64.within(dtype, v, *ref[name], name))
+    wants = [[i == j for j in range(7)] for i in range(7) if possible[i]]
+    wants += [[p and rng.random() < 0.5 for p in possible] for _ in range(6)]
+    for want in wants:
+        if any(want):
+            assert all(a is None or torch.equal(a, b) for a, b in zip(call(want), whole)), want
